@@ -382,6 +382,55 @@ moe_status moe_reap_keep_bias(const double* saliency, int32_t num_experts, int32
 moe_status moe_linear_bf16(const void* in, const void* W, int64_t num_tokens, int32_t n_in,
                            int32_t n_out, void* out, moe_stream_t stream);
 
+/* ---- low-rank adapters of many requests beside the shared projections ---- */
+
+/* A stack of adapters for one projection [n_out][n_in], and which of them each token of the
+ * call uses.  Adapter i adds scale[i] B_i A_i to the projection's matrix for the tokens that
+ * name it; no matrix is ever merged, so one copy of the weights serves all requests.
+ *  - Ranks of rank[i] and more are never used, whatever a and b hold there: adapters of
+ *    different ranks share one stack.  rank NULL: every adapter has max_rank.  A value
+ *    outside 0..max_rank counts as the nearer end.
+ *  - A token whose id lies outside [0, num_adapters) (-1, say) has no adapter: its row is
+ *    the projection alone.
+ *  - Rows do not mix: an infinity or NaN in one adapter reaches only its own tokens. */
+typedef struct {
+  const void* a;          /* bf16 [num_adapters][max_rank][n_in], 16-byte aligned */
+  const void* b;          /* bf16 [num_adapters][n_out][max_rank], 16-byte aligned */
+  const float* scale;     /* fp32 [num_adapters] */
+  const int32_t* rank;    /* nullable [num_adapters] */
+  const int32_t* adapter; /* [num_tokens] ids */
+  int32_t num_adapters;   /* 1..1024 */
+  int32_t max_rank;       /* a multiple of 8, 8..128 */
+} moe_lora;
+
+/* Workspace bytes of moe_linear_lora (host function; reads num_adapters and max_rank of
+ * lora only, so its pointers may be NULL here). */
+moe_status moe_linear_lora_workspace_size(int64_t num_tokens, int32_t n_in, const moe_lora* lora, size_t* bytes);
+
+/* The projection of moe_linear_bf16 with an adapter per token:
+ *   u[t][r]   = sum_i a[id_t][r][i] in[t][i]                                   (fp32)
+ *   out[t][o] = bf16(sum_i in[t][i] W[o][i] + scale[id_t] sum_r b[id_t][o][r] u[t][r])
+ * with one rounding, of the whole sum (on the matrix cores scale u enters the second
+ * product with 16 significant bits).  n_in a multiple of 32, at most 8192; any n_out;
+ * num_tokens up to 2^24.  in, out and workspace must not overlap; workspace 16-byte
+ * aligned, of at least moe_linear_lora_workspace_size bytes, needing no clearing. */
+moe_status moe_linear_lora(const void* in, const void* W, const moe_lora* lora, int64_t num_tokens, int32_t n_in,
+                           int32_t n_out, void* out, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* moe_layer_forward / moe_layer_forward_shared with adapters on the latent projections:
+ *   h = bf16(x W_d^T + adapter(lora_down)), out = bf16(z W_u^T + adapter(lora_up) [+ shared]).
+ * The router sees x alone: an adapter changes no token's experts.  Either may be NULL;
+ * shared_blob is NULL when cfg->num_shared is 0.  Workspace:
+ * moe_layer_lora_workspace_size bytes.  Other arguments as moe_layer_forward_shared. */
+moe_status moe_layer_lora_workspace_size(const moe_config* cfg, int32_t k, const moe_lora* lora_down,
+                                         const moe_lora* lora_up, size_t* bytes);
+moe_status moe_layer_forward_lora(const void* x, const void* router_w, const void* latent_down,
+                                  const void* latent_up, const uint8_t* expert_blob, int32_t k,
+                                  const moe_config* cfg, const float* router_bias, const uint8_t* shared_blob,
+                                  const moe_lora* lora_down, const moe_lora* lora_up, void* out,
+                                  moe_routing_out* routing, void* workspace, size_t workspace_bytes,
+                                  moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

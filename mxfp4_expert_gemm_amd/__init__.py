@@ -12,7 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -31,7 +31,8 @@ EXPORTS = ["moe_expert_bytes", "moe_packed_expert_bytes", "moe_pack_experts", "m
            "moe_dequant_mxfp4", "moe_route", "moe_topk", "moe_permute", "moe_expert_ffn", "moe_combine",
            "moe_linear_bf16", "moe_reap_saliency", "moe_layer_forward_shared", "moe_expert_slots_bytes",
            "moe_layer_forward_streamed", "moe_layer_forward_noalloc", "moe_reap_keep_bias",
-           "moe_permute_workspace_size"]
+           "moe_permute_workspace_size", "moe_linear_lora_workspace_size", "moe_linear_lora",
+           "moe_layer_lora_workspace_size", "moe_layer_forward_lora"]
 
 
 class MoEError(RuntimeError):
@@ -69,6 +70,24 @@ class RoutingOut(ctypes.Structure):
                 ("saliency", ctypes.c_void_p)]
 
 
+class LoraArg(ctypes.Structure):
+    """moe_lora."""
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("rank", ctypes.c_void_p), ("adapter", ctypes.c_void_p), ("num_adapters", ctypes.c_int32),
+                ("max_rank", ctypes.c_int32)]
+
+
+class Lora(NamedTuple):
+    """Adapters of one projection [n_out, n_in] and the adapter of each token: a bf16
+    [N, R, n_in], b bf16 [N, n_out, R], scale fp32 [N], adapter int32 [T] (-1: none), rank
+    int32 [N] (ranks in use; None: all R).  R a multiple of 8, at most 128; N at most 1024."""
+    a: torch.Tensor
+    b: torch.Tensor
+    scale: torch.Tensor
+    adapter: torch.Tensor
+    rank: Optional[torch.Tensor] = None
+
+
 _lib = None
 
 
@@ -81,6 +100,7 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         cfgp, rp = ctypes.POINTER(MoEConfig), ctypes.POINTER(RoutingOut)
+        lp = ctypes.POINTER(LoraArg)
         sig = {
             "moe_expert_bytes": (sz, [i32, i32]),
             "moe_packed_expert_bytes": (sz, [i32, i32]),
@@ -105,6 +125,11 @@ def lib():
             "moe_layer_forward_noalloc": (ctypes.c_int, [vp, vp, vp, vp, vp, i32, cfgp, vp, vp, rp, vp]),
             "moe_layer_forward_streamed": (ctypes.c_int, [vp, vp, vp, vp, vp, i32, cfgp, vp, vp, sz, vp, rp, vp, sz,
                                                           vp]),
+            "moe_linear_lora_workspace_size": (ctypes.c_int, [i64, i32, lp, ctypes.POINTER(sz)]),
+            "moe_linear_lora": (ctypes.c_int, [vp, vp, lp, i64, i32, i32, vp, vp, sz, vp]),
+            "moe_layer_lora_workspace_size": (ctypes.c_int, [cfgp, i32, lp, lp, ctypes.POINTER(sz)]),
+            "moe_layer_forward_lora": (ctypes.c_int, [vp, vp, vp, vp, vp, i32, cfgp, vp, vp, lp, lp, vp, rp, vp, sz,
+                                                      vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -177,14 +202,77 @@ def _routing(r: Optional[dict]) -> Optional[RoutingOut]:
                                               "perm", "saliency")])
 
 
+def _lora(lo: Lora, T: int, n_in: int, n_out: int, device) -> LoraArg:
+    """The adapters as the library takes them, their shapes, types and device checked."""
+    if lo.a.dim() != 3 or lo.a.shape[2] != n_in or lo.a.element_size() != 2:
+        raise ValueError(f"a must be a bf16 [N, R, {n_in}] tensor")
+    N, R = lo.a.shape[:2]
+    if tuple(lo.b.shape) != (N, n_out, R) or lo.b.element_size() != 2:
+        raise ValueError(f"b must be a bf16 [{N}, {n_out}, {R}] tensor")
+    for name, t, shape, dtype in (("scale", lo.scale, (N,), torch.float32), ("adapter", lo.adapter, (T,), torch.int32),
+                                  ("rank", lo.rank, (N,), torch.int32)):
+        if t is not None and (tuple(t.shape) != shape or t.dtype != dtype):
+            raise ValueError(f"{name} must be a {dtype} tensor of shape {shape}")
+    if any(t is not None and t.device != device for t in lo):
+        raise ValueError("the adapters must live on the device of the input")
+    return LoraArg(_p(lo.a), _p(lo.b), _p(lo.scale), _p(lo.rank), _p(lo.adapter), N, R)
+
+
+def _same_device(x: torch.Tensor, *others):
+    """A call's tensors live on one device, and it runs on that one: the current device is
+    the one whose stream the library is handed."""
+    if x.device.index != torch.cuda.current_device() or any(t is not None and t.device != x.device for t in others):
+        raise ValueError("the tensors must live on the current CUDA device")
+
+
+def linear_lora_workspace_size(num_tokens: int, n_in: int, num_adapters: int, max_rank: int) -> int:
+    n = ctypes.c_size_t(0)
+    a = LoraArg(None, None, None, None, None, num_adapters, max_rank)
+    _check(lib().moe_linear_lora_workspace_size(num_tokens, n_in, ctypes.byref(a), ctypes.byref(n)),
+           "moe_linear_lora_workspace_size")
+    return int(n.value)
+
+
+def linear_lora(inp: torch.Tensor, W: torch.Tensor, lora: Lora, *, out: Optional[torch.Tensor] = None,
+                workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """linear_bf16 with a low-rank adapter per token beside it (moe_linear_lora):
+    out[t] = bf16(W inp[t] + scale b (a inp[t])) with the adapter that lora.adapter[t] names."""
+    T, n_in = inp.shape
+    n_out = W.shape[0]
+    if tuple(W.shape) != (n_out, n_in) or W.element_size() != 2 or inp.element_size() != 2:
+        raise ValueError(f"inp and W must be bf16, W [n_out, {n_in}]")
+    _same_device(inp, W, out, workspace)
+    arg = _lora(lora, T, n_in, n_out, inp.device)
+    if out is None:
+        out = torch.empty((T, n_out), dtype=inp.dtype, device=inp.device)
+    elif tuple(out.shape) != (T, n_out) or out.element_size() != 2:
+        raise ValueError(f"out must be a 2-byte [{T}, {n_out}] tensor")
+    if workspace is None:
+        workspace = torch.empty(linear_lora_workspace_size(T, n_in, arg.num_adapters, arg.max_rank),
+                                dtype=torch.uint8, device=inp.device)
+    _check(lib().moe_linear_lora(_p(inp), _p(W), ctypes.byref(arg), T, n_in, n_out, _p(out), _p(workspace),
+                                 workspace.numel() * workspace.element_size(), _stream(stream)), "moe_linear_lora")
+    return out
+
+
+def layer_lora_workspace_size(cfg: MoEConfig, k: int, down: Optional[LoraArg], up: Optional[LoraArg]) -> int:
+    n = ctypes.c_size_t(0)
+    ref = lambda a: None if a is None else ctypes.byref(a)
+    _check(lib().moe_layer_lora_workspace_size(ctypes.byref(cfg), k, ref(down), ref(up), ctypes.byref(n)),
+           "moe_layer_lora_workspace_size")
+    return int(n.value)
+
+
 def layer_forward(x, router_w, latent_down, latent_up, expert_blob, k: int, *, d_ffn: int,
                   bias: Optional[torch.Tensor] = None, renormalize: bool = True, act: int = ACT_SILU,
                   out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                   routing: Optional[dict] = None, stream=None, packed: bool = False,
                   act_format: int = ACT_FMT_BF16, shared_blob: Optional[torch.Tensor] = None,
-                  num_shared: int = 0, d_ffn_shared: int = 0) -> torch.Tensor:
+                  num_shared: int = 0, d_ffn_shared: int = 0, lora_down: Optional[Lora] = None,
+                  lora_up: Optional[Lora] = None) -> torch.Tensor:
     """out = layer(x); routing (dict of preallocated tensors) receives the routing if given;
-    shared_blob with num_shared records of width d_ffn_shared adds the shared experts."""
+    shared_blob with num_shared records of width d_ffn_shared adds the shared experts;
+    lora_down / lora_up are the tokens' adapters on the latent projections."""
     T, d = x.shape
     E = router_w.shape[0]
     L = latent_down.shape[0]
@@ -192,6 +280,20 @@ def layer_forward(x, router_w, latent_down, latent_up, expert_blob, k: int, *, d
                       act_format=act_format, num_shared=num_shared, d_ffn_shared=d_ffn_shared)
     if out is None:
         out = torch.empty((T, d), dtype=x.dtype, device=x.device)
+    if lora_down is not None or lora_up is not None:
+        _same_device(x, out, workspace)
+        down = None if lora_down is None else _lora(lora_down, T, d, L, x.device)
+        up = None if lora_up is None else _lora(lora_up, T, L, d, x.device)
+        if workspace is None:
+            workspace = torch.empty(max(layer_lora_workspace_size(cfg, k, down, up), 256), dtype=torch.uint8,
+                                    device=x.device)
+        r = _routing(routing)
+        ref = lambda a: None if a is None else ctypes.byref(a)
+        _check(lib().moe_layer_forward_lora(_p(x), _p(router_w), _p(latent_down), _p(latent_up), _p(expert_blob), k,
+                                            ctypes.byref(cfg), _p(bias), _p(shared_blob) if num_shared > 0 else None,
+                                            ref(down), ref(up), _p(out), ref(r), _p(workspace), workspace.numel(),
+                                            _stream(stream)), "moe_layer_forward_lora")
+        return out
     if workspace is None:
         workspace = alloc_workspace(cfg, k, x.device)
     r = _routing(routing)
@@ -404,4 +506,4 @@ __all__ = ["lib", "MoEConfig", "RoutingOut", "MoEError", "make_config", "expert_
            "alloc_workspace", "layer_forward", "layer_forward_profiled", "StageEvents", "STAGES", "dequant_mxfp4", "route", "topk", "permute", "expert_ffn", "combine",
            "linear_bf16", "reap_saliency", "reap_prune_bias", "ACT_SILU", "ACT_SITU", "ROUTE_EXACT_ALL", "EXPORTS",
            "LIB_PATH", "expert_slots_bytes", "alloc_expert_slots", "layer_forward_streamed", "layer_forward_noalloc",
-           "NOALLOC_SCRATCH_BYTES"]
+           "NOALLOC_SCRATCH_BYTES", "Lora", "linear_lora", "linear_lora_workspace_size", "layer_lora_workspace_size"]

@@ -3,6 +3,7 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "common.h"
@@ -203,7 +204,7 @@ moe_status zero_i32(int32_t* p, int n, hipStream_t st) {
 
 // router logits (fast, with norms) and optionally the latent down projection, in one launch
 moe_status run_router_and_down(const moe_config& c, const void* x, const void* router_w, const void* latent_down,
-                               void* ws, const Layout& l, hipStream_t st) {
+                               void* ws, const Layout& l, hipStream_t st, const LoraSeg* lora = nullptr) {
   DenseSeg segs[2];
   segs[0].W = static_cast<const uint16_t*>(router_w);
   segs[0].rows = c.num_experts;
@@ -221,7 +222,39 @@ moe_status run_router_and_down(const moe_config& c, const void* x, const void* r
     segs[1].xnorm = nullptr;
     nseg = 2;
   }
-  return dev(launch_dense(static_cast<const uint16_t*>(x), c.num_tokens, c.d_model, segs, nseg, st));
+  return dev(launch_dense(static_cast<const uint16_t*>(x), c.num_tokens, c.d_model, segs, nseg, st, lora));
+}
+
+// ---- adapters: their checks, and the first product into the workspace
+moe_status check_lora(const moe_lora* a) {
+  if (a->num_adapters < 1 || a->max_rank < 8 || a->max_rank % 8) return MOE_ERR_INVALID_ARG;
+  if (a->num_adapters > LORA_MAX_ADAPTERS || a->max_rank > LORA_MAX_RANK) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+moe_status check_lora_pointers(const moe_lora* a) {
+  auto aligned4 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; };
+  if (!a->a || !a->b || !a->scale || !a->adapter || !aligned16(a->a) || !aligned16(a->b) || !aligned4(a->scale) ||
+      !aligned4(a->adapter) || !aligned4(a->rank))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+size_t lora_bytes(const moe_lora* a, int64_t T, int32_t n_in) {
+  return a ? lora_ws_bytes(T, n_in, a->num_adapters, a->max_rank) : 0;
+}
+moe_status run_lora(const moe_lora* a, const void* x, int64_t T, int32_t n_in, void* ws, LoraSeg* seg,
+                    hipStream_t st) {
+  LoraArgs p;
+  p.x = static_cast<const uint16_t*>(x);
+  p.A = static_cast<const uint16_t*>(a->a);
+  p.B = static_cast<const uint16_t*>(a->b);
+  p.scale = a->scale;
+  p.rank = a->rank;
+  p.adapter = a->adapter;
+  p.T = T;
+  p.K = n_in;
+  p.N = a->num_adapters;
+  p.R = a->max_rank;
+  return dev(launch_lora_shrink(p, ws, seg, st));
 }
 
 RouteArgs route_args(const moe_config& c, int k, int flags, const void* x, const void* router_w, const float* bias,
@@ -460,9 +493,12 @@ static moe_status forward_impl(const void* x, const void* router_w, const void* 
                                const uint8_t* expert_blob, int32_t k, const moe_config* cfg, const float* router_bias,
                                const uint8_t* shared_blob, void* out, moe_routing_out* routing, void* workspace,
                                size_t workspace_bytes, const moe_stage_events* ev, moe_stream_t stream,
-                               uint8_t* expert_slots = nullptr, size_t slots_bytes = 0) {
+                               uint8_t* expert_slots = nullptr, size_t slots_bytes = 0,
+                               const moe_lora* lora_down = nullptr, const moe_lora* lora_up = nullptr) {
   MOE_TRY(check_config(cfg, k));
   const moe_config& c = *cfg;
+  if (lora_down) MOE_TRY(check_lora(lora_down));
+  if (lora_up) MOE_TRY(check_lora(lora_up));
   if (c.num_shared > 0 && (!shared_blob || !aligned16(shared_blob))) return MOE_ERR_INVALID_ARG;
   if (c.num_tokens == 0) return MOE_OK;  // nothing to do; pointers may be NULL
   if (!x || !router_w || !latent_down || !latent_up || !expert_blob || !out) return MOE_ERR_INVALID_ARG;
@@ -480,10 +516,15 @@ static moe_status forward_impl(const void* x, const void* router_w, const void* 
   }
   const size_t xbytes = (size_t)c.num_tokens * c.d_model * 2;
   if (overlap(x, xbytes, out, xbytes)) return MOE_ERR_INVALID_ARG;
+  if (lora_down) MOE_TRY(check_lora_pointers(lora_down));
+  if (lora_up) MOE_TRY(check_lora_pointers(lora_up));
   const Layout l = layout(c, k);
-  if (!workspace || workspace_bytes < l.total) return MOE_ERR_WORKSPACE;
+  // the two projections' adapters use one scratch behind the layer's, one after the other
+  const size_t need = l.total + std::max(lora_bytes(lora_down, c.num_tokens, c.d_model),
+                                         lora_bytes(lora_up, c.num_tokens, c.d_latent));
+  if (!workspace || workspace_bytes < need) return MOE_ERR_WORKSPACE;
   if (!aligned16(workspace)) return MOE_ERR_INVALID_ARG;
-  if (overlap(workspace, l.total, x, xbytes) || overlap(workspace, l.total, out, xbytes)) return MOE_ERR_INVALID_ARG;
+  if (overlap(workspace, need, x, xbytes) || overlap(workspace, need, out, xbytes)) return MOE_ERR_INVALID_ARG;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   void* ws = workspace;
   auto mark = [&](int stage, bool begin) -> moe_status {
@@ -526,7 +567,9 @@ static moe_status forward_impl(const void* x, const void* router_w, const void* 
     float* logits_out = routing ? routing->logits : nullptr;
 
     MOE_TRY(mark(MOE_STAGE_ROUTER_DOWN, true));
-    MOE_TRY(run_router_and_down(c, x, router_w, latent_down, ws, l, st));
+    LoraSeg seg;
+    if (lora_down) MOE_TRY(run_lora(lora_down, x, c.num_tokens, c.d_model, at<void>(ws, l.total), &seg, st));
+    MOE_TRY(run_router_and_down(c, x, router_w, latent_down, ws, l, st, lora_down ? &seg : nullptr));
     MOE_TRY(mark(MOE_STAGE_ROUTER_DOWN, false));
     RouteArgs ra = route_args(c, k, 0, x, router_w, router_bias, idx, w, logits_out, ws, l);
     ra.h = at<uint16_t>(ws, l.h);
@@ -636,7 +679,9 @@ static moe_status forward_impl(const void* x, const void* router_w, const void* 
     up.add = at<float>(ws, l.s_y);
     up.add_rows = c.num_shared;
   }
-  MOE_TRY(dev(launch_dense(at<uint16_t>(ws, l.z), c.num_tokens, c.d_latent, &up, 1, st)));
+  LoraSeg seg;
+  if (lora_up) MOE_TRY(run_lora(lora_up, at<void>(ws, l.z), c.num_tokens, c.d_latent, at<void>(ws, l.total), &seg, st));
+  MOE_TRY(dev(launch_dense(at<uint16_t>(ws, l.z), c.num_tokens, c.d_latent, &up, 1, st, lora_up ? &seg : nullptr)));
   return mark(MOE_STAGE_UP, false);
 }
 
@@ -670,6 +715,27 @@ moe_status moe_layer_forward_shared(const void* x, const void* router_w, const v
                                     moe_stream_t stream) {
   return forward_impl(x, router_w, latent_down, latent_up, expert_blob, k, cfg, router_bias, shared_blob, out,
                       routing, workspace, workspace_bytes, nullptr, stream);
+}
+
+moe_status moe_layer_lora_workspace_size(const moe_config* cfg, int32_t k, const moe_lora* lora_down,
+                                         const moe_lora* lora_up, size_t* bytes) {
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_config(cfg, k));
+  if (lora_down) MOE_TRY(check_lora(lora_down));
+  if (lora_up) MOE_TRY(check_lora(lora_up));
+  *bytes = layout(*cfg, k).total + std::max(lora_bytes(lora_down, cfg->num_tokens, cfg->d_model),
+                                            lora_bytes(lora_up, cfg->num_tokens, cfg->d_latent));
+  return MOE_OK;
+}
+
+moe_status moe_layer_forward_lora(const void* x, const void* router_w, const void* latent_down,
+                                  const void* latent_up, const uint8_t* expert_blob, int32_t k,
+                                  const moe_config* cfg, const float* router_bias, const uint8_t* shared_blob,
+                                  const moe_lora* lora_down, const moe_lora* lora_up, void* out,
+                                  moe_routing_out* routing, void* workspace, size_t workspace_bytes,
+                                  moe_stream_t stream) {
+  return forward_impl(x, router_w, latent_down, latent_up, expert_blob, k, cfg, router_bias, shared_blob, out,
+                      routing, workspace, workspace_bytes, nullptr, stream, nullptr, 0, lora_down, lora_up);
 }
 
 moe_status moe_layer_forward_profiled(const void* x, const void* router_w, const void* latent_down,
@@ -864,6 +930,41 @@ moe_status moe_linear_bf16(const void* in, const void* W, int64_t num_tokens, in
   s.xnorm = nullptr;
   return dev(launch_dense(static_cast<const uint16_t*>(in), num_tokens, n_in, &s, 1,
                                reinterpret_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_linear_lora_workspace_size(int64_t num_tokens, int32_t n_in, const moe_lora* lora, size_t* bytes) {
+  if (!bytes || !lora || num_tokens < 0 || n_in <= 0 || n_in % 32) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_lora(lora));
+  if (n_in > MAX_DIM || num_tokens > (int64_t)1 << 24) return MOE_ERR_UNSUPPORTED;
+  *bytes = num_tokens == 0 ? 0 : lora_bytes(lora, num_tokens, n_in);
+  return MOE_OK;
+}
+
+moe_status moe_linear_lora(const void* in, const void* W, const moe_lora* lora, int64_t num_tokens, int32_t n_in,
+                           int32_t n_out, void* out, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  size_t need = 0;
+  if (n_out <= 0) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(moe_linear_lora_workspace_size(num_tokens, n_in, lora, &need));
+  if (num_tokens == 0) return MOE_OK;
+  if (!in || !W || !out || !aligned16(in) || !aligned16(W) || (reinterpret_cast<uintptr_t>(out) & 1u))
+    return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_lora_pointers(lora));
+  if (!workspace || workspace_bytes < need) return MOE_ERR_WORKSPACE;
+  const size_t in_bytes = (size_t)num_tokens * n_in * 2, out_bytes = (size_t)num_tokens * n_out * 2;
+  if (!aligned16(workspace) || overlap(in, in_bytes, out, out_bytes) || overlap(workspace, need, in, in_bytes) ||
+      overlap(workspace, need, out, out_bytes))
+    return MOE_ERR_INVALID_ARG;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  LoraSeg seg;
+  MOE_TRY(run_lora(lora, in, num_tokens, n_in, workspace, &seg, st));
+  DenseSeg s;
+  s.W = static_cast<const uint16_t*>(W);
+  s.rows = n_out;
+  s.router = 0;
+  s.out = out;
+  s.wnorm = nullptr;
+  s.xnorm = nullptr;
+  return dev(launch_dense(static_cast<const uint16_t*>(in), num_tokens, n_in, &s, 1, st, &seg));
 }
 
 }  // extern "C"

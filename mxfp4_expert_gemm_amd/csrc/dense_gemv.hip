@@ -32,13 +32,19 @@ struct DenseParams {
   int32_t K;
   int32_t nseg;
   DenseSeg seg[2];
+  LoraSeg lora;  // of the last segment
 };
 
 // The token rows are staged once per block in LDS (their loads issued first, then the
 // weight row's, so the wait for them leaves the weight loads in flight): the registers
 // then hold only the weight row, and more waves fit a SIMD, so the router + latent-down
 // grid (4480 rows at one token) and the latent-up grid (7168 rows) run in one round.
-template <int NCH, int G>
+//
+// LORA: the last segment's rows also take their adapters' term, sum_r B[a_t][row][r] u[t][r].
+// Lane l holds ranks l and l + 64 of each token; the products (exact in fp64) join the lane's
+// fp64 sum before the wave reduction, so the term costs two loads a lane and token, issued
+// before the weight row's, and no rounding of its own.
+template <int NCH, int G, bool LORA>
 __global__ void __launch_bounds__(256) dense_gemv_kernel(DenseParams p) {
   constexpr int XN = G * NCH * 64;            // 16-byte pieces of the block's token rows
   constexpr int XPT = (XN + 255) / 256;       // per thread
@@ -67,6 +73,28 @@ __global__ void __launch_bounds__(256) dense_gemv_kernel(DenseParams p) {
     const int64_t t = t0 + g < p.T ? t0 + g : p.T - 1;
     xv[u] = *reinterpret_cast<const uint4*>(p.x + t * K + (col < K ? col : 0));
     if (col >= K || t0 + g >= p.T) xv[u] = make_uint4(0, 0, 0, 0);
+  }
+  uint16_t lb[LORA ? G : 1][2];
+  float lu[LORA ? G : 1][2];
+  if constexpr (LORA) {
+    const bool mine = second || p.nseg < 2;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int64_t t = t0 + g < p.T ? t0 + g : p.T - 1;
+      const int a = p.lora.adapter[t];
+      const bool on = mine && (uint32_t)a < (uint32_t)p.lora.N;
+      const int rk = !on ? 0 : !p.lora.rank ? p.lora.R : min(p.lora.rank[a], p.lora.R);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = lane + WAVE * h;
+        lb[g][h] = 0;
+        lu[g][h] = 0.f;
+        if (r < rk) {
+          lb[g][h] = p.lora.B[((int64_t)a * s.rows + row) * p.lora.R + r];
+          lu[g][h] = p.lora.u[t * p.lora.R + r];
+        }
+      }
+    }
   }
   uint4 wr[NCH];
   const uint16_t* wrow = s.W + row * K;
@@ -98,6 +126,12 @@ __global__ void __launch_bounds__(256) dense_gemv_kernel(DenseParams p) {
         pc = dot2(xc.w, wr[c].w, pc);
         acc[g] += (double)pc;
       }
+    if constexpr (LORA) {
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) acc[g] += (double)lu[g][h] * (double)bf16f(lb[g][h]);
+    }
     uint16_t* out = reinterpret_cast<uint16_t*>(s.out);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
@@ -170,7 +204,10 @@ static hipError_t launch_nch_g(const DenseParams& p, hipStream_t st) {
   int64_t rows = p.seg[0].rows + (p.nseg > 1 ? p.seg[1].rows : 0);
   if (ceil_div(p.T, G) > 65535 || ceil_div(rows, 4) > 0x7FFFFFFF) return hipErrorInvalidValue;
   dim3 grid((unsigned)ceil_div(rows, 4), (unsigned)ceil_div(p.T, G));
-  hipLaunchKernelGGL((dense_gemv_kernel<NCH, G>), grid, dim3(256), 0, st, p);
+  if (p.lora.B)
+    hipLaunchKernelGGL((dense_gemv_kernel<NCH, G, true>), grid, dim3(256), 0, st, p);
+  else
+    hipLaunchKernelGGL((dense_gemv_kernel<NCH, G, false>), grid, dim3(256), 0, st, p);
   return hipGetLastError();
 }
 
@@ -183,8 +220,9 @@ static hipError_t launch_nch(const DenseParams& p, hipStream_t st) {
 }
 
 hipError_t launch_dense_gemv(const uint16_t* x, int64_t T, int32_t K, const DenseSeg* segs, int nseg,
-                             hipStream_t st) {
+                             hipStream_t st, const LoraSeg* lora) {
   DenseParams p;
+  if (lora) p.lora = *lora;
   p.x = x;
   p.T = T;
   p.K = K;

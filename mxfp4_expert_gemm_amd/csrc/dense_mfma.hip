@@ -57,9 +57,65 @@ struct DenseMfmaArgs {
   int32_t nblocks;    // ntm * ntn (the grid is rounded up to a multiple of 8)
   const float* add;   // nullable: fp32 [T][add_rows][N] added before the bf16 rounding
   int32_t add_rows;
+  LoraSeg lora;       // LORA kernels: the adapters' term
 };
 
-template <int WM, int WN, int PF, bool ROUTER>
+// ranks [0, valid) of eight consecutive ones, zeros for the others (whatever is stored there)
+__device__ __forceinline__ u32x4_t keep_ranks(u32x4_t v, int valid) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = 2 * i + 1 < valid ? v[i] : 2 * i < valid ? v[i] & 0xFFFFu : 0u;
+  return v;
+}
+
+// The adapters' term of a wave's tile (16 WM tokens from tb, 16 WN rows from nb), added to
+// its accumulators: per 16 tokens, each adapter met among them multiplies all 16 rows of u
+// by its B (hi and lo terms of u: 16 significant bits, against the 8 of the output), and
+// the rows that name it take the product.  Taken by a select, not by zeroed operands: an
+// infinity in one request's adapter must not reach another request's row.  Tokens of one
+// request usually stand together, so most tiles meet one adapter or two.
+template <int WM, int WN>
+__device__ __forceinline__ void lora_expand(const DenseMfmaArgs& p, int64_t tb, int nb, f32x4_t (&acc)[WM][WN]) {
+  const LoraSeg& l = p.lora;
+  const int lane = lane_id(), nl = lane & 15, g = lane >> 4;
+  const int RP = rank_pad(l.R);
+#pragma unroll
+  for (int i = 0; i < WM; ++i) {
+    const int64_t t = tb + 16 * i + nl;
+    const int64_t tc = t < p.T ? t : p.T - 1;
+    int a = l.adapter[tc];
+    if (t >= p.T || (uint32_t)a >= (uint32_t)l.N) a = -1;
+    for (uint32_t todo = (uint32_t)__ballot(a >= 0) & 0xFFFFu; todo;) {
+      const int ad = __builtin_amdgcn_readlane(a, __ffs((int)todo) - 1);
+      const uint32_t same = (uint32_t)__ballot(a == ad) & 0xFFFFu;
+      todo &= ~same;
+      const int rk = l.rank ? min(l.rank[ad], l.R) : l.R;
+      const uint16_t* B = l.B + (int64_t)ad * p.N * l.R;
+      f32x4_t d[WN];
+#pragma unroll
+      for (int jn = 0; jn < WN; ++jn) d[jn] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int r0 = 0; r0 < rk; r0 += 32) {
+        const int r = r0 + 8 * g;
+        const bf16x8_t hi = *reinterpret_cast<const bf16x8_t*>(l.uhi + tc * RP + r);
+        const bf16x8_t lo = *reinterpret_cast<const bf16x8_t*>(l.ulo + tc * RP + r);
+#pragma unroll
+        for (int jn = 0; jn < WN; ++jn) {
+          const int n = nb + 16 * jn + nl < p.N ? nb + 16 * jn + nl : p.N - 1;
+          u32x4_t v = {0u, 0u, 0u, 0u};
+          if (r < rk) v = keep_ranks(*reinterpret_cast<const u32x4_t*>(B + (int64_t)n * l.R + r), rk - r);
+          const bf16x8_t b = __builtin_bit_cast(bf16x8_t, v);
+          d[jn] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, b, d[jn], 0, 0, 0);
+          d[jn] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, b, d[jn], 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int jn = 0; jn < WN; ++jn)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][jn][j] += (same >> (4 * g + j)) & 1u ? d[jn][j] : 0.f;
+    }
+  }
+}
+
+template <int WM, int WN, int PF, bool ROUTER, bool LORA>
 __global__ void __launch_bounds__(256, 2) dense_mfma_kernel(DenseMfmaArgs p) {
   constexpr int BM = 32 * WM, BN = 32 * WN;
   constexpr int AP = BM * 8 / 256, BP = BN * 8 / 256;  // 16-byte pieces per thread and K tile
@@ -183,6 +239,7 @@ __global__ void __launch_bounds__(256, 2) dense_mfma_kernel(DenseMfmaArgs p) {
     });
   }
 
+  if constexpr (LORA) lora_expand<WM, WN>(p, t0 + 16 * WM * wm, n0 + 16 * WN * wn, acc);
 #pragma unroll
   for (int i = 0; i < WM; ++i)
 #pragma unroll
@@ -214,7 +271,7 @@ __global__ void __launch_bounds__(256, 2) dense_mfma_kernel(DenseMfmaArgs p) {
 // K-tile arithmetic (and the router's fp64 folds) is the one of dense_mfma_kernel, so the
 // results are the same.  (Wave tiles of 128 x 64 in 256 x 128 blocks, which the free
 // registers allow at one block per CU, measured 2.69 ms against 1.67 ms at prefill32k.)
-template <int WM, int WN, bool ROUTER, int MINB>
+template <int WM, int WN, bool ROUTER, int MINB, bool LORA>
 __global__ void __launch_bounds__(256, MINB) dense_mfma_dma_kernel(DenseMfmaArgs p) {
   constexpr int BM = 32 * WM, BN = 32 * WN;
   constexpr int NU = (BM + BN) / 32;  // 1 KB loads per wave and K tile
@@ -307,6 +364,7 @@ __global__ void __launch_bounds__(256, MINB) dense_mfma_dma_kernel(DenseMfmaArgs
     wait_barrier();  // tile kt + 1 is in LDS; every wave is past tile kt
   }
 
+  if constexpr (LORA) lora_expand<WM, WN>(p, t0 + 16 * WM * wm, n0 + 16 * WN * wn, acc);
 #pragma unroll
   for (int i = 0; i < WM; ++i)
 #pragma unroll
@@ -381,7 +439,7 @@ double dense_router_gamma(int64_t T, int32_t K) {
   return dense_uses_mfma(T, K) ? DENSE_MFMA_ROUTER_GAMMA : GEMV_ROUTER_GAMMA;
 }
 
-template <int WM, int WN, int PF, bool ROUTER>
+template <int WM, int WN, int PF, bool ROUTER, bool LORA = false>
 static hipError_t launch_dm(const DenseMfmaArgs& a0, hipStream_t st) {
   constexpr int BM = 32 * WM, BN = 32 * WN;
   constexpr int LDS = 2 * (BM + BN) * DM_RS;
@@ -394,15 +452,15 @@ static hipError_t launch_dm(const DenseMfmaArgs& a0, hipStream_t st) {
   const unsigned grid = (unsigned)((nb + 7) / 8 * 8);
   if constexpr (LDS > 65536) {
     static const hipError_t e = hipFuncSetAttribute(
-        reinterpret_cast<const void*>(&dense_mfma_kernel<WM, WN, PF, ROUTER>),
+        reinterpret_cast<const void*>(&dense_mfma_kernel<WM, WN, PF, ROUTER, LORA>),
         hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((dense_mfma_kernel<WM, WN, PF, ROUTER>), dim3(grid), dim3(256), LDS, st, a);
+  hipLaunchKernelGGL((dense_mfma_kernel<WM, WN, PF, ROUTER, LORA>), dim3(grid), dim3(256), LDS, st, a);
   return hipGetLastError();
 }
 
-template <int WM, int WN, bool ROUTER, int MINB>
+template <int WM, int WN, bool ROUTER, int MINB, bool LORA = false>
 static hipError_t launch_dm_dma(const DenseMfmaArgs& a0, hipStream_t st) {
   constexpr int BM = 32 * WM, BN = 32 * WN;
   constexpr int LDS = 2 * (BM + BN) * DM_RS;
@@ -415,11 +473,11 @@ static hipError_t launch_dm_dma(const DenseMfmaArgs& a0, hipStream_t st) {
   const unsigned grid = (unsigned)((nb + 7) / 8 * 8);
   if constexpr (LDS > 65536) {
     static const hipError_t e = hipFuncSetAttribute(
-        reinterpret_cast<const void*>(&dense_mfma_dma_kernel<WM, WN, ROUTER, MINB>),
+        reinterpret_cast<const void*>(&dense_mfma_dma_kernel<WM, WN, ROUTER, MINB, LORA>),
         hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((dense_mfma_dma_kernel<WM, WN, ROUTER, MINB>), dim3(grid), dim3(256), LDS, st, a);
+  hipLaunchKernelGGL((dense_mfma_dma_kernel<WM, WN, ROUTER, MINB, LORA>), dim3(grid), dim3(256), LDS, st, a);
   return hipGetLastError();
 }
 
@@ -440,7 +498,21 @@ static int small_tile(int64_t T, int32_t N) {
   return 2;
 }
 
-hipError_t launch_dense_mfma(const uint16_t* x, int64_t T, int32_t K, const DenseSeg& s, hipStream_t st) {
+// the latent projections, with the adapters' term or without
+template <bool LORA>
+static hipError_t launch_projection(const DenseMfmaArgs& a, hipStream_t st) {
+  if (a.T >= 256)
+    return dm_dma_pays(a.T, a.N, 128, 128) ? launch_dm_dma<4, 4, false, 2, LORA>(a, st)
+                                           : launch_dm<4, 4, 2, false, LORA>(a, st);
+  switch (small_tile(a.T, a.N)) {
+    case 0: return launch_dm<2, 2, 4, false, LORA>(a, st);
+    case 1: return launch_dm<2, 1, 4, false, LORA>(a, st);
+    default: return launch_dm<1, 1, 4, false, LORA>(a, st);
+  }
+}
+
+hipError_t launch_dense_mfma(const uint16_t* x, int64_t T, int32_t K, const DenseSeg& s, hipStream_t st,
+                             const LoraSeg* lora) {
   if (T == 0) return hipSuccess;
   if (!dense_uses_mfma(T, K) || s.rows <= 0) return hipErrorInvalidValue;
   DenseMfmaArgs a;
@@ -463,19 +535,16 @@ hipError_t launch_dense_mfma(const uint16_t* x, int64_t T, int32_t K, const Dens
       default: return launch_dm<1, 1, 4, true>(a, st);
     }
   }
-  if (T >= 256)
-    return dm_dma_pays(T, s.rows, 128, 128) ? launch_dm_dma<4, 4, false, 2>(a, st) : launch_dm<4, 4, 2, false>(a, st);
-  switch (small_tile(T, s.rows)) {
-    case 0: return launch_dm<2, 2, 4, false>(a, st);
-    case 1: return launch_dm<2, 1, 4, false>(a, st);
-    default: return launch_dm<1, 1, 4, false>(a, st);
-  }
+  if (!lora) return launch_projection<false>(a, st);
+  a.lora = *lora;
+  return launch_projection<true>(a, st);
 }
 
-hipError_t launch_dense(const uint16_t* x, int64_t T, int32_t K, const DenseSeg* segs, int nseg, hipStream_t st) {
-  if (!dense_uses_mfma(T, K)) return launch_dense_gemv(x, T, K, segs, nseg, st);
+hipError_t launch_dense(const uint16_t* x, int64_t T, int32_t K, const DenseSeg* segs, int nseg, hipStream_t st,
+                        const LoraSeg* lora) {
+  if (!dense_uses_mfma(T, K)) return launch_dense_gemv(x, T, K, segs, nseg, st, lora);
   for (int i = 0; i < nseg; ++i) {
-    const hipError_t e = launch_dense_mfma(x, T, K, segs[i], st);
+    const hipError_t e = launch_dense_mfma(x, T, K, segs[i], st, i == nseg - 1 ? lora : nullptr);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;

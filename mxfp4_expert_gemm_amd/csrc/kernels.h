@@ -11,6 +11,37 @@ namespace moe {
 hipError_t launch_dequant(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols,
                           float* out, hipStream_t st);
 
+// ---- lora.hip: low-rank adapters beside a projection
+// The second half of an adapter's term, added where the projection is computed:
+// out[t][o] += sum_r B[a_t][o][r] u[t][r] with u already scaled and zero past the adapter's
+// rank.  B null: no adapters.
+struct LoraSeg {
+  const uint16_t* B = nullptr;         // [N][n_out][R]
+  const int32_t* adapter = nullptr;    // [T]; ids outside [0, N) have no term
+  const int32_t* rank = nullptr;       // nullable [N]
+  const float* u = nullptr;            // [T][R], the GEMV's operand
+  const uint16_t* uhi = nullptr;       // [T][rank_pad(R)] bf16, the matrix cores' operand: u = uhi + ulo
+  const uint16_t* ulo = nullptr;
+  int32_t N = 0, R = 0;
+};
+constexpr int LORA_MAX_RANK = 128;
+constexpr int LORA_MAX_ADAPTERS = 1024;
+// ranks on the matrix cores come in K steps of 32
+__host__ __device__ constexpr int rank_pad(int R) { return (R + 31) / 32 * 32; }
+struct LoraArgs {
+  const uint16_t* x;       // [T][K]
+  const uint16_t* A;       // [N][R][K]
+  const uint16_t* B;       // [N][n_out][R]
+  const float* scale;      // [N]
+  const int32_t* rank;     // nullable [N]
+  const int32_t* adapter;  // [T]
+  int64_t T;
+  int32_t K, N, R;
+};
+size_t lora_ws_bytes(int64_t T, int32_t K, int32_t N, int32_t R);
+// u of every token into the workspace; *seg names it for launch_dense
+hipError_t launch_lora_shrink(const LoraArgs& a, void* ws, LoraSeg* seg, hipStream_t st);
+
 // ---- dense_gemv.hip
 // One output "segment" of a dense bf16 GEMV over rows of W[rows][K].
 struct DenseSeg {
@@ -26,17 +57,20 @@ struct DenseSeg {
 // Relative accumulation error bound of router logits from launch_dense_gemv, per
 // unit of |x_t| |w_e| (see the kernel for its derivation).
 constexpr double GEMV_ROUTER_GAMMA = 16.0 / 8388608.0;  // 16 * 2^-23
+// lora, when given, is the adapters' term of the last segment
 hipError_t launch_dense_gemv(const uint16_t* x, int64_t T, int32_t K, const DenseSeg* segs, int nseg,
-                             hipStream_t st);
+                             hipStream_t st, const LoraSeg* lora = nullptr);
 
 // ---- dense_mfma.hip: the same projections on the matrix cores for token batches
 constexpr double DENSE_MFMA_ROUTER_GAMMA = 66.0 / 8388608.0;  // 66 * 2^-23
 bool dense_uses_mfma(int64_t T, int32_t K);
 // relative error bound of the router logits of launch_dense for T tokens of width K
 double dense_router_gamma(int64_t T, int32_t K);
-hipError_t launch_dense_mfma(const uint16_t* x, int64_t T, int32_t K, const DenseSeg& s, hipStream_t st);
+hipError_t launch_dense_mfma(const uint16_t* x, int64_t T, int32_t K, const DenseSeg& s, hipStream_t st,
+                             const LoraSeg* lora = nullptr);
 // the GEMV for few tokens, the matrix-core GEMM otherwise
-hipError_t launch_dense(const uint16_t* x, int64_t T, int32_t K, const DenseSeg* segs, int nseg, hipStream_t st);
+hipError_t launch_dense(const uint16_t* x, int64_t T, int32_t K, const DenseSeg* segs, int nseg, hipStream_t st,
+                        const LoraSeg* lora = nullptr);
 
 // ---- route.hip
 struct RouteArgs {
