@@ -431,6 +431,27 @@ moe_status moe_layer_forward_lora(const void* x, const void* router_w, const voi
                                   moe_routing_out* routing, void* workspace, size_t workspace_bytes,
                                   moe_stream_t stream);
 
+/* ---- the layer for the few tokens of a decode step ---- */
+
+/* moe_layer_forward for up to MOE_DECODE_MAX_TOKENS tokens with num_tokens * k at most
+ * MOE_DECODE_MAX_ROWS, in two launches (three with lora_down) instead of five or more, for
+ * callers to whom a step's latency counts.  The result, routing outputs included, is that of
+ * moe_layer_forward / moe_layer_forward_lora bit for bit.
+ *  - lora_down, lora_up: nullable adapters on the latent projections.
+ *  - Larger batches, cfg->num_shared > 0 and routing->saliency return MOE_ERR_UNSUPPORTED.
+ *  - Workspace: moe_layer_decode_workspace_size bytes, 16-byte aligned, needing no clearing;
+ *    calls that may overlap in time need workspaces of their own.
+ *  - The second launch's blocks hand work over within the launch; a block waits only for
+ *    blocks that already run, so it shares the GPU with any other work. */
+#define MOE_DECODE_MAX_TOKENS 8
+#define MOE_DECODE_MAX_ROWS 64
+moe_status moe_layer_decode_workspace_size(const moe_config* cfg, int32_t k, const moe_lora* lora_down,
+                                           const moe_lora* lora_up, size_t* bytes);
+moe_status moe_layer_decode(const void* x, const void* router_w, const void* latent_down, const void* latent_up,
+                            const uint8_t* expert_blob, int32_t k, const moe_config* cfg, const float* router_bias,
+                            const moe_lora* lora_down, const moe_lora* lora_up, void* out, moe_routing_out* routing,
+                            void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -32,7 +32,8 @@ EXPORTS = ["moe_expert_bytes", "moe_packed_expert_bytes", "moe_pack_experts", "m
            "moe_linear_bf16", "moe_reap_saliency", "moe_layer_forward_shared", "moe_expert_slots_bytes",
            "moe_layer_forward_streamed", "moe_layer_forward_noalloc", "moe_reap_keep_bias",
            "moe_permute_workspace_size", "moe_linear_lora_workspace_size", "moe_linear_lora",
-           "moe_layer_lora_workspace_size", "moe_layer_forward_lora"]
+           "moe_layer_lora_workspace_size", "moe_layer_forward_lora", "moe_layer_decode_workspace_size",
+           "moe_layer_decode"]
 
 
 class MoEError(RuntimeError):
@@ -130,6 +131,8 @@ def lib():
             "moe_layer_lora_workspace_size": (ctypes.c_int, [cfgp, i32, lp, lp, ctypes.POINTER(sz)]),
             "moe_layer_forward_lora": (ctypes.c_int, [vp, vp, vp, vp, vp, i32, cfgp, vp, vp, lp, lp, vp, rp, vp, sz,
                                                       vp]),
+            "moe_layer_decode_workspace_size": (ctypes.c_int, [cfgp, i32, lp, lp, ctypes.POINTER(sz)]),
+            "moe_layer_decode": (ctypes.c_int, [vp, vp, vp, vp, vp, i32, cfgp, vp, lp, lp, vp, rp, vp, sz, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -306,6 +309,45 @@ def layer_forward(x, router_w, latent_down, latent_up, expert_blob, k: int, *, d
         _check(lib().moe_layer_forward(_p(x), _p(router_w), _p(latent_down), _p(latent_up), _p(expert_blob), k,
                                        ctypes.byref(cfg), _p(bias), _p(out), ctypes.byref(r) if r else None,
                                        _p(workspace), workspace.numel(), _stream(stream)), "moe_layer_forward")
+    return out
+
+
+DECODE_MAX_TOKENS, DECODE_MAX_ROWS = 8, 64  # MOE_DECODE_MAX_TOKENS, MOE_DECODE_MAX_ROWS
+
+
+def layer_decode_workspace_size(cfg: MoEConfig, k: int, down: Optional[LoraArg] = None,
+                                up: Optional[LoraArg] = None) -> int:
+    n = ctypes.c_size_t(0)
+    ref = lambda a: None if a is None else ctypes.byref(a)
+    _check(lib().moe_layer_decode_workspace_size(ctypes.byref(cfg), k, ref(down), ref(up), ctypes.byref(n)),
+           "moe_layer_decode_workspace_size")
+    return int(n.value)
+
+
+def layer_decode(x, router_w, latent_down, latent_up, expert_blob, k: int, *, d_ffn: int,
+                 bias: Optional[torch.Tensor] = None, renormalize: bool = True, act: int = ACT_SILU,
+                 out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                 routing: Optional[dict] = None, stream=None, packed: bool = False,
+                 act_format: int = ACT_FMT_BF16, lora_down: Optional[Lora] = None,
+                 lora_up: Optional[Lora] = None) -> torch.Tensor:
+    """layer_forward for a decode step of at most DECODE_MAX_TOKENS tokens and DECODE_MAX_ROWS
+    routed rows (moe_layer_decode): the same result, bit for bit, in two launches."""
+    T, d = x.shape
+    L = latent_down.shape[0]
+    cfg = make_config(T, d, L, d_ffn, router_w.shape[0], act=act, renormalize=renormalize, bias=bias, packed=packed,
+                      act_format=act_format)
+    _same_device(x, router_w, latent_down, latent_up, expert_blob, out, workspace)
+    down = None if lora_down is None else _lora(lora_down, T, d, L, x.device)
+    up = None if lora_up is None else _lora(lora_up, T, L, d, x.device)
+    if out is None:
+        out = torch.empty((T, d), dtype=x.dtype, device=x.device)
+    if workspace is None:
+        workspace = torch.empty(layer_decode_workspace_size(cfg, k, down, up), dtype=torch.uint8, device=x.device)
+    r = _routing(routing)
+    ref = lambda a: None if a is None else ctypes.byref(a)
+    _check(lib().moe_layer_decode(_p(x), _p(router_w), _p(latent_down), _p(latent_up), _p(expert_blob), k,
+                                  ctypes.byref(cfg), _p(bias), ref(down), ref(up), _p(out), ref(r), _p(workspace),
+                                  workspace.numel(), _stream(stream)), "moe_layer_decode")
     return out
 
 
@@ -506,4 +548,5 @@ __all__ = ["lib", "MoEConfig", "RoutingOut", "MoEError", "make_config", "expert_
            "alloc_workspace", "layer_forward", "layer_forward_profiled", "StageEvents", "STAGES", "dequant_mxfp4", "route", "topk", "permute", "expert_ffn", "combine",
            "linear_bf16", "reap_saliency", "reap_prune_bias", "ACT_SILU", "ACT_SITU", "ROUTE_EXACT_ALL", "EXPORTS",
            "LIB_PATH", "expert_slots_bytes", "alloc_expert_slots", "layer_forward_streamed", "layer_forward_noalloc",
-           "NOALLOC_SCRATCH_BYTES", "Lora", "linear_lora", "linear_lora_workspace_size", "layer_lora_workspace_size"]
+           "NOALLOC_SCRATCH_BYTES", "Lora", "linear_lora", "linear_lora_workspace_size", "layer_lora_workspace_size",
+           "layer_decode", "layer_decode_workspace_size", "DECODE_MAX_TOKENS", "DECODE_MAX_ROWS"]

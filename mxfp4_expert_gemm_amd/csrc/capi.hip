@@ -202,16 +202,23 @@ moe_status zero_i32(int32_t* p, int n, hipStream_t st) {
   return dev(hipGetLastError());
 }
 
+template <class Lay>
+DenseSeg router_seg(const moe_config& c, const void* router_w, void* ws, const Lay& l) {
+  DenseSeg s;
+  s.W = static_cast<const uint16_t*>(router_w);
+  s.rows = c.num_experts;
+  s.router = 1;
+  s.out = at<float>(ws, l.logits_fast);
+  s.wnorm = at<float>(ws, l.wnorm);
+  s.xnorm = at<float>(ws, l.xnorm);
+  return s;
+}
+
 // router logits (fast, with norms) and optionally the latent down projection, in one launch
 moe_status run_router_and_down(const moe_config& c, const void* x, const void* router_w, const void* latent_down,
                                void* ws, const Layout& l, hipStream_t st, const LoraSeg* lora = nullptr) {
   DenseSeg segs[2];
-  segs[0].W = static_cast<const uint16_t*>(router_w);
-  segs[0].rows = c.num_experts;
-  segs[0].router = 1;
-  segs[0].out = at<float>(ws, l.logits_fast);
-  segs[0].wnorm = at<float>(ws, l.wnorm);
-  segs[0].xnorm = at<float>(ws, l.xnorm);
+  segs[0] = router_seg(c, router_w, ws, l);
   int nseg = 1;
   if (latent_down) {
     segs[1].W = static_cast<const uint16_t*>(latent_down);
@@ -257,8 +264,9 @@ moe_status run_lora(const moe_lora* a, const void* x, int64_t T, int32_t n_in, v
   return dev(launch_lora_shrink(p, ws, seg, st));
 }
 
+template <class Lay>
 RouteArgs route_args(const moe_config& c, int k, int flags, const void* x, const void* router_w, const float* bias,
-                     int32_t* idx, float* w, float* logits_out, void* ws, const Layout& l) {
+                     int32_t* idx, float* w, float* logits_out, void* ws, const Lay& l) {
   RouteArgs a;
   a.logits_fast = at<float>(ws, l.logits_fast);
   a.xnorm = at<float>(ws, l.xnorm);
@@ -314,6 +322,40 @@ MxArgs mx_args(const moe_config& c, int k, const uint8_t* blob, void* ws, const 
   m.sal = nullptr;
   m.sal_chunks = 0;
   return m;
+}
+
+// ---- workspace of the few-token layer
+struct DecodeLayout {
+  size_t logits_fast, xnorm, wnorm, h, aq, z, u, ctr, lora_down, total;
+};
+DecodeLayout decode_layout(const moe_config& c, int k, const moe_lora* down, const moe_lora* up) {
+  DecodeLayout l;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align_up(off + bytes, 256);
+    return o;
+  };
+  const size_t T = (size_t)c.num_tokens, E = (size_t)c.num_experts, L = (size_t)c.d_latent;
+  l.logits_fast = take(T * E * 4);
+  l.xnorm = take(T * 4);
+  l.wnorm = take(E * 4);
+  l.h = take(T * L * 2);
+  l.aq = take(decode_aq_bytes((int64_t)T * k, c.d_ffn));
+  l.z = take(T * L * 2);
+  l.u = take(up ? T * (size_t)up->max_rank * 4 : 0);
+  l.ctr = take(DECODE_COUNTERS * 4);
+  l.lora_down = take(lora_bytes(down, c.num_tokens, c.d_model));
+  l.total = off;
+  return l;
+}
+moe_status check_decode(const moe_config* cfg, int32_t k, const moe_lora* down, const moe_lora* up) {
+  MOE_TRY(check_config(cfg, k));
+  if (down) MOE_TRY(check_lora(down));
+  if (up) MOE_TRY(check_lora(up));
+  if (cfg->num_tokens > DECODE_MAX_TOKENS || cfg->num_tokens * k > DECODE_MAX_ROWS || cfg->num_shared > 0)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
 }
 
 // ---- scratch of the entry point without a workspace argument
@@ -930,6 +972,79 @@ moe_status moe_linear_bf16(const void* in, const void* W, int64_t num_tokens, in
   s.xnorm = nullptr;
   return dev(launch_dense(static_cast<const uint16_t*>(in), num_tokens, n_in, &s, 1,
                                reinterpret_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_layer_decode_workspace_size(const moe_config* cfg, int32_t k, const moe_lora* lora_down,
+                                           const moe_lora* lora_up, size_t* bytes) {
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_decode(cfg, k, lora_down, lora_up));
+  *bytes = decode_layout(*cfg, k, lora_down, lora_up).total;
+  return MOE_OK;
+}
+
+moe_status moe_layer_decode(const void* x, const void* router_w, const void* latent_down, const void* latent_up,
+                            const uint8_t* expert_blob, int32_t k, const moe_config* cfg, const float* router_bias,
+                            const moe_lora* lora_down, const moe_lora* lora_up, void* out, moe_routing_out* routing,
+                            void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  MOE_TRY(check_decode(cfg, k, lora_down, lora_up));
+  const moe_config& c = *cfg;
+  if (routing && routing->saliency) return MOE_ERR_UNSUPPORTED;
+  if (c.num_tokens == 0) return MOE_OK;
+  if (!x || !router_w || !latent_down || !latent_up || !expert_blob || !out || !aligned16(x) || !aligned16(router_w) ||
+      !aligned16(latent_down) || !aligned16(latent_up) || !aligned16(expert_blob) || !aligned16(out))
+    return MOE_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(router_bias) & 3u) return MOE_ERR_INVALID_ARG;
+  if (lora_down) MOE_TRY(check_lora_pointers(lora_down));
+  if (lora_up) MOE_TRY(check_lora_pointers(lora_up));
+  const DecodeLayout l = decode_layout(c, k, lora_down, lora_up);
+  if (!workspace || workspace_bytes < l.total) return MOE_ERR_WORKSPACE;
+  const size_t xbytes = (size_t)c.num_tokens * c.d_model * 2;
+  if (!aligned16(workspace) || overlap(x, xbytes, out, xbytes) || overlap(workspace, l.total, x, xbytes) ||
+      overlap(workspace, l.total, out, xbytes))
+    return MOE_ERR_INVALID_ARG;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  void* ws = workspace;
+
+  LoraSeg down;
+  if (lora_down) MOE_TRY(run_lora(lora_down, x, c.num_tokens, c.d_model, at<void>(ws, l.lora_down), &down, st));
+  DenseSeg segs[2];
+  segs[0] = router_seg(c, router_w, ws, l);
+  segs[1].W = static_cast<const uint16_t*>(latent_down);
+  segs[1].rows = c.d_latent;
+  segs[1].router = 0;
+  segs[1].out = at<uint16_t>(ws, l.h);
+  segs[1].wnorm = segs[1].xnorm = nullptr;
+  MOE_TRY(dev(launch_dense_gemv(static_cast<const uint16_t*>(x), c.num_tokens, c.d_model, segs, 2, st,
+                                lora_down ? &down : nullptr, at<int32_t>(ws, l.ctr), DECODE_COUNTERS)));
+  DecodeArgs a;
+  a.r = route_args(c, k, 0, x, router_w, router_bias, nullptr, nullptr, routing ? routing->logits : nullptr, ws, l);
+  a.r.h = at<uint16_t>(ws, l.h);
+  a.blob = expert_blob;
+  a.F = c.d_ffn;
+  a.latent_up = static_cast<const uint16_t*>(latent_up);
+  a.aq = at<uint8_t>(ws, l.aq);
+  a.z = at<uint16_t>(ws, l.z);
+  a.out = static_cast<uint16_t*>(out);
+  a.ctr = at<int32_t>(ws, l.ctr);
+  a.lora_a = nullptr;
+  a.lora_scale = nullptr;
+  a.u = nullptr;
+  if (lora_up) {
+    a.lora.B = static_cast<const uint16_t*>(lora_up->b);
+    a.lora.adapter = lora_up->adapter;
+    a.lora.rank = lora_up->rank;
+    a.lora.N = lora_up->num_adapters;
+    a.lora.R = lora_up->max_rank;
+    a.lora_a = static_cast<const uint16_t*>(lora_up->a);
+    a.lora_scale = lora_up->scale;
+    a.u = at<float>(ws, l.u);
+  }
+  a.idx = routing ? routing->topk_idx : nullptr;
+  a.w = routing ? routing->topk_w : nullptr;
+  a.counts = routing ? routing->expert_counts : nullptr;
+  a.offsets = routing ? routing->expert_offsets : nullptr;
+  a.perm = routing ? routing->perm : nullptr;
+  return dev(launch_decode(a, c.expert_layout == MOE_LAYOUT_PACKED, st));
 }
 
 moe_status moe_linear_lora_workspace_size(int64_t num_tokens, int32_t n_in, const moe_lora* lora, size_t* bytes) {

@@ -58,8 +58,10 @@ struct DenseSeg {
 // unit of |x_t| |w_e| (see the kernel for its derivation).
 constexpr double GEMV_ROUTER_GAMMA = 16.0 / 8388608.0;  // 16 * 2^-23
 // lora, when given, is the adapters' term of the last segment
+// clear, when given, is nclear words (at most 256) that the launch sets to zero
 hipError_t launch_dense_gemv(const uint16_t* x, int64_t T, int32_t K, const DenseSeg* segs, int nseg,
-                             hipStream_t st, const LoraSeg* lora = nullptr);
+                             hipStream_t st, const LoraSeg* lora = nullptr, int32_t* clear = nullptr,
+                             int32_t nclear = 0);
 
 // ---- dense_mfma.hip: the same projections on the matrix cores for token batches
 constexpr double DENSE_MFMA_ROUTER_GAMMA = 66.0 / 8388608.0;  // 66 * 2^-23
@@ -210,6 +212,33 @@ hipError_t launch_reap_partials(const double* sal, int32_t nch, const float* w, 
 // bias[e] = 0 for the n_keep experts of highest saliency (ties to the lower index, NaN
 // lowest), -inf for the others
 hipError_t launch_reap_keep_bias(const double* saliency, int32_t E, int32_t n_keep, float* bias, hipStream_t st);
+
+// ---- decode.hip: a few tokens' layer behind the router logits and the latent rows
+constexpr int DECODE_MAX_TOKENS = 8;
+constexpr int DECODE_MAX_ROWS = 64;   // T * k
+constexpr int DECODE_COUNTERS = 224;  // words of phase counters, zero when the kernel starts
+struct DecodeArgs {
+  RouteArgs r;               // h set; idx, w and hq unused
+  const uint8_t* blob;
+  int32_t F;
+  const uint16_t* latent_up;  // [d][L]
+  uint8_t* aq;               // decode_aq_bytes(T*k, F): the GLU rows by slot, quantised
+  uint16_t* z;               // [T][L]
+  uint16_t* out;             // [T][d]
+  int32_t* ctr;              // [DECODE_COUNTERS]
+  LoraSeg lora;              // of latent_up; u is this kernel's own
+  const uint16_t* lora_a;    // [N][R][L]
+  const float* lora_scale;   // [N]
+  float* u;                  // [T][R]
+  // the caller's, nullable
+  int32_t* idx;
+  float* w;
+  int32_t* counts;
+  int32_t* offsets;
+  int32_t* perm;
+};
+size_t decode_aq_bytes(int64_t rows, int32_t F);
+hipError_t launch_decode(const DecodeArgs& a, bool packed, hipStream_t st);
 
 // ---- combine.hip
 hipError_t launch_combine(const float* y, const float* w, int64_t T, int32_t k, int32_t L, uint16_t* z,
