@@ -326,7 +326,7 @@ MxArgs mx_args(const moe_config& c, int k, const uint8_t* blob, void* ws, const 
 
 // ---- workspace of the few-token layer
 struct DecodeLayout {
-  size_t logits_fast, xnorm, wnorm, h, aq, z, u, ctr, lora_down, total;
+  size_t logits_fast, xnorm, wnorm, h, aq, y, z, u, ctr, lora_down, total;
 };
 DecodeLayout decode_layout(const moe_config& c, int k, const moe_lora* down, const moe_lora* up) {
   DecodeLayout l;
@@ -342,9 +342,10 @@ DecodeLayout decode_layout(const moe_config& c, int k, const moe_lora* down, con
   l.wnorm = take(E * 4);
   l.h = take(T * L * 2);
   l.aq = take(decode_aq_bytes((int64_t)T * k, c.d_ffn));
+  l.y = take(T * (size_t)k * L * 4);
   l.z = take(T * L * 2);
   l.u = take(up ? T * (size_t)up->max_rank * 4 : 0);
-  l.ctr = take(DECODE_COUNTERS * 4);
+  l.ctr = take((size_t)decode_counters(c.d_latent) * 128);
   l.lora_down = take(lora_bytes(down, c.num_tokens, c.d_model));
   l.total = off;
   return l;
@@ -1015,7 +1016,7 @@ moe_status moe_layer_decode(const void* x, const void* router_w, const void* lat
   segs[1].out = at<uint16_t>(ws, l.h);
   segs[1].wnorm = segs[1].xnorm = nullptr;
   MOE_TRY(dev(launch_dense_gemv(static_cast<const uint16_t*>(x), c.num_tokens, c.d_model, segs, 2, st,
-                                lora_down ? &down : nullptr, at<int32_t>(ws, l.ctr), DECODE_COUNTERS)));
+                                lora_down ? &down : nullptr, at<int32_t>(ws, l.ctr), decode_counters(c.d_latent))));
   DecodeArgs a;
   a.r = route_args(c, k, 0, x, router_w, router_bias, nullptr, nullptr, routing ? routing->logits : nullptr, ws, l);
   a.r.h = at<uint16_t>(ws, l.h);
@@ -1023,6 +1024,7 @@ moe_status moe_layer_decode(const void* x, const void* router_w, const void* lat
   a.F = c.d_ffn;
   a.latent_up = static_cast<const uint16_t*>(latent_up);
   a.aq = at<uint8_t>(ws, l.aq);
+  a.y = at<float>(ws, l.y);
   a.z = at<uint16_t>(ws, l.z);
   a.out = static_cast<uint16_t*>(out);
   a.ctr = at<int32_t>(ws, l.ctr);

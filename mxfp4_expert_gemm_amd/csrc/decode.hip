@@ -4,22 +4,33 @@
 // A decode step of a few tokens reads a few hundred MB once, so its time is the HBM's plus
 // what each launch costs on the way: its first loads' latency, its last blocks' drain, and
 // the routing, during which nothing streams.  Here one block per CU goes through the phases
-//   route      every block routes all tokens for itself (a wave per token) and quantises h
-//              into its LDS: no block waits for another's selection;
-//   gate / up  work items of 32 FFN rows of one routed expert, a wave each;
-//   down       work items of 16 latent rows of all routed experts, with the combine;
-//   up         work items of a few output rows a wave;
-// and phases hand over through counters in the workspace, not through launches.
+//   route      every block routes all tokens for itself and quantises h into its LDS: no
+//              block waits for another's selection;
+//   gate / up  16 FFN rows of one routed expert for its tokens, a wave each; two of them make a
+//              scale block of the down operand, which the later one quantises;
+//   down       16 latent rows of up to 16 routed rows, a block each, with the combine where
+//              that is all of them (else the block that finishes a group of rows combines);
+//   up         a share of the output rows per block, whose weights are under way long
+//              before: some into the LDS while the routing runs, some into registers while
+//              the last gate / up items finish.
 //
-// Progress.  A block claims an item from the phase's counter when it is about to work on it,
-// moves on when none is left, and waits only for items that were claimed before, each by a
-// block that runs and waits for earlier phases at most.  So the grid drains however many of
-// its blocks are resident at a time, beside whatever else the GPU runs.  The counters are
-// cleared by the launch before.
+// Progress.  A block claims gate / up chunks and down items when it is about to work on them,
+// and waits only for items of earlier phases, which it does when all of them are claimed, by
+// blocks that run and wait for still earlier phases at most.  Nothing waits for up rows, which
+// are dealt out in advance.  So the grid drains however many of its blocks are resident at a
+// time, beside whatever else the GPU runs.
+//
+// Counters.  2048 atomic additions to one address take 23 us here (11 ns each, at the memory
+// side, since the XCDs' L2s are not shared), to 32 addresses 1 us: an item counter is 32
+// shards on lines of their own (item 32 j + s is the j-th of shard s, and a claimer whose shard
+// is spent looks for another that has some left), and completion is counted per expert,
+// per row group and over 8 lines.  The launch before clears them.  What one wave hands to
+// another is written through to the memory side (agent-scope stores), waited for, and only
+// then counted; the reader's loads are agent-scope too.  A hand-over takes 0.8 us.
 //
 // The arithmetic of every value is that of the kernels moe_layer_forward runs on a batch of
-// this size (dense_gemv_kernel, route_token, stream_group, the down kernel's fp64 combine),
-// in the same order: the outputs are bit-identical.
+// this size (dense_gemv_kernel, the routing, stream_group, the fp64 combine), in the same
+// order: the outputs are bit-identical.
 #include "mfma_stream.h"
 #include "route_token.h"
 
@@ -27,76 +38,122 @@ namespace moe {
 
 constexpr int DEC_THREADS = 512;
 constexpr int DEC_WAVES = DEC_THREADS / WAVE;
-constexpr int DEC_ROWS = 32;   // FFN rows of a gate / up item: one scale block of the down operand
-constexpr int DEC_GU_PF = 4;   // K steps in flight, of four weight streams a wave
-constexpr int DEC_DN_PF = 8;   // of one or two
-constexpr int DEC_LDS_STATIC = 24 * 1024;  // room for the statically allocated LDS
+constexpr int DEC_GU_PF = 4;   // K steps in flight, of a gate and an up stream
+constexpr int DEC_DN_PF = 8;   // of a down stream
+constexpr int DEC_SLOTS = 2 * DEC_WAVES;  // routed rows of a down item: two a wave
+constexpr int DEC_TILES = 16;  // pairs of gate / up items a block may have open
+constexpr int DEC_SHARDS = 32;
 static_assert(DECODE_MAX_TOKENS <= DEC_WAVES && DECODE_MAX_ROWS <= WAVE, "a wave per token, a lane per routed row");
 
 // a staged activation row: hi codes, lo codes, hi scales, lo scales
 __host__ __device__ constexpr int dec_row_bytes(int K) { return (2 * K + K / 16 + 15) / 16 * 16; }
 __device__ __forceinline__ ALds dec_row(uint8_t* row, int K) { return {row, row + K, row + 2 * K, row + 2 * K + K / 32}; }
 
-// ---- phase counters, a 128-byte line each
-enum { C_GATEUP, C_GATEUP_DONE, C_DOWN, C_DOWN_DONE, C_U, C_U_DONE, C_UP, C_COUNT };
-static_assert(C_COUNT * 32 == DECODE_COUNTERS, "the first launch clears the counters");
+// ---- counters, each on a 128-byte line of its own
+constexpr int DEC_DONE_LINES = 8;
+enum {
+  C_GATEUP = 0,                         // claimed items, by shard
+  C_DOWN = C_GATEUP + DEC_SHARDS,
+  C_U = C_DOWN + DEC_SHARDS,
+  C_EXPERT = C_U + DEC_SHARDS,          // quantised gate / up scale blocks, by expert
+  C_Z = C_EXPERT + DECODE_MAX_ROWS,     // combined row groups
+  C_U_DONE = C_Z + DEC_DONE_LINES,      // finished (token, rank) pairs
+  C_ROWS = C_U_DONE + DEC_DONE_LINES    // finished down items, by row group
+};
+int32_t decode_counters(int32_t L) { return C_ROWS + L / 16; }
+__device__ __forceinline__ int32_t* line(int32_t* ctr, int i) { return ctr + 32 * i; }
 
-__device__ __forceinline__ int claim(int32_t* ctr, int n, int* shared) {
-  __syncthreads();  // the last claim has been read
-  if (threadIdx.x == 0) *shared = __hip_atomic_fetch_add(ctr, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __syncthreads();
-  return *shared;
+template <class V>
+__device__ __forceinline__ void put(V* p, V v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-// the block's stores of n items are in memory before the count says so
-__device__ __forceinline__ void publish(int32_t* ctr, int n) {
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // each wave's own stores have left
-  __syncthreads();
-  if (threadIdx.x == 0 && n > 0) {
-    __threadfence();
-    __hip_atomic_fetch_add(ctr, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
+template <class V>
+__device__ __forceinline__ V get(const V* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ void await(int32_t* ctr, int n) {
-  if (threadIdx.x == 0)
-    while (__hip_atomic_load(ctr, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < n) __builtin_amdgcn_s_sleep(1);
-  __syncthreads();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+__device__ __forceinline__ int add1(int32_t* p) {
+  return __hip_atomic_fetch_add(p, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
+// the wave's stores so far have reached the memory side
+__device__ __forceinline__ void stores_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
   __builtin_amdgcn_wave_barrier();
 }
 
-// stream_group with NS weight streams that share one activation row group (ONE_A) or have one
-// each: acc[q] += A_q W_q^T over all K steps, sb and ring filled by prime_stream
-template <class W, int NS, int PF, bool ONE_A>
-__device__ __forceinline__ void dec_stream(const W (&w)[NS], SBlock (&sb)[NS], uint4 (&ring)[NS][PF],
-                                           const ALds (&ad)[ONE_A ? 1 : NS], bool on, int K, int g, f32x4 (&acc)[NS]) {
+// Claims of one phase's n items by a wave.  take() sends the request for the wave's next item
+// early; item() waits for it and is -1 when no item is left.
+struct Claims {
+  int32_t* ctr;
+  int n, shard, asked;
+  __device__ __forceinline__ Claims(int32_t* base, int n_) : ctr(base), n(n_), shard(blockIdx.x % DEC_SHARDS), asked(0) {}
+  __device__ __forceinline__ void take() {
+    if (lane_id() == 0) asked = add1(line(ctr, shard));
+  }
+  __device__ __forceinline__ int item() {
+    for (;;) {
+      const int i = DEC_SHARDS * __builtin_amdgcn_readfirstlane(asked) + shard;
+      if (i < n) return i;
+      const int lane = lane_id();
+      const int at = lane < DEC_SHARDS ? (lane + shard) % DEC_SHARDS : 0;
+      const int used = lane < DEC_SHARDS ? get(line(ctr, at)) : n;
+      const unsigned long long left = __ballot(lane < DEC_SHARDS && DEC_SHARDS * used + at < n);
+      if (!left) return -1;
+      shard = (__ffsll((long long)left) - 1 + shard) % DEC_SHARDS;
+      take();
+    }
+  }
+};
+
+// stream_group with NS weight streams on one activation row group: acc[q] += A W_q^T over all K
+// steps, sb and ring filled by prime_stream.  With `chain` the ring goes on with the first
+// steps of wn as w's loads end, and wn's scales are in sb after, as prime_stream would leave
+// them (K / 128 a multiple of PF, so that the ring's slots fit).  Records take two steps'
+// loads at a time: a row of one gives 64 bytes a step, so two side by side read whole
+// 128-byte lines.
+template <class W, int NS, int PF>
+__device__ __forceinline__ void dec_stream(const W (&w)[NS], const W (&wn)[NS], bool chain, SBlock (&sb)[NS],
+                                           uint4 (&ring)[NS][PF], const ALds& ad, bool on, int K, int g,
+                                           f32x4 (&acc)[NS]) {
+  constexpr int SIDE = std::is_same<W, RecordW>::value ? 2 : 1;
   const int nks = K / 128, nc = (nks + 15) / 16;
   SBlock sbn[NS];
   for (int c = 0; c < nc; ++c) {
 #pragma unroll
-    for (int q = 0; q < NS; ++q) w[q].sblock(sbn[q], c + 1 < nc ? c + 1 : c);
-    unroll16([&](auto jc) {
-      constexpr int J = decltype(jc)::value;
-      const int ks = 16 * c + J;
-      uint4 cw[NS];
+    for (int q = 0; q < NS; ++q) {
+      const bool next = chain && c + 1 == nc;
+      (next ? wn[q] : w[q]).sblock(sbn[q], next ? 0 : c + 1 < nc ? c + 1 : c);
+    }
+    unroll_n<16 / SIDE>([&](auto jc) {
+      constexpr int J2 = SIDE * decltype(jc)::value;
+      const int ks2 = 16 * c + J2;
+      uint4 cw[SIDE][NS];
 #pragma unroll
-      for (int q = 0; q < NS; ++q) {
-        cw[q] = ring[q][J % PF];
-        ring[q][J % PF] = w[q].load(ks + PF < nks ? ks + PF : nks - 1);
-      }
-      if (ks < nks) {
-        AStep a;
+      for (int q = 0; q < NS; ++q)
 #pragma unroll
-        for (int q = 0; q < NS; ++q) {
-          if (!ONE_A || q == 0) read_a(a, ad[ONE_A ? 0 : q], on ? 0 : 1, 1, K, ks, g);
-          const uint32_t sw = w[q].template scale<J>(sb[q]);
-          const i32x8 b = as_b(cw[q]);
-          acc[q] = mx_mfma<W::opsel(J)>(a.hi, b, acc[q], a.shi, sw);
-          acc[q] = mx_mfma<W::opsel(J)>(a.lo, b, acc[q], a.slo, sw);
+        for (int h = 0; h < SIDE; ++h) {
+          cw[h][q] = ring[q][(J2 + h) % PF];
+          // every step loads, on every path (see prime_stream): past w's steps, those of wn
+          // that the ring's slot is for, or w's last again
+          const int at = ks2 + h + PF;
+          const bool next = chain && at >= nks;
+          ring[q][(J2 + h) % PF] = (next ? wn[q] : w[q]).load(next ? (at - nks) % PF : at < nks ? at : nks - 1);
         }
-      }
+      unroll_n<SIDE>([&](auto hc) {
+        constexpr int H = decltype(hc)::value, J = J2 + H;
+        const int ks = ks2 + H;
+        if (ks < nks) {
+          AStep a;
+          read_a(a, ad, on ? 0 : 1, 1, K, ks, g);
+#pragma unroll
+          for (int q = 0; q < NS; ++q) {
+            const uint32_t sw = w[q].template scale<J>(sb[q]);
+            const i32x8 b = as_b(cw[H][q]);
+            acc[q] = mx_mfma<W::opsel(J)>(a.hi, b, acc[q], a.shi, sw);
+            acc[q] = mx_mfma<W::opsel(J)>(a.lo, b, acc[q], a.slo, sw);
+          }
+        }
+      });
     });
 #pragma unroll
     for (int q = 0; q < NS; ++q) sb[q] = sbn[q];
@@ -105,60 +162,272 @@ __device__ __forceinline__ void dec_stream(const W (&w)[NS], SBlock (&sb)[NS], u
 
 struct DecodeLds {
   union {
-    RouteLds route[DEC_WAVES];
-    float atile[DEC_WAVES][DECODE_MAX_TOKENS][DEC_ROWS + 1];  // an item's GLU outputs, a wave's own
-    float ys[DECODE_MAX_ROWS][16];                            // an item's expert outputs by slot
+    RouteLds route[DECODE_MAX_TOKENS];  // candidates and output of a token
+    struct {
+      uint16_t tile[DEC_TILES][DECODE_MAX_TOKENS][34];  // GLU outputs of a pair of items
+      float ys[2][DEC_SLOTS][16];                       // expert outputs of a down item, by slot
+    };
   };
+  uint32_t gmax[DEC_WAVES][WAVE];
+  int wcnt[DEC_WAVES][16];
+  float wup[DEC_WAVES];
+  uint8_t crank[DECODE_MAX_TOKENS][ROUTE_CAND];
+  uint32_t redo;               // tokens whose selection the block could not decide
+  // the routing
   int sel[DECODE_MAX_ROWS];    // expert of slot t k + j
   float w[DECODE_MAX_ROWS];    // its weight
-  int gexp[DECODE_MAX_ROWS];   // distinct experts, and the slots of each
+  int sgrp[DECODE_MAX_ROWS];   // its group: the distinct experts, and the slots of each
+  int gexp[DECODE_MAX_ROWS];
   int gn[DECODE_MAX_ROWS];
-  int gslot[DECODE_MAX_ROWS][DECODE_MAX_TOKENS];
+  uint8_t gslot[DECODE_MAX_ROWS][DECODE_MAX_TOKENS];
   int ng;
-  int claimed;
+  // the block's gate / up chunk: (sequence << 16 | chunk) << 32 | items taken of it
+  unsigned long long chunk;
+  int tile_of[DEC_TILES], tile_n[DEC_TILES];  // the pair a tile is for, items of it there
+  int ditem[2];
 };
-static_assert(sizeof(DecodeLds) <= DEC_LDS_STATIC, "static LDS");
+constexpr uint32_t DEC_NO_CHUNK = 0xFFFFFFFFu;
+constexpr size_t DEC_LDS = (160 * 1024 - sizeof(DecodeLds)) / 1024 * 1024;  // what is left for the launch to size
 
-// Routing of all tokens into S, and h quantised into hq, by the whole block; the first block
-// also writes what the caller asked for.
-__device__ __forceinline__ void dec_route(const DecodeArgs& p, DecodeLds& S, uint8_t* hq) {
-  const int tid = threadIdx.x, lane = lane_id(), wave = tid / WAVE;
-  const int T = (int)p.r.T, k = p.r.k, E = p.r.E, L = p.r.L, n = T * k;
-  const bool writer = blockIdx.x == 0;
-  RouteArgs a = p.r;
-  a.idx = S.sel;
-  a.w = S.w;
-  if (!writer) a.logits_out = nullptr;
-  if (wave < T) route_token(a, wave, &S.route[wave]);
-  // the waves that route nothing quantise meanwhile
-  const int q0 = T < DEC_WAVES ? T : 0;
-  if (wave >= q0)
-    for (int t = 0; t < T; ++t) {
-      const ALds r = dec_row(hq + t * dec_row_bytes(L), L);
-      quantize_quads(a.h + (int64_t)t * L, QRows{r.hi, r.lo, r.shi, r.slo}, L, tid - q0 * WAVE,
-                     DEC_THREADS - q0 * WAVE, a.mxfp8 != 0);
+// route_token as a call: its registers are not reserved in the kernel, where it runs only
+// when the block's own selection cannot decide
+__attribute__((noinline)) __device__ void dec_route_alone(RouteArgs a, int64_t t, RouteLds* L) { route_token(a, t, L); }
+
+// Routing of all tokens at once, W = 16 / EPT waves a token and EPT experts a lane: the values,
+// cut, certification and output of route_token's fast path (see there).  What it cannot
+// decide is left to route_token (S.redo).  load() brings a token's logits, select() works on
+// them; every wave of the block calls both.
+template <int EPT>
+struct RouteBlock {
+  static constexpr int W = 16 / EPT;
+  float lf[EPT], bv[EPT], wn[EPT], xn;
+
+  __device__ __forceinline__ static int expert(int i) { return (i * W + (threadIdx.x / WAVE) % W) * WAVE + lane_id(); }
+  __device__ __forceinline__ void load(const RouteArgs& a) {
+    const int t = min((int)threadIdx.x / WAVE / W, (int)a.T - 1);
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+      const int e = min(expert(i), a.E - 1);
+      lf[i] = a.logits_fast[(int64_t)t * a.E + e];
+      bv[i] = a.bias ? a.bias[t * a.bias_stride + e] : 0.f;
+      wn[i] = a.wnorm[e];
     }
-  __syncthreads();
-  if (wave == 0) {  // a lane per slot: the first slot of an expert leads its group
-    const int e = lane < n ? S.sel[lane] : -1;
-    unsigned long long mine = 0;
-    for (int s = 0; s < n; ++s) {
-      const unsigned long long m = __ballot(e == __builtin_amdgcn_readlane(e, s));
-      if (e >= 0 && (m >> lane) & 1ull) mine = m;
-    }
-    const unsigned long long below = (1ull << lane) - 1ull;
-    const bool lead = e >= 0 && (mine & below) == 0ull;
-    const unsigned long long leads = __ballot(lead);
-    if (e >= 0) {
-      const int first = __ffsll((long long)mine) - 1;
-      const int grp = __popcll(leads & ((1ull << first) - 1ull));
-      S.gslot[grp][__popcll(mine & below)] = lane;
-      if (lead) {
-        S.gexp[grp] = e;
-        S.gn[grp] = __popcll(mine);
+    xn = a.xnorm[t];
+  }
+  __device__ __forceinline__ void arrived() const {  // the loads above have come
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) asm volatile("" ::"v"(lf[i]), "v"(bv[i]), "v"(wn[i]));
+    asm volatile("" ::"v"(xn));
+  }
+  __device__ __forceinline__ void select(const RouteArgs& a, DecodeLds& S) const {
+    const int lane = lane_id(), wave = threadIdx.x / WAVE, t = wave / W, sub = wave % W;
+    const int E = a.E, k = a.k;
+    const bool token = t < a.T;
+    RouteLds& L = S.route[token ? t : 0];
+    const float gam = (float)a.gamma * (1.f + 0x1p-18f) * xn;
+    const float pad = (float)a.d * 0x1p-124f;
+    float c[EPT], R[EPT];
+    uint32_t key[EPT], kmax = 0u;
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+      c[i] = -__builtin_inff();
+      R[i] = 0.f;
+      key[i] = 0u;
+      if (expert(i) < E) {
+        c[i] = lf[i] + bv[i];
+        R[i] = gam * wn[i] + pad + 0x1p-20f * (fabsf(lf[i]) + fabsf(bv[i]));
+        if (bv[i] == -__builtin_inff()) {
+          const float rr = gam * wn[i] + pad + 0x1p-20f * fabsf(lf[i]);
+          const bool known = __builtin_isfinite(lf[i]) && __builtin_isfinite(rr) && fabsf(lf[i]) + rr < 0x1p127f;
+          c[i] = -__builtin_inff();
+          R[i] = known ? 0.f : __builtin_inff();
+        } else if (!(__builtin_isfinite(c[i]) && __builtin_isfinite(R[i]))) {
+          c[i] = -__builtin_inff();
+          R[i] = __builtin_inff();
+        }
+        key[i] = order_key(c[i]);
+        kmax = max(kmax, key[i]);
       }
     }
-    if (lane == 0) S.ng = __popcll(leads);
+    S.gmax[wave][lane] = kmax;
+    lds_barrier();
+    // the cut: the k-th largest of the maxima of 64 groups (experts equal mod 64)
+    uint32_t gm = 0u;
+#pragma unroll
+    for (int v = 0; v < W; ++v) gm = max(gm, S.gmax[wave - sub + v][lane]);
+    const uint32_t tau = kth_of_lanes(gm, k);
+    unsigned long long cb[EPT];
+    float up = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+      const bool cand = key[i] != 0u && key[i] >= tau;
+      cb[i] = __ballot(cand);
+      if (key[i] != 0u && !cand) up = fmaxf(up, R[i] == __builtin_inff() ? __builtin_inff() : next_up(c[i] + R[i]));
+      if (lane == 0) S.wcnt[wave - sub][i * W + sub] = __popcll(cb[i]);
+    }
+    up = wave_max_dpp(up);
+    if (lane == 0) S.wup[wave] = up;
+    lds_barrier();
+    int base[EPT], n_c = 0;
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      const int n = S.wcnt[wave - sub][v];
+      if (v % W == sub) base[v / W] = n_c;
+      n_c += n;
+    }
+    const bool fits = n_c <= ROUTE_CAND;
+    if (token && fits)
+#pragma unroll
+      for (int i = 0; i < EPT; ++i)
+        if ((cb[i] >> lane) & 1ull) {
+          const int pos = base[i] + __popcll(cb[i] & ((1ull << lane) - 1ull));
+          L.ckey[pos] = key[i];
+          L.cidx[pos] = expert(i);
+          L.cval[pos] = c[i];
+          L.crad[pos] = R[i];
+        }
+    lds_barrier();
+    if (token && fits) {  // a candidate's rank: those ahead of it are counted
+      constexpr int PER = ROUTE_CAND / W;
+      const bool live = lane < n_c;
+      const uint32_t mk = live ? L.ckey[lane] : 0u;
+      const int me = live ? L.cidx[lane] : 0x7FFFFFFF;
+      for (int i = PER * sub; i < min(PER * sub + PER, n_c); ++i) {
+        const uint32_t ki = (uint32_t)__builtin_amdgcn_readlane((int)mk, i);
+        const int ei = __builtin_amdgcn_readlane(me, i);
+        const int r = __popcll(__ballot(live && (mk > ki || (mk == ki && me < ei))));
+        if (lane == 0) S.crank[t][i] = (uint8_t)r;
+      }
+    }
+    lds_barrier();
+    if (token && sub == 0) {
+      bool fast = fits && a.renormalize && !(a.flags & MOE_ROUTE_EXACT_ALL);
+      const bool live = fast && lane < n_c;
+      const bool sel = live && S.crank[t][lane] < k;
+      const float mc = live ? L.cval[lane] : 0.f, mr = live ? L.crad[lane] : 0.f;
+      if (fast && k < E) {
+        float Mloc = __builtin_inff(), mloc = -__builtin_inff();
+        if (sel) Mloc = mr == __builtin_inff() ? -__builtin_inff() : next_down(mc - mr);
+        if (live && !sel) mloc = mr == __builtin_inff() ? __builtin_inff() : next_up(mc + mr);
+        if (lane < W) mloc = fmaxf(mloc, S.wup[wave + lane]);
+        fast = wave_min_dpp(Mloc) > wave_max_dpp(mloc);
+      }
+      if (fast) {
+        // candidates are in expert order, so the output place is the count of selected below
+        const int op = __popcll(__ballot(sel) & ((1ull << lane) - 1ull));
+        if (sel) {
+          L.oidx[op] = L.cidx[lane];
+          L.oval[op] = mc;
+        }
+        wave_sync();
+        emit_topk(a, t, &L, 0.f, 1.f);
+      } else if (lane == 0) {
+        atomicOr(&S.redo, 1u << t);
+      }
+    }
+    if (token && a.logits_out) {  // a redo overwrites what it recomputes
+#pragma unroll
+      for (int i = 0; i < EPT; ++i)
+        if (expert(i) < E) a.logits_out[(int64_t)t * E + expert(i)] = c[i];
+    }
+  }
+};
+
+// Routing of all tokens into S, and h quantised into hq, by the whole block; the first block
+// also writes what the caller asked for.  ahead() starts loads that the routing hides: it
+// runs when nothing the routing needs is on its way any more.
+template <int EPT, class Fn>
+__device__ __forceinline__ void dec_route(const DecodeArgs& p, const RouteArgs& a, DecodeLds& S, uint8_t* hq,
+                                          Fn&& ahead) {
+  const int tid = threadIdx.x;
+  const int T = (int)a.T, L = a.L;
+  RouteBlock<EPT> rb;
+  rb.load(a);
+  constexpr int U = 4;  // groups of eight latent values a thread has in flight
+  const int per = L / 8, groups = T * per;
+  uint4 raw[U];
+  auto load_h = [&](int j0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + DEC_THREADS * u;
+      if (DEC_THREADS * u < groups) raw[u] = *reinterpret_cast<const uint4*>(a.h + 8 * (int64_t)(j < groups ? j : 0));
+    }
+  };
+  load_h(tid);
+  for (int j0 = tid; j0 < groups; j0 += DEC_THREADS * U) {
+    if (j0 != tid) load_h(j0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + DEC_THREADS * u;
+      if (j < groups) {  // the four groups of a scale block are a quad of lanes
+        const int t = j / per, jj = j - t * per;
+        const ALds r = dec_row(hq + t * dec_row_bytes(L), L);
+        const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[2 * i] = bf16lo(w[i]);
+          v[2 * i + 1] = bf16hi(w[i]);
+        }
+        uint32_t hi[2], lo[2], shi, slo;
+        quantize_quad8_fmt(v, hi, lo, shi, slo, a.mxfp8 != 0);
+        *reinterpret_cast<uint2*>(r.hi + 8 * jj) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(r.lo + 8 * jj) = make_uint2(lo[0], lo[1]);
+        if ((jj & 3) == 0) {
+          r.shi[jj >> 2] = (uint8_t)shi;
+          r.slo[jj >> 2] = (uint8_t)slo;
+        }
+      }
+    }
+  }
+  // a wait for older loads would wait for the ones ahead() starts: take them first
+  rb.arrived();
+  ahead();
+  rb.select(a, S);
+}
+
+// the selection's groups, the caller's routing outputs and the first gate / up chunk
+__device__ __forceinline__ void dec_group(const DecodeArgs& p, const RouteArgs& a, DecodeLds& S) {
+  const int tid = threadIdx.x, lane = lane_id(), wave = tid / WAVE;
+  const int T = (int)a.T, k = a.k, n = T * k;
+  const bool writer = blockIdx.x == 0;
+  lds_barrier();  // loads that ahead() started stay in flight
+  const uint32_t redo = S.redo;
+  if (redo) {
+    if (wave < T && (redo >> wave) & 1u) dec_route_alone(a, wave, &S.route[wave]);
+    __syncthreads();
+  }
+  if (wave == 0) {
+    const int e = lane < n ? S.sel[lane] : -1;
+    if (T == 1) {  // a token's experts are distinct
+      if (lane < n) {
+        S.sgrp[lane] = lane;
+        S.gexp[lane] = e;
+        S.gn[lane] = 1;
+        S.gslot[lane][0] = (uint8_t)lane;
+      }
+      if (lane == 0) S.ng = n;
+    } else {  // a lane per slot: the first slot of an expert leads its group
+      unsigned long long mine = 0;
+      for (int s = 0; s < n; ++s) {
+        const unsigned long long m = __ballot(e == __builtin_amdgcn_readlane(e, s));
+        if (e >= 0 && (m >> lane) & 1ull) mine = m;
+      }
+      const unsigned long long below = (1ull << lane) - 1ull;
+      const bool lead = e >= 0 && (mine & below) == 0ull;
+      const unsigned long long leads = __ballot(lead);
+      if (e >= 0) {
+        const int first = __ffsll((long long)mine) - 1;
+        const int grp = __popcll(leads & ((1ull << first) - 1ull));
+        S.sgrp[lane] = grp;
+        S.gslot[grp][__popcll(mine & below)] = (uint8_t)lane;
+        if (lead) {
+          S.gexp[grp] = e;
+          S.gn[grp] = __popcll(mine);
+        }
+      }
+      if (lane == 0) S.ng = __popcll(leads);
+    }
     if (writer && lane < n) {
       if (p.idx) p.idx[lane] = e;
       if (p.w) p.w[lane] = S.w[lane];
@@ -168,242 +437,388 @@ __device__ __forceinline__ void dec_route(const DecodeArgs& p, DecodeLds& S, uin
         p.perm[at] = lane;
       }
     }
+  } else if (wave == 1 && lane < DEC_TILES) {
+    S.tile_of[lane] = lane;
+    S.tile_n[lane] = 0;
   }
   if (writer && (p.counts || p.offsets))
-    for (int e = tid; e <= E; e += DEC_THREADS) {
+    for (int e = tid; e <= a.E; e += DEC_THREADS) {
       int below = 0, same = 0;
       for (int s = 0; s < n; ++s) {
         below += S.sel[s] < e;
         same += S.sel[s] == e;
       }
-      if (p.counts && e < E) p.counts[e] = same;
+      if (p.counts && e < a.E) p.counts[e] = same;
       if (p.offsets) p.offsets[e] = below;
     }
-  __syncthreads();
 }
 
-// NS: routed rows a wave takes through the down matrices side by side.  UC chunks of 512
-// latent columns of UR output rows are a wave's share of an up item.
-template <class W, int NS, int UC, int UR>
+// ranks of token t's adapter in use, and its id
+__device__ __forceinline__ int dec_rank(const LoraSeg& l, int t, int& a) {
+  a = l.adapter[t];
+  if ((uint32_t)a >= (uint32_t)l.N) return 0;
+  return l.rank ? min(l.rank[a], l.R) : l.R;
+}
+
+// UC chunks of 512 latent columns cover an up row; a wave holds UA of them through the down
+// phase.
+template <class W, int UC, int UA>
 __global__ void __launch_bounds__(DEC_THREADS) decode_kernel(DecodeArgs p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ DecodeLds S;
-  const int tid = threadIdx.x, lane = lane_id(), wave = tid / WAVE;
+  const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
   const int nl = lane & 15, g = lane >> 4;
-  const int T = (int)p.r.T, k = p.r.k, L = p.r.L, F = p.F, d = p.r.d, n = T * k;
-  const int arow = dec_row_bytes(F);
+  const int T = (int)p.r.T, k = p.r.k, L = p.r.L, F = p.F, d = p.r.d;
+  const int hrow = dec_row_bytes(L), arow = dec_row_bytes(F);
+  uint8_t* stage = smem + p.stage_offset + wave * arow;
 
-  dec_route(p, S, smem);
-  const int ng = S.ng;
+  // the block's up rows: the first slab_rows wait in the LDS, the others are taken by the
+  // waves in turn
+  const int up0 = min(d, (int)blockIdx.x * p.up_rows), up1 = min(d, up0 + p.up_rows);
+  const int slab1 = min(up1, up0 + p.slab_rows);
+  uint16_t* slab = reinterpret_cast<uint16_t*>(smem + p.slab_offset);
+
+  // ---- routing; the first claims are on their way meanwhile (wave 0's)
+  Claims chunks(line(p.ctr, C_GATEUP), 0), downs(line(p.ctr, C_DOWN), 0);
+  if (wave == 0) {
+    chunks.take();
+    downs.take();
+  }
+  RouteArgs ra = p.r;
+  ra.idx = S.sel;
+  ra.w = S.w;
+  if (blockIdx.x != 0) ra.logits_out = nullptr;
+  if (tid == 0) S.redo = 0u;  // read behind barriers
+  auto ahead = [&]() {
+    const int bytes = (slab1 - up0) * L * 2;
+    for (int i = 1024 * wave; i < bytes; i += 1024 * DEC_WAVES)
+      if (i + 16 * lane < bytes)
+        lds_dma16(reinterpret_cast<const uint8_t*>(p.latent_up + (int64_t)up0 * L) + i + 16 * lane,
+                  reinterpret_cast<const uint8_t*>(slab) + i);
+  };
+  if (T == 1) dec_route<2>(p, ra, S, smem, ahead);
+  else if (T == 2) dec_route<4>(p, ra, S, smem, ahead);
+  else if (T <= 4) dec_route<8>(p, ra, S, smem, ahead);
+  else dec_route<16>(p, ra, S, smem, ahead);
+  dec_group(p, ra, S);
+  // chunks of consecutive pairs, about half as many items as waves or as many: a CU's waves
+  // then read one stretch of memory
+  if (wave == 0) wave_sync();
+  lds_barrier();
+  const int ng = S.ng, nrb = F / 32, pairs = ng * nrb;
+  const int rounds = max(1, (int)ceil_div(pairs, (int64_t)gridDim.x * (DEC_WAVES / 2)));
+  const int cp = (int)ceil_div(pairs, (int64_t)gridDim.x * rounds);
+  chunks.n = (pairs + cp - 1) / cp;
+  const int nrg = L / 16, nsc = (T * k + DEC_SLOTS - 1) / DEC_SLOTS;
+  downs.n = nrg * nsc;
+  if (wave == 0) {
+    const int c = chunks.item(), dn = downs.item();
+    if (lane == 0) {
+      S.chunk = (unsigned long long)(c < 0 ? DEC_NO_CHUNK : (uint32_t)c) << 32;
+      S.ditem[0] = dn;
+    }
+  }
+  lds_barrier();
 
   // ---- gate / up
-  const int nrb = F / DEC_ROWS, n1 = ng * nrb;
-  {
-    const int chunk = max(1, min(DEC_WAVES, (n1 + (int)gridDim.x - 1) / (int)gridDim.x));
-    int mine = 0;
+  struct Half {
+    int pair, seq, h;  // pair of the phase, of the block; which of its two items
+  };
+  auto next_half = [&](Half& x) -> bool {
     for (;;) {
-      const int c = claim(p.ctr + 32 * C_GATEUP, chunk, &S.claimed);
-      if (c >= n1) break;
-      mine += min(chunk, n1 - c);
-      const int item = c + wave;
-      if (wave < chunk && item < n1) {
-        const int grp = item / nrb, rb = item - grp * nrb, e = S.gexp[grp], nt = S.gn[grp];
-        const W w[4] = {W::make(p.blob, e, L, F, MAT_GATE, 2 * rb, lane), W::make(p.blob, e, L, F, MAT_GATE, 2 * rb + 1, lane),
-                        W::make(p.blob, e, L, F, MAT_UP, 2 * rb, lane), W::make(p.blob, e, L, F, MAT_UP, 2 * rb + 1, lane)};
-        SBlock sb[4];
-        uint4 ring[4][DEC_GU_PF];
-        prime_stream<W, 4, DEC_GU_PF>(w, sb, ring, L / 128);
-        const bool on = nl < nt;
-        const ALds ad[1] = {dec_row(smem + (on ? S.gslot[grp][nl] / k : 0) * dec_row_bytes(L), L)};
-        f32x4 acc[4];
+      unsigned long long v = 0;
+      if (lane == 0) v = atomicAdd(&S.chunk, 1ull);
+      const uint32_t id = (uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32));
+      const int at = __builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+      if (id == DEC_NO_CHUNK) return false;
+      if (at < 2 * cp) {
+        x.pair = (int)(id & 0xFFFFu) * cp + at / 2;
+        x.seq = (int)(id >> 16) * cp + at / 2;
+        x.h = at & 1;
+        if (x.pair < pairs) return true;
+      } else if (at == 2 * cp) {  // the wave that finds it spent brings the next
+        chunks.take();
+        const int c = chunks.item();
+        const uint32_t nid = c < 0 ? DEC_NO_CHUNK : ((id >> 16) + 1) << 16 | (uint32_t)c;
+        if (lane == 0)
+          __hip_atomic_store(&S.chunk, (unsigned long long)nid << 32, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+      } else {
+        __builtin_amdgcn_s_sleep(1);
+      }
+    }
+  };
+  {
+    W w[2], wn[2];
+    SBlock sb[2];
+    uint4 ring[2][DEC_GU_PF];
+    const bool fit = (L / 128) % DEC_GU_PF == 0;
+    auto make = [&](W(&m)[2], const Half& x) {
+      const int grp = x.pair / nrb, r = 2 * (x.pair - grp * nrb) + x.h, e = __builtin_amdgcn_readfirstlane(S.gexp[grp]);
+      m[0] = W::make(p.blob, e, L, F, MAT_GATE, r, lane);
+      m[1] = W::make(p.blob, e, L, F, MAT_UP, r, lane);
+    };
+    Half x, y;
+    bool more = next_half(x);
+    if (more) {
+      make(w, x);
+      prime_stream<W, 2, DEC_GU_PF>(w, sb, ring, L / 128);
+    }
+    while (more) {
+      const int grp = x.pair / nrb, rb = x.pair - grp * nrb, nt = __builtin_amdgcn_readfirstlane(S.gn[grp]);
+      const bool again = next_half(y);
+      if (again) make(wn, y);
+      else {
+        wn[0] = w[0];
+        wn[1] = w[1];
+      }
+      const bool on = nl < nt;
+      f32x4 acc[2];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
-        dec_stream<W, 4, DEC_GU_PF, true>(w, sb, ring, ad, on, L, g, acc);
-        // lane: rows 16 h + nl of the item, tokens 4 g + j of the expert
-        float(*at)[DEC_ROWS + 1] = S.atile[wave];
+      for (int q = 0; q < 2; ++q) acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+      dec_stream<W, 2, DEC_GU_PF>(w, wn, again && fit, sb, ring,
+                                  dec_row(smem + (on ? S.gslot[grp][nl] / k : 0) * hrow, L), on, L, g, acc);
+      if (again && !fit) prime_stream<W, 2, DEC_GU_PF>(wn, sb, ring, L / 128);
+      // lane: row nl of the item, tokens 4 g + j of the expert
+      const int ti = x.seq % DEC_TILES;
+      while (__hip_atomic_load(&S.tile_of[ti], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) != x.seq)
+        __builtin_amdgcn_s_sleep(1);  // a pair of the block's 16 before this one is still open
+      uint16_t(*at)[34] = S.tile[ti];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (4 * g + j < nt) at[4 * g + j][16 * h + nl] = bf16f(glu_bf16(acc[h][j], acc[2 + h][j]));
+      for (int j = 0; j < 4; ++j)
+        if (4 * g + j < nt) at[4 * g + j][16 * x.h + nl] = glu_bf16(acc[0][j], acc[1][j]);
+      wave_sync();
+      int there = 0;
+      if (lane == 0) there = atomicAdd(&S.tile_n[ti], 1);
+      if (__builtin_amdgcn_readfirstlane(there) == 1) {
         wave_sync();
-        // a quad of lanes per token, eight of the block's 32 values each
+        // the pair is whole: a quad of lanes per token, eight of its 32 values each
         const int m = lane >> 2, sub = lane & 3;
         float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = m < nt ? at[m][8 * sub + i] : 0.f;
+        for (int i = 0; i < 8; ++i) v[i] = m < nt ? bf16f(at[m][8 * sub + i]) : 0.f;
         uint32_t hi[2], lo[2], shi, slo;
         quantize_quad8_fmt(v, hi, lo, shi, slo, p.r.mxfp8 != 0);
         if (m < nt) {
           const ALds o = dec_row(p.aq + (int64_t)S.gslot[grp][m] * arow, F);
-          *reinterpret_cast<uint2*>(o.hi + DEC_ROWS * rb + 8 * sub) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2*>(o.lo + DEC_ROWS * rb + 8 * sub) = make_uint2(lo[0], lo[1]);
+          put(reinterpret_cast<unsigned long long*>(o.hi + 32 * rb + 8 * sub), (unsigned long long)hi[1] << 32 | hi[0]);
+          put(reinterpret_cast<unsigned long long*>(o.lo + 32 * rb + 8 * sub), (unsigned long long)lo[1] << 32 | lo[0]);
           if (sub == 0) {
-            o.shi[rb] = (uint8_t)shi;
-            o.slo[rb] = (uint8_t)slo;
+            put(o.shi + rb, (uint8_t)shi);
+            put(o.slo + rb, (uint8_t)slo);
           }
         }
-      }
-    }
-    publish(p.ctr + 32 * C_GATEUP_DONE, mine);
-  }
-
-  // ---- down and combine: item = 16 latent rows of every routed row
-  const int n2 = L / 16;
-  {
-    uint8_t* rows = smem + wave * NS * arow;
-    bool ready = false;
-    int mine = 0;
-    for (;;) {
-      const int c = claim(p.ctr + 32 * C_DOWN, 1, &S.claimed);
-      if (c >= n2) break;
-      ++mine;
-      int s0 = wave * NS;
-      W w[NS];
-      SBlock sb[NS];
-      uint4 ring[NS][DEC_DN_PF];
-      auto prime = [&]() {
-#pragma unroll
-        for (int q = 0; q < NS; ++q)
-          w[q] = W::make(p.blob, S.sel[min(s0 + q, n - 1)], L, F, MAT_DOWN, c, lane);
-        prime_stream<W, NS, DEC_DN_PF>(w, sb, ring, F / 128);
-      };
-      if (s0 < n) prime();
-      if (!ready) await(p.ctr + 32 * C_GATEUP_DONE, n1);
-      ready = true;
-      while (s0 < n) {
-        ALds ad[NS];
-#pragma unroll
-        for (int q = 0; q < NS; ++q) {
-          ad[q] = dec_row(rows + q * arow, F);
-          const uint8_t* src = p.aq + (int64_t)min(s0 + q, n - 1) * arow;
-          for (int i = 16 * lane; i < arow; i += 16 * WAVE)
-            *reinterpret_cast<uint4*>(rows + q * arow + i) = *reinterpret_cast<const uint4*>(src + i);
+        wave_sync();
+        if (lane == 0) {  // the tile is the 16th next pair's
+          S.tile_n[ti] = 0;
+          __hip_atomic_store(&S.tile_of[ti], x.seq + DEC_TILES, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
         }
-        wave_sync();
-        f32x4 acc[NS];
-#pragma unroll
-        for (int q = 0; q < NS; ++q) acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
-        dec_stream<W, NS, DEC_DN_PF, false>(w, sb, ring, ad, nl == 0, F, g, acc);
-#pragma unroll
-        for (int q = 0; q < NS; ++q)
-          if (g == 0 && s0 + q < n) S.ys[s0 + q][nl] = acc[q][0];
-        wave_sync();
-        s0 += DEC_WAVES * NS;
-        if (s0 < n) prime();
+        stores_done();
+        if (lane == 0) add1(line(p.ctr, C_EXPERT + grp));
       }
-      __syncthreads();
-      for (int q = tid; q < T * 16; q += DEC_THREADS) {
-        const int t = q >> 4, r = q & 15;
-        double acc = 0.0;
-        for (int j = 0; j < k; ++j) acc += (double)S.w[t * k + j] * (double)S.ys[t * k + j][r];
-        p.z[(int64_t)t * L + c * 16 + r] = f64_to_bf16(acc);
-      }
+      more = again;
+      x = y;
+      w[0] = wn[0];
+      w[1] = wn[1];
     }
-    publish(p.ctr + 32 * C_DOWN_DONE, mine);
   }
+  if (p.stage_offset == 0) __syncthreads();  // the staged rows take the place of h
 
-  // ---- up (with the adapters' two products)
-  uint16_t* zs = reinterpret_cast<uint16_t*>(smem);
-  bool ready = false;
-  auto stage_z = [&]() {  // every block that reads z holds all of it
-    await(p.ctr + 32 * C_DOWN_DONE, n2);
-    for (int i = tid; i < T * L / 8; i += DEC_THREADS)
-      *reinterpret_cast<uint4*>(zs + 8 * i) = *reinterpret_cast<const uint4*>(p.z + 8 * i);
-    __syncthreads();
-    ready = true;
+  // ---- down and combine
+  uint4 wr[UA][UC];
+  auto load_up = [&](int row, int r) {  // row of the matrix into wr[r]
+    row = max(0, min(row, up1 - 1));
+#pragma unroll
+    for (int q = 0; q < UC; ++q) {
+      const int col = 8 * (WAVE * q + lane);
+      wr[r][q] = load_nt16(p.latent_up + (int64_t)row * L + (col < L ? col : 0));
+    }
   };
-  const bool lora = p.lora.B != nullptr;
-  const int nu = T * p.lora.R;
-  if (lora) {
-    int mine = 0;
-    for (;;) {  // item = a (token, rank) pair per wave
-      const int c = claim(p.ctr + 32 * C_U, DEC_WAVES, &S.claimed);
-      if (c >= nu) break;
-      mine += min(DEC_WAVES, nu - c);
-      if (!ready) stage_z();
-      const int i = c + wave;
-      if (i < nu) {
-        const int t = i / p.lora.R, r = i - t * p.lora.R, a = p.lora.adapter[t];
-        const bool have = (uint32_t)a < (uint32_t)p.lora.N;
-        const int rk = !have ? 0 : p.lora.rank ? min(p.lora.rank[a], p.lora.R) : p.lora.R;
-        float v = 0.f;
-        if (r < rk) {
-          const uint16_t* A = p.lora_a + ((int64_t)a * p.lora.R + r) * L;
-          double acc = 0.0;
-          for (int col = 8 * lane; col < L; col += 8 * WAVE) {
-            const uint4 x = *reinterpret_cast<const uint4*>(zs + t * L + col);
-            const uint4 av = *reinterpret_cast<const uint4*>(A + col);
-            float q = dot2(x.x, av.x, 0.f);
-            q = dot2(x.y, av.y, q);
-            q = dot2(x.z, av.z, q);
-            q = dot2(x.w, av.w, q);
-            acc += (double)q;
+  {
+    const int n = T * k;
+    W w[1], wn[1];
+    SBlock sb[1];
+    uint4 ring[1][DEC_DN_PF];
+    const bool fit = (F / 128) % DEC_DN_PF == 0;
+    int ditem = S.ditem[0], par = 0;
+    bool first = true;
+    for (;;) {
+      const int sc = ditem < 0 ? 0 : ditem / nrg, rg = ditem < 0 ? 0 : ditem - sc * nrg;
+      int s = DEC_SLOTS * sc + wave;
+      const bool mine = ditem >= 0 && s < n;
+      if (mine) {
+        w[0] = W::make(p.blob, __builtin_amdgcn_readfirstlane(S.sel[s]), L, F, MAT_DOWN, rg, lane);
+        prime_stream<W, 1, DEC_DN_PF>(w, sb, ring, F / 128);
+      }
+      if (first) {
+#pragma unroll
+        for (int r = 0; r < UA; ++r) load_up(slab1 + wave + DEC_WAVES * r, r);
+        first = false;
+      }
+      if (ditem < 0) break;
+      if (wave == 0) downs.take();
+      if (mine)
+        for (int u = 0; u < 2; ++u) {
+          const bool again = u == 0 && s + DEC_WAVES < n;
+          wn[0] = again ? W::make(p.blob, __builtin_amdgcn_readfirstlane(S.sel[s + DEC_WAVES]), L, F, MAT_DOWN, rg, lane)
+                        : w[0];
+          int32_t* ready = line(p.ctr, C_EXPERT + S.sgrp[s]);
+          while (get(ready) < nrb) __builtin_amdgcn_s_sleep(1);
+          // the row by 8-byte agent-scope loads, SU of a lane in flight
+          constexpr int SU = 13;
+          const uint8_t* src = p.aq + (int64_t)s * arow;
+          for (int i0 = 8 * lane; i0 < arow; i0 += 8 * WAVE * SU) {
+            unsigned long long v[SU];
+#pragma unroll
+            for (int q = 0; q < SU; ++q) {
+              const int i = i0 + 8 * WAVE * q;
+              v[q] = get(reinterpret_cast<const unsigned long long*>(src + (i < arow ? i : 0)));
+            }
+#pragma unroll
+            for (int q = 0; q < SU; ++q) {
+              const int i = i0 + 8 * WAVE * q;
+              if (i < arow) *reinterpret_cast<unsigned long long*>(stage + i) = v[q];
+            }
           }
-          v = (float)(wave_sum_dpp(acc) * (double)p.lora_scale[a]);
+          wave_sync();
+          f32x4 acc[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
+          dec_stream<W, 1, DEC_DN_PF>(w, wn, again && fit, sb, ring, dec_row(stage, F), nl == 0, F, g, acc);
+          if (g == 0) {
+            if (nsc == 1) S.ys[par][s][nl] = acc[0][0];
+            else put(p.y + (int64_t)s * L + 16 * rg + nl, acc[0][0]);
+          }
+          if (!again) break;
+          wave_sync();  // the next row may overwrite this one
+          w[0] = wn[0];
+          if (!fit) prime_stream<W, 1, DEC_DN_PF>(w, sb, ring, F / 128);
+          s += DEC_WAVES;
         }
-        if (lane == 0) p.u[i] = v;
+      if (nsc > 1) stores_done();
+      if (wave == 0) {
+        const int nx = downs.item();
+        if (lane == 0) S.ditem[par ^ 1] = nx;
       }
+      lds_barrier();
+      ditem = S.ditem[par ^ 1];
+      if (wave == 0) {
+        // z[t][l] = bf16(sum_j w[t][j] y[t k + j][l]) in slot order, in fp64, once every slot's
+        // outputs of these rows are there
+        int before = 0;
+        if (nsc > 1 && lane == 0) before = add1(line(p.ctr, C_ROWS + rg));
+        if (__builtin_amdgcn_readfirstlane(before) == nsc - 1) {
+          for (int i = lane; i < T * 16; i += WAVE) {
+            const int t = i / 16, r = i % 16;
+            double acc = 0.0;
+            constexpr int YU = 16;
+            for (int j0 = 0; j0 < k; j0 += YU) {
+              float v[YU];
+#pragma unroll
+              for (int u = 0; u < YU; ++u) {
+                const int sl = t * k + min(j0 + u, k - 1);
+                v[u] = nsc == 1 ? S.ys[par][sl][r] : get(p.y + (int64_t)sl * L + 16 * rg + r);
+              }
+#pragma unroll
+              for (int u = 0; u < YU; ++u)
+                if (j0 + u < k) acc += (double)S.w[t * k + j0 + u] * (double)v[u];
+            }
+            put(p.z + (int64_t)t * L + 16 * rg + r, f64_to_bf16(acc));
+          }
+          stores_done();
+          if (lane == 0) add1(line(p.ctr, C_Z + rg % DEC_DONE_LINES));
+        }
+      }
+      par ^= 1;
     }
-    publish(p.ctr + 32 * C_U_DONE, mine);
   }
-  const int chunk = max(1, min(DEC_WAVES * UR, (d + (int)gridDim.x - 1) / (int)gridDim.x));
-  bool uready = !lora;
-  for (;;) {
-    const int c = claim(p.ctr + 32 * C_UP, chunk, &S.claimed);
-    if (c >= d) break;
-    const int end = min(c + chunk, d);
-    uint4 wr[UR][UC];
+
+  // ---- up (with the adapters' two products): every block holds all of z
+  // one wave a block watches the sum of DEC_DONE_LINES counters: every wave's loads of them
+  // would hold up the additions
+  auto await = [&](int first, int n) {
+    __syncthreads();
+    if (wave == 0)
+      for (;;) {
+        const int v = lane < DEC_DONE_LINES ? get(line(p.ctr, first + lane)) : 0;
+        int sum = 0;
 #pragma unroll
-    for (int i = 0; i < UR; ++i) {
-      const int row = min(c + wave + DEC_WAVES * i, d - 1);
-#pragma unroll
-      for (int q = 0; q < UC; ++q) {
-        const int col = 8 * (WAVE * q + lane);
-        wr[i][q] = load_nt16(p.latent_up + (int64_t)row * L + (col < L ? col : 0));
+        for (int i = 0; i < DEC_DONE_LINES; ++i) sum += __builtin_amdgcn_readlane(v, i);
+        if (sum >= n) break;
+        __builtin_amdgcn_s_sleep(1);
       }
+    __syncthreads();
+  };
+  uint16_t* zs = reinterpret_cast<uint16_t*>(smem);
+  stores_done();  // the slab's loads: behind the barriers every wave sees all of it
+  await(C_Z, nrg);
+  for (int i = 4 * tid; i < T * L; i += 4 * DEC_THREADS)
+    *reinterpret_cast<unsigned long long*>(zs + i) = get(reinterpret_cast<const unsigned long long*>(p.z + i));
+  __syncthreads();
+  const bool lora = p.lora.B != nullptr;
+  if (lora) {
+    const int R = p.lora.R;
+    Claims its(line(p.ctr, C_U), T * R);
+    its.take();
+    for (int item = its.item(); item >= 0; item = its.item()) {
+      its.take();
+      const int t = item / R, r = item - t * R;
+      int a;
+      const int rk = dec_rank(p.lora, t, a);
+      float v = 0.f;
+      if (r < rk) {
+        const uint16_t* A = p.lora_a + ((int64_t)a * R + r) * L;
+        double acc = 0.0;
+        for (int col = 8 * lane; col < L; col += 8 * WAVE) {
+          const uint4 x = *reinterpret_cast<const uint4*>(zs + t * L + col);
+          const uint4 av = *reinterpret_cast<const uint4*>(A + col);
+          float q = dot2(x.x, av.x, 0.f);
+          q = dot2(x.y, av.y, q);
+          q = dot2(x.z, av.z, q);
+          q = dot2(x.w, av.w, q);
+          acc += (double)q;
+        }
+        v = (float)(wave_sum_dpp(acc) * (double)p.lora_scale[a]);
+      }
+      if (lane == 0) put(p.u + item, v);
+      stores_done();
+      if (lane == 0) add1(line(p.ctr, C_U_DONE + item % DEC_DONE_LINES));
     }
-    if (!ready) stage_z();
-    if (!uready) await(p.ctr + 32 * C_U_DONE, nu);
-    uready = true;
+    await(C_U_DONE, T * R);
+  }
+  // one row for every token: weights(q) is chunk q of the row
+  auto up_row = [&](int row, auto&& weights) {
     for (int t = 0; t < T; ++t) {
-      double acc[UR];
-#pragma unroll
-      for (int i = 0; i < UR; ++i) acc[i] = 0.0;
+      double acc = 0.0;
 #pragma unroll
       for (int q = 0; q < UC; ++q) {
         const int col = 8 * (WAVE * q + lane);
         if (col < L) {
-          const uint4 x = *reinterpret_cast<const uint4*>(zs + t * L + col);
-#pragma unroll
-          for (int i = 0; i < UR; ++i) {
-            float s = dot2(x.x, wr[i][q].x, 0.f);
-            s = dot2(x.y, wr[i][q].y, s);
-            s = dot2(x.z, wr[i][q].z, s);
-            s = dot2(x.w, wr[i][q].w, s);
-            acc[i] += (double)s;
-          }
+          const uint4 x = *reinterpret_cast<const uint4*>(zs + t * L + col), v = weights(q);
+          float s = dot2(x.x, v.x, 0.f);
+          s = dot2(x.y, v.y, s);
+          s = dot2(x.z, v.z, s);
+          s = dot2(x.w, v.w, s);
+          acc += (double)s;
         }
       }
       if (lora) {
-        const int a = p.lora.adapter[t];
-        const bool have = (uint32_t)a < (uint32_t)p.lora.N;
-        const int rk = !have ? 0 : p.lora.rank ? min(p.lora.rank[a], p.lora.R) : p.lora.R;
-#pragma unroll
-        for (int i = 0; i < UR; ++i) {
-          const int row = min(c + wave + DEC_WAVES * i, d - 1);
-          for (int r = lane; r < rk; r += WAVE)
-            acc[i] += (double)p.u[t * p.lora.R + r] * (double)bf16f(p.lora.B[((int64_t)a * d + row) * p.lora.R + r]);
-        }
+        int a;
+        const int rk = dec_rank(p.lora, t, a);
+        for (int r = lane; r < rk; r += WAVE)
+          acc += (double)get(p.u + t * p.lora.R + r) * (double)bf16f(p.lora.B[((int64_t)a * d + row) * p.lora.R + r]);
       }
-#pragma unroll
-      for (int i = 0; i < UR; ++i) {
-        const int row = c + wave + DEC_WAVES * i;
-        const double v = wave_sum_dpp(acc[i]);
-        if (lane == 0 && row < end) p.out[(int64_t)t * d + row] = f64_to_bf16(v);
-      }
+      acc = wave_sum_dpp(acc);
+      if (lane == 0) p.out[(int64_t)t * d + row] = f64_to_bf16(acc);
     }
+  };
+  for (int row = slab1 + wave; row < up1; row += DEC_WAVES * UA) {
+#pragma unroll
+    for (int r = 0; r < UA; ++r)
+      if (row + DEC_WAVES * r < up1) up_row(row + DEC_WAVES * r, [&](int q) { return wr[r][q]; });
+    if (row + DEC_WAVES * UA < up1)
+#pragma unroll
+      for (int r = 0; r < UA; ++r) load_up(row + DEC_WAVES * (UA + r), r);
   }
+  for (int row = up0 + wave; row < slab1; row += DEC_WAVES)
+    up_row(row, [&](int q) { return *reinterpret_cast<const uint4*>(slab + (row - up0) * L + 8 * (WAVE * q + lane)); });
 }
 
 // ------------------------------------------------------------------------- host
@@ -421,41 +836,42 @@ static int cu_count() {
   return n;
 }
 
-template <class W, int NS, int UC, int UR>
+template <class W, int UC, int UA>
 static hipError_t launch_decode_as(const DecodeArgs& a, unsigned grid, size_t lds, hipStream_t st) {
   static const hipError_t e =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(&decode_kernel<W, NS, UC, UR>),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024 - DEC_LDS_STATIC);
+      hipFuncSetAttribute(reinterpret_cast<const void*>(&decode_kernel<W, UC, UA>),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, (int)DEC_LDS);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((decode_kernel<W, NS, UC, UR>), dim3(grid), dim3(DEC_THREADS), lds, st, a);
+  hipLaunchKernelGGL((decode_kernel<W, UC, UA>), dim3(grid), dim3(DEC_THREADS), lds, st, a);
   return hipGetLastError();
 }
 
-hipError_t launch_decode(const DecodeArgs& a, bool packed, hipStream_t st) {
+hipError_t launch_decode(const DecodeArgs& args, bool packed, hipStream_t st) {
+  DecodeArgs a = args;
   const int T = (int)a.r.T, n = T * a.r.k, L = a.r.L, F = a.F;
   if (T < 1 || T > DECODE_MAX_TOKENS || n > DECODE_MAX_ROWS || L % 128 || F % 128 || L > 7168 || F > 7168 ||
       a.r.E > ROUTE_MAXI * WAVE || a.r.d % 8)
     return hipErrorInvalidValue;
-  const size_t avail = 160 * 1024 - DEC_LDS_STATIC;
-  // two rows a wave side by side halve the waves' dependent steps; where sixteen staged rows
-  // exceed the LDS, one
-  const bool two = (size_t)2 * DEC_WAVES * dec_row_bytes(F) <= avail;
-  size_t lds = (size_t)T * dec_row_bytes(L);
-  lds = lds > (size_t)(two ? 2 : 1) * DEC_WAVES * dec_row_bytes(F) ? lds : (size_t)(two ? 2 : 1) * DEC_WAVES * dec_row_bytes(F);
-  if (lds > avail) return hipErrorInvalidValue;
   // one block per CU, fewer where no phase has that many items
-  int64_t items = (int64_t)n * (F / DEC_ROWS);
-  if (items < L / 16) items = L / 16;
+  int64_t items = ceil_div((int64_t)n * (F / 16), DEC_WAVES);
+  if (items < (L / 16) * ceil_div(n, DEC_SLOTS)) items = (L / 16) * ceil_div(n, DEC_SLOTS);
   if (items < a.r.d / DEC_WAVES) items = a.r.d / DEC_WAVES;
   const unsigned grid = (unsigned)(items < cu_count() ? items : cu_count());
+  a.up_rows = (int32_t)ceil_div(a.r.d, grid);
+  // LDS: the quantised h; each wave's staged row of the down operand behind it, or, where they
+  // do not fit there, in its place (and the block meets a barrier); then the slab
+  const size_t hq = (size_t)T * dec_row_bytes(L), rows = (size_t)DEC_WAVES * dec_row_bytes(F);
+  a.stage_offset = hq + rows <= DEC_LDS ? (int32_t)hq : 0;
+  size_t used = a.stage_offset + rows;
+  if (used < hq) used = hq;
+  if (used > DEC_LDS) return hipErrorInvalidValue;
+  a.slab_offset = (int32_t)used;
+  const int64_t slab = (int64_t)((DEC_LDS - used) / ((size_t)L * 2));
+  a.slab_rows = (int32_t)(slab < a.up_rows ? slab : a.up_rows);
+  const size_t lds = used + (size_t)a.slab_rows * L * 2;
   const bool wide = L > 7 * 512;
-  auto go = [&](auto wt) -> hipError_t {
-    using W = decltype(wt);
-    if (two)
-      return wide ? launch_decode_as<W, 2, 14, 2>(a, grid, lds, st) : launch_decode_as<W, 2, 7, 4>(a, grid, lds, st);
-    return wide ? launch_decode_as<W, 1, 14, 2>(a, grid, lds, st) : launch_decode_as<W, 1, 7, 4>(a, grid, lds, st);
-  };
-  return packed ? go(PackedW{}) : go(RecordW{});
+  if (packed) return wide ? launch_decode_as<PackedW, 14, 1>(a, grid, lds, st) : launch_decode_as<PackedW, 7, 2>(a, grid, lds, st);
+  return wide ? launch_decode_as<RecordW, 14, 1>(a, grid, lds, st) : launch_decode_as<RecordW, 7, 2>(a, grid, lds, st);
 }
 
 }  // namespace moe

@@ -33,7 +33,7 @@ struct DenseParams {
   int32_t nseg;
   DenseSeg seg[2];
   LoraSeg lora;  // of the last segment
-  int32_t* clear = nullptr;  // words the first block sets to zero
+  int32_t* clear = nullptr;  // words, 32 apart, that the first blocks set to zero
   int32_t nclear = 0;
 };
 
@@ -65,7 +65,8 @@ __global__ void __launch_bounds__(256) dense_gemv_kernel(DenseParams p) {
   if (!valid) row = s.rows - 1;
   const int32_t K = p.K;
   const int64_t t0 = (int64_t)blockIdx.y * G;
-  if (blockIdx.x == 0 && blockIdx.y == 0 && (int)threadIdx.x < p.nclear) p.clear[threadIdx.x] = 0;
+  if (blockIdx.y == 0)
+    for (int i = blockIdx.x * 256 + threadIdx.x; i < p.nclear; i += gridDim.x * 256) p.clear[32 * i] = 0;
 
   uint4 xv[XPT];
 #pragma unroll
@@ -225,7 +226,6 @@ static hipError_t launch_nch(const DenseParams& p, hipStream_t st) {
 hipError_t launch_dense_gemv(const uint16_t* x, int64_t T, int32_t K, const DenseSeg* segs, int nseg,
                              hipStream_t st, const LoraSeg* lora, int32_t* clear, int32_t nclear) {
   DenseParams p;
-  if (nclear > 256) return hipErrorInvalidValue;
   if (lora) p.lora = *lora;
   p.clear = clear;
   p.nclear = clear ? nclear : 0;

@@ -58,7 +58,7 @@ struct DenseSeg {
 // unit of |x_t| |w_e| (see the kernel for its derivation).
 constexpr double GEMV_ROUTER_GAMMA = 16.0 / 8388608.0;  // 16 * 2^-23
 // lora, when given, is the adapters' term of the last segment
-// clear, when given, is nclear words (at most 256) that the launch sets to zero
+// clear, when given, is nclear words, 32 words apart, that the launch sets to zero
 hipError_t launch_dense_gemv(const uint16_t* x, int64_t T, int32_t K, const DenseSeg* segs, int nseg,
                              hipStream_t st, const LoraSeg* lora = nullptr, int32_t* clear = nullptr,
                              int32_t nclear = 0);
@@ -216,7 +216,7 @@ hipError_t launch_reap_keep_bias(const double* saliency, int32_t E, int32_t n_ke
 // ---- decode.hip: a few tokens' layer behind the router logits and the latent rows
 constexpr int DECODE_MAX_TOKENS = 8;
 constexpr int DECODE_MAX_ROWS = 64;   // T * k
-constexpr int DECODE_COUNTERS = 224;  // words of phase counters, zero when the kernel starts
+int32_t decode_counters(int32_t L);   // counters, 32 words apart, zero when the kernel starts
 struct DecodeArgs {
   RouteArgs r;               // h set; idx, w and hq unused
   const uint8_t* blob;
@@ -225,7 +225,8 @@ struct DecodeArgs {
   uint8_t* aq;               // decode_aq_bytes(T*k, F): the GLU rows by slot, quantised
   uint16_t* z;               // [T][L]
   uint16_t* out;             // [T][d]
-  int32_t* ctr;              // [DECODE_COUNTERS]
+  float* y;                  // [T*k][L]
+  int32_t* ctr;              // [32 * decode_counters(L)]
   LoraSeg lora;              // of latent_up; u is this kernel's own
   const uint16_t* lora_a;    // [N][R][L]
   const float* lora_scale;   // [N]
@@ -236,6 +237,9 @@ struct DecodeArgs {
   int32_t* counts;
   int32_t* offsets;
   int32_t* perm;
+  // set by the launcher
+  int32_t stage_offset;              // the waves' LDS rows of the down operand
+  int32_t up_rows, slab_rows, slab_offset;  // a block's up rows, and those of them that wait in its LDS
 };
 size_t decode_aq_bytes(int64_t rows, int32_t F);
 hipError_t launch_decode(const DecodeArgs& a, bool packed, hipStream_t st);

@@ -49,7 +49,7 @@ struct RecordW {
   int nsb, n, g;     // scale bytes per row; lane row and K block
 
   // matrix `mat` of expert e, rows 16 grp .. 16 grp + 15
-  __device__ static RecordW make(const uint8_t* blob, int e, int L, int F, int mat, int grp, int lane) {
+  __device__ __forceinline__ static RecordW make(const uint8_t* blob, int e, int L, int F, int mat, int grp, int lane) {
     const int64_t mbytes = (int64_t)F * L / 2 + (int64_t)F * L / 32;
     const int K = mat == MAT_DOWN ? F : L;
     const uint8_t* m = blob + (int64_t)e * 3 * mbytes + mat * mbytes;
@@ -93,7 +93,7 @@ struct PackedW {
   const uint8_t* s;  // scale tile 0 + 4 lane
   int nsc;           // scale tiles
 
-  __device__ static PackedW make(const uint8_t* blob, int e, int L, int F, int mat, int grp, int lane) {
+  __device__ __forceinline__ static PackedW make(const uint8_t* blob, int e, int L, int F, int mat, int grp, int lane) {
     const int K = mat == MAT_DOWN ? F : L;
     const int64_t gu = (int64_t)(F / 16) * packed_group_bytes(L);
     const uint8_t* m =
