@@ -326,7 +326,8 @@ MxArgs mx_args(const moe_config& c, int k, const uint8_t* blob, void* ws, const 
 
 // ---- workspace of the few-token layer
 struct DecodeLayout {
-  size_t logits_fast, xnorm, wnorm, h, aq, y, z, u, ctr, lora_down, total;
+  size_t logits_fast, xnorm, wnorm, h, aq, y, ctr, lora_down, total;
+  size_t z, u, ones_bytes;  // what the first launch sets to all ones, in one piece
 };
 DecodeLayout decode_layout(const moe_config& c, int k, const moe_lora* down, const moe_lora* up) {
   DecodeLayout l;
@@ -345,6 +346,7 @@ DecodeLayout decode_layout(const moe_config& c, int k, const moe_lora* down, con
   l.y = take(T * (size_t)k * L * 4);
   l.z = take(T * L * 2);
   l.u = take(up ? T * (size_t)up->max_rank * 4 : 0);
+  l.ones_bytes = off - l.z;
   l.ctr = take((size_t)decode_counters(c.d_latent) * 128);
   l.lora_down = take(lora_bytes(down, c.num_tokens, c.d_model));
   l.total = off;
@@ -1015,8 +1017,13 @@ moe_status moe_layer_decode(const void* x, const void* router_w, const void* lat
   segs[1].router = 0;
   segs[1].out = at<uint16_t>(ws, l.h);
   segs[1].wnorm = segs[1].xnorm = nullptr;
+  Clear clear;
+  clear.zero = at<int32_t>(ws, l.ctr);
+  clear.nzero = decode_counters(c.d_latent);
+  clear.ones = at<uint4>(ws, l.z);
+  clear.nones = (int32_t)(l.ones_bytes / 16);
   MOE_TRY(dev(launch_dense_gemv(static_cast<const uint16_t*>(x), c.num_tokens, c.d_model, segs, 2, st,
-                                lora_down ? &down : nullptr, at<int32_t>(ws, l.ctr), decode_counters(c.d_latent))));
+                                lora_down ? &down : nullptr, &clear)));
   DecodeArgs a;
   a.r = route_args(c, k, 0, x, router_w, router_bias, nullptr, nullptr, routing ? routing->logits : nullptr, ws, l);
   a.r.h = at<uint16_t>(ws, l.h);
@@ -1026,11 +1033,11 @@ moe_status moe_layer_decode(const void* x, const void* router_w, const void* lat
   a.aq = at<uint8_t>(ws, l.aq);
   a.y = at<float>(ws, l.y);
   a.z = at<uint16_t>(ws, l.z);
+  a.u = at<uint32_t>(ws, l.u);
   a.out = static_cast<uint16_t*>(out);
   a.ctr = at<int32_t>(ws, l.ctr);
   a.lora_a = nullptr;
   a.lora_scale = nullptr;
-  a.u = nullptr;
   if (lora_up) {
     a.lora.B = static_cast<const uint16_t*>(lora_up->b);
     a.lora.adapter = lora_up->adapter;
@@ -1039,7 +1046,6 @@ moe_status moe_layer_decode(const void* x, const void* router_w, const void* lat
     a.lora.R = lora_up->max_rank;
     a.lora_a = static_cast<const uint16_t*>(lora_up->a);
     a.lora_scale = lora_up->scale;
-    a.u = at<float>(ws, l.u);
   }
   a.idx = routing ? routing->topk_idx : nullptr;
   a.w = routing ? routing->topk_w : nullptr;

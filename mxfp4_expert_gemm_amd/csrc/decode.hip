@@ -11,8 +11,8 @@
 //   down       16 latent rows of up to 16 routed rows, a block each, with the combine where
 //              that is all of them (else the block that finishes a group of rows combines);
 //   up         a share of the output rows per block, whose weights are under way long
-//              before: some into the LDS while the routing runs, some into registers while
-//              the last gate / up items finish.
+//              before: some into the LDS as the routing ends, some into registers while the
+//              last gate / up items finish.
 //
 // Progress.  A block claims gate / up chunks and down items when it is about to work on them,
 // and waits only for items of earlier phases, which it does when all of them are claimed, by
@@ -23,10 +23,13 @@
 // Counters.  2048 atomic additions to one address take 23 us here (11 ns each, at the memory
 // side, since the XCDs' L2s are not shared), to 32 addresses 1 us: an item counter is 32
 // shards on lines of their own (item 32 j + s is the j-th of shard s, and a claimer whose shard
-// is spent looks for another that has some left), and completion is counted per expert,
-// per row group and over 8 lines.  The launch before clears them.  What one wave hands to
-// another is written through to the memory side (agent-scope stores), waited for, and only
-// then counted; the reader's loads are agent-scope too.  A hand-over takes 0.8 us.
+// is spent looks for another that has some left), and completion is counted per expert
+// and per row group.  What one wave hands to another is written through to the memory side
+// (agent-scope stores), and, where it is counted, waited for before; the reader's loads are
+// agent-scope too.  A hand-over takes 0.8 us.  z and the adapters' u need no count: their
+// words start as all ones, which none of them can be (a bf16 NaN here is 0x7FC0, and an fp32
+// NaN's low bits are zeros), and a reader asks again until a word is another.  The launch
+// before sets counters and words.
 //
 // The arithmetic of every value is that of the kernels moe_layer_forward runs on a batch of
 // this size (dense_gemv_kernel, the routing, stream_group, the fp64 combine), in the same
@@ -50,15 +53,12 @@ __host__ __device__ constexpr int dec_row_bytes(int K) { return (2 * K + K / 16 
 __device__ __forceinline__ ALds dec_row(uint8_t* row, int K) { return {row, row + K, row + 2 * K, row + 2 * K + K / 32}; }
 
 // ---- counters, each on a 128-byte line of its own
-constexpr int DEC_DONE_LINES = 8;
 enum {
   C_GATEUP = 0,                         // claimed items, by shard
   C_DOWN = C_GATEUP + DEC_SHARDS,
   C_U = C_DOWN + DEC_SHARDS,
   C_EXPERT = C_U + DEC_SHARDS,          // quantised gate / up scale blocks, by expert
-  C_Z = C_EXPERT + DECODE_MAX_ROWS,     // combined row groups
-  C_U_DONE = C_Z + DEC_DONE_LINES,      // finished (token, rank) pairs
-  C_ROWS = C_U_DONE + DEC_DONE_LINES    // finished down items, by row group
+  C_ROWS = C_EXPERT + DECODE_MAX_ROWS   // finished down items, by row group
 };
 int32_t decode_counters(int32_t L) { return C_ROWS + L / 16; }
 __device__ __forceinline__ int32_t* line(int32_t* ctr, int i) { return ctr + 32 * i; }
@@ -79,6 +79,22 @@ __device__ __forceinline__ void stores_done() { asm volatile("s_waitcnt vmcnt(0)
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
   __builtin_amdgcn_wave_barrier();
+}
+
+// words that are still to come
+__device__ __forceinline__ bool missing16(unsigned long long v) {  // a 16-bit lane is all ones
+  const unsigned long long t = ~v;
+  return ((t - 0x0001000100010001ull) & ~t & 0x8000800080008000ull) != 0ull;
+}
+__device__ __forceinline__ unsigned long long await16(const uint16_t* p) {
+  unsigned long long v;
+  while (missing16(v = get(reinterpret_cast<const unsigned long long*>(p)))) __builtin_amdgcn_s_sleep(2);
+  return v;
+}
+__device__ __forceinline__ uint32_t await32(const uint32_t* p) {
+  uint32_t v;
+  while ((v = get(p)) == 0xFFFFFFFFu) __builtin_amdgcn_s_sleep(2);
+  return v;
 }
 
 // Claims of one phase's n items by a wave.  take() sends the request for the wave's next item
@@ -214,11 +230,6 @@ struct RouteBlock {
     }
     xn = a.xnorm[t];
   }
-  __device__ __forceinline__ void arrived() const {  // the loads above have come
-#pragma unroll
-    for (int i = 0; i < EPT; ++i) asm volatile("" ::"v"(lf[i]), "v"(bv[i]), "v"(wn[i]));
-    asm volatile("" ::"v"(xn));
-  }
   __device__ __forceinline__ void select(const RouteArgs& a, DecodeLds& S) const {
     const int lane = lane_id(), wave = threadIdx.x / WAVE, t = wave / W, sub = wave % W;
     const int E = a.E, k = a.k;
@@ -334,16 +345,17 @@ struct RouteBlock {
 };
 
 // Routing of all tokens into S, and h quantised into hq, by the whole block; the first block
-// also writes what the caller asked for.  ahead() starts loads that the routing hides: it
-// runs when nothing the routing needs is on its way any more.
-template <int EPT, class Fn>
+// also writes what the caller asked for.  ahead() starts loads that the end of the routing
+// hides; before() takes what is still on its way (a wait for an older load, afterwards, would
+// wait for those too).
+template <int EPT, class Fb, class Fn>
 __device__ __forceinline__ void dec_route(const DecodeArgs& p, const RouteArgs& a, DecodeLds& S, uint8_t* hq,
-                                          Fn&& ahead) {
+                                          Fb&& before, Fn&& ahead) {
   const int tid = threadIdx.x;
   const int T = (int)a.T, L = a.L;
   RouteBlock<EPT> rb;
   rb.load(a);
-  constexpr int U = 4;  // groups of eight latent values a thread has in flight
+  constexpr int U = 2;  // groups of eight latent values a thread has in flight
   const int per = L / 8, groups = T * per;
   uint4 raw[U];
   auto load_h = [&](int j0) {
@@ -380,10 +392,9 @@ __device__ __forceinline__ void dec_route(const DecodeArgs& p, const RouteArgs& 
       }
     }
   }
-  // a wait for older loads would wait for the ones ahead() starts: take them first
-  rb.arrived();
-  ahead();
   rb.select(a, S);
+  before();
+  ahead();  // by most waves while few certify
 }
 
 // the selection's groups, the caller's routing outputs and the first gate / up chunk
@@ -496,10 +507,11 @@ __global__ void __launch_bounds__(DEC_THREADS) decode_kernel(DecodeArgs p) {
         lds_dma16(reinterpret_cast<const uint8_t*>(p.latent_up + (int64_t)up0 * L) + i + 16 * lane,
                   reinterpret_cast<const uint8_t*>(slab) + i);
   };
-  if (T == 1) dec_route<2>(p, ra, S, smem, ahead);
-  else if (T == 2) dec_route<4>(p, ra, S, smem, ahead);
-  else if (T <= 4) dec_route<8>(p, ra, S, smem, ahead);
-  else dec_route<16>(p, ra, S, smem, ahead);
+  auto before = [&]() { asm volatile("" ::"v"(chunks.asked), "v"(downs.asked)); };
+  if (T == 1) dec_route<2>(p, ra, S, smem, before, ahead);
+  else if (T == 2) dec_route<4>(p, ra, S, smem, before, ahead);
+  else if (T <= 4) dec_route<8>(p, ra, S, smem, before, ahead);
+  else dec_route<16>(p, ra, S, smem, before, ahead);
   dec_group(p, ra, S);
   // chunks of consecutive pairs, about half as many items as waves or as many: a CU's waves
   // then read one stretch of memory
@@ -722,8 +734,6 @@ __global__ void __launch_bounds__(DEC_THREADS) decode_kernel(DecodeArgs p) {
             }
             put(p.z + (int64_t)t * L + 16 * rg + r, f64_to_bf16(acc));
           }
-          stores_done();
-          if (lane == 0) add1(line(p.ctr, C_Z + rg % DEC_DONE_LINES));
         }
       }
       par ^= 1;
@@ -731,94 +741,126 @@ __global__ void __launch_bounds__(DEC_THREADS) decode_kernel(DecodeArgs p) {
   }
 
   // ---- up (with the adapters' two products): every block holds all of z
-  // one wave a block watches the sum of DEC_DONE_LINES counters: every wave's loads of them
-  // would hold up the additions
-  auto await = [&](int first, int n) {
-    __syncthreads();
-    if (wave == 0)
-      for (;;) {
-        const int v = lane < DEC_DONE_LINES ? get(line(p.ctr, first + lane)) : 0;
-        int sum = 0;
-#pragma unroll
-        for (int i = 0; i < DEC_DONE_LINES; ++i) sum += __builtin_amdgcn_readlane(v, i);
-        if (sum >= n) break;
-        __builtin_amdgcn_s_sleep(1);
-      }
-    __syncthreads();
-  };
-  uint16_t* zs = reinterpret_cast<uint16_t*>(smem);
-  stores_done();  // the slab's loads: behind the barriers every wave sees all of it
-  await(C_Z, nrg);
-  for (int i = 4 * tid; i < T * L; i += 4 * DEC_THREADS)
-    *reinterpret_cast<unsigned long long*>(zs + i) = get(reinterpret_cast<const unsigned long long*>(p.z + i));
-  __syncthreads();
   const bool lora = p.lora.B != nullptr;
+  const int R = p.lora.R;
+  Claims us(line(p.ctr, C_U), T * R);
+  if (lora) us.take();
+  stores_done();    // the slab's loads: behind the barriers every wave sees all of it
+  lds_barrier();    // no wave reads its staged rows any more
+  uint16_t* zs = reinterpret_cast<uint16_t*>(smem);
+  float* ul = reinterpret_cast<float*>(smem + T * L * 2);                  // [T][R]
+  uint16_t* bl = reinterpret_cast<uint16_t*>(ul + T * R);                 // [up row][T][R], where it fits
+  const bool bfit = T * L * 2 + T * R * (4 + 2 * p.up_rows) <= p.slab_offset;
+  int ui = -1;
+  uint4 ua[UC];
+  auto load_a = [&]() {  // a row of an adapter's first matrix, for (token, rank) pair ui
+    ui = us.item();
+    if (ui < 0) return;
+    const int t = ui / R, r = ui - t * R;
+    int a;
+    const int rk = dec_rank(p.lora, t, a);
+#pragma unroll
+    for (int q = 0; q < UC; ++q) {
+      const int col = 8 * (WAVE * q + lane);
+      ua[q] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < rk && col < L) ua[q] = *reinterpret_cast<const uint4*>(p.lora_a + ((int64_t)a * R + r) * L + col);
+    }
+  };
   if (lora) {
-    const int R = p.lora.R;
-    Claims its(line(p.ctr, C_U), T * R);
-    its.take();
-    for (int item = its.item(); item >= 0; item = its.item()) {
-      its.take();
-      const int t = item / R, r = item - t * R;
+    load_a();
+    if (bfit)  // the rows of the second matrices, eight ranks a thread
+      for (int i = tid; i < (up1 - up0) * T * (R / 8); i += DEC_THREADS) {
+        const int row = i / (T * (R / 8)), t = i / (R / 8) % T, r = i % (R / 8) * 8;
+        int a;
+        const int rk = dec_rank(p.lora, t, a);
+        if (r < rk)
+          *reinterpret_cast<uint4*>(bl + (row * T + t) * R + r) =
+              *reinterpret_cast<const uint4*>(p.lora.B + ((int64_t)a * d + up0 + row) * R + r);
+      }
+  }
+  for (int i = 4 * tid; i < T * L; i += 4 * DEC_THREADS)
+    *reinterpret_cast<unsigned long long*>(zs + i) = await16(p.z + i);
+  lds_barrier();
+  if (lora) {
+    while (ui >= 0) {
+      us.take();
+      const int t = ui / R, r = ui - t * R;
       int a;
       const int rk = dec_rank(p.lora, t, a);
       float v = 0.f;
       if (r < rk) {
-        const uint16_t* A = p.lora_a + ((int64_t)a * R + r) * L;
         double acc = 0.0;
-        for (int col = 8 * lane; col < L; col += 8 * WAVE) {
-          const uint4 x = *reinterpret_cast<const uint4*>(zs + t * L + col);
-          const uint4 av = *reinterpret_cast<const uint4*>(A + col);
-          float q = dot2(x.x, av.x, 0.f);
-          q = dot2(x.y, av.y, q);
-          q = dot2(x.z, av.z, q);
-          q = dot2(x.w, av.w, q);
-          acc += (double)q;
+#pragma unroll
+        for (int q = 0; q < UC; ++q) {
+          const int col = 8 * (WAVE * q + lane);
+          if (col < L) {
+            const uint4 x = *reinterpret_cast<const uint4*>(zs + t * L + col);
+            float s = dot2(x.x, ua[q].x, 0.f);
+            s = dot2(x.y, ua[q].y, s);
+            s = dot2(x.z, ua[q].z, s);
+            s = dot2(x.w, ua[q].w, s);
+            acc += (double)s;
+          }
         }
         v = (float)(wave_sum_dpp(acc) * (double)p.lora_scale[a]);
       }
-      if (lane == 0) put(p.u + item, v);
-      stores_done();
-      if (lane == 0) add1(line(p.ctr, C_U_DONE + item % DEC_DONE_LINES));
+      if (lane == 0) put(p.u + ui, __float_as_uint(v));
+      load_a();
     }
-    await(C_U_DONE, T * R);
+    for (int i = tid; i < T * R; i += DEC_THREADS) ul[i] = __uint_as_float(await32(p.u + i));
+    lds_barrier();
   }
-  // one row for every token: weights(q) is chunk q of the row
-  auto up_row = [&](int row, auto&& weights) {
+  // NR rows, DEC_WAVES apart, for every token: weights(r, q) is chunk q of the r-th
+  auto rows_up = [&](int row0, int end, auto nr, auto&& weights) {
+    constexpr int NR = decltype(nr)::value;
     for (int t = 0; t < T; ++t) {
-      double acc = 0.0;
+      double acc[NR];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) acc[r] = 0.0;
 #pragma unroll
       for (int q = 0; q < UC; ++q) {
         const int col = 8 * (WAVE * q + lane);
         if (col < L) {
-          const uint4 x = *reinterpret_cast<const uint4*>(zs + t * L + col), v = weights(q);
-          float s = dot2(x.x, v.x, 0.f);
-          s = dot2(x.y, v.y, s);
-          s = dot2(x.z, v.z, s);
-          s = dot2(x.w, v.w, s);
-          acc += (double)s;
+          const uint4 x = *reinterpret_cast<const uint4*>(zs + t * L + col);
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            const uint4 v = weights(r, q);
+            float s = dot2(x.x, v.x, 0.f);
+            s = dot2(x.y, v.y, s);
+            s = dot2(x.z, v.z, s);
+            s = dot2(x.w, v.w, s);
+            acc[r] += (double)s;
+          }
         }
       }
       if (lora) {
         int a;
         const int rk = dec_rank(p.lora, t, a);
-        for (int r = lane; r < rk; r += WAVE)
-          acc += (double)get(p.u + t * p.lora.R + r) * (double)bf16f(p.lora.B[((int64_t)a * d + row) * p.lora.R + r]);
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const int row = min(row0 + DEC_WAVES * r, end - 1);
+          const uint16_t* B = bfit ? bl + ((row - up0) * T + t) * R : p.lora.B + ((int64_t)a * d + row) * R;
+          for (int i = lane; i < rk; i += WAVE) acc[r] += (double)ul[t * R + i] * (double)bf16f(B[i]);
+        }
       }
-      acc = wave_sum_dpp(acc);
-      if (lane == 0) p.out[(int64_t)t * d + row] = f64_to_bf16(acc);
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const double v = wave_sum_dpp(acc[r]);
+        if (lane == 0 && row0 + DEC_WAVES * r < end) p.out[(int64_t)t * d + row0 + DEC_WAVES * r] = f64_to_bf16(v);
+      }
     }
   };
   for (int row = slab1 + wave; row < up1; row += DEC_WAVES * UA) {
-#pragma unroll
-    for (int r = 0; r < UA; ++r)
-      if (row + DEC_WAVES * r < up1) up_row(row + DEC_WAVES * r, [&](int q) { return wr[r][q]; });
+    rows_up(row, up1, std::integral_constant<int, UA>{}, [&](int r, int q) { return wr[r][q]; });
     if (row + DEC_WAVES * UA < up1)
 #pragma unroll
       for (int r = 0; r < UA; ++r) load_up(row + DEC_WAVES * (UA + r), r);
   }
-  for (int row = up0 + wave; row < slab1; row += DEC_WAVES)
-    up_row(row, [&](int q) { return *reinterpret_cast<const uint4*>(slab + (row - up0) * L + 8 * (WAVE * q + lane)); });
+  for (int row = up0 + wave; row < slab1; row += DEC_WAVES * 2)
+    rows_up(row, slab1, std::integral_constant<int, 2>{}, [&](int r, int q) {
+      const int at = min(row + DEC_WAVES * r, slab1 - 1) - up0;
+      return *reinterpret_cast<const uint4*>(slab + at * L + 8 * (WAVE * q + lane));
+    });
 }
 
 // ------------------------------------------------------------------------- host

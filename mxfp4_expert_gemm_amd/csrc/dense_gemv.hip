@@ -33,8 +33,7 @@ struct DenseParams {
   int32_t nseg;
   DenseSeg seg[2];
   LoraSeg lora;  // of the last segment
-  int32_t* clear = nullptr;  // words, 32 apart, that the first blocks set to zero
-  int32_t nclear = 0;
+  Clear clear;
 };
 
 // The token rows are staged once per block in LDS (their loads issued first, then the
@@ -65,8 +64,11 @@ __global__ void __launch_bounds__(256) dense_gemv_kernel(DenseParams p) {
   if (!valid) row = s.rows - 1;
   const int32_t K = p.K;
   const int64_t t0 = (int64_t)blockIdx.y * G;
-  if (blockIdx.y == 0)
-    for (int i = blockIdx.x * 256 + threadIdx.x; i < p.nclear; i += gridDim.x * 256) p.clear[32 * i] = 0;
+  if (blockIdx.y == 0) {
+    for (int i = blockIdx.x * 256 + threadIdx.x; i < p.clear.nzero; i += gridDim.x * 256) p.clear.zero[32 * i] = 0;
+    for (int i = blockIdx.x * 256 + threadIdx.x; i < p.clear.nones; i += gridDim.x * 256)
+      p.clear.ones[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+  }
 
   uint4 xv[XPT];
 #pragma unroll
@@ -217,18 +219,21 @@ static hipError_t launch_nch_g(const DenseParams& p, hipStream_t st) {
 
 template <int NCH>
 static hipError_t launch_nch(const DenseParams& p, hipStream_t st) {
-  // keep the token registers (G * NCH * 4 VGPRs) near 64
-  if (NCH <= 4 && p.T >= 4) return launch_nch_g<NCH, 4>(p, st);
-  if (NCH <= 8 && p.T >= 2) return launch_nch_g<NCH, 2>(p, st);
+  // tokens per block: a weight row is read once for G of them (results do not depend on it).
+  // Four from three tokens on, where a row is long enough that reading it twice costs more
+  // than the unused fourth (4480 x 7168: 4 tokens 36 us with one a block, 19.4 with four;
+  // 3 tokens 28 and 20.5; 1024 x 2048: 3 tokens 3.4 with two, 3.8 with four), else two
+  // (4480 x 7168: 2 tokens 19.7 and 13.5 us).
+  if (p.T >= 4 || (p.T == 3 && NCH > 4)) return launch_nch_g<NCH, 4>(p, st);
+  if (p.T >= 2) return launch_nch_g<NCH, 2>(p, st);
   return launch_nch_g<NCH, 1>(p, st);
 }
 
 hipError_t launch_dense_gemv(const uint16_t* x, int64_t T, int32_t K, const DenseSeg* segs, int nseg,
-                             hipStream_t st, const LoraSeg* lora, int32_t* clear, int32_t nclear) {
+                             hipStream_t st, const LoraSeg* lora, const Clear* clear) {
   DenseParams p;
   if (lora) p.lora = *lora;
-  p.clear = clear;
-  p.nclear = clear ? nclear : 0;
+  if (clear) p.clear = *clear;
   p.x = x;
   p.T = T;
   p.K = K;

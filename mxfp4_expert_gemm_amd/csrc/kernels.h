@@ -58,10 +58,15 @@ struct DenseSeg {
 // unit of |x_t| |w_e| (see the kernel for its derivation).
 constexpr double GEMV_ROUTER_GAMMA = 16.0 / 8388608.0;  // 16 * 2^-23
 // lora, when given, is the adapters' term of the last segment
-// clear, when given, is nclear words, 32 words apart, that the launch sets to zero
+// clear, when given, is memory that the launch sets besides
+struct Clear {
+  int32_t* zero = nullptr;  // nzero words, 32 apart, to 0
+  int32_t nzero = 0;
+  uint4* ones = nullptr;    // nones pieces of 16 bytes to all ones
+  int32_t nones = 0;
+};
 hipError_t launch_dense_gemv(const uint16_t* x, int64_t T, int32_t K, const DenseSeg* segs, int nseg,
-                             hipStream_t st, const LoraSeg* lora = nullptr, int32_t* clear = nullptr,
-                             int32_t nclear = 0);
+                             hipStream_t st, const LoraSeg* lora = nullptr, const Clear* clear = nullptr);
 
 // ---- dense_mfma.hip: the same projections on the matrix cores for token batches
 constexpr double DENSE_MFMA_ROUTER_GAMMA = 66.0 / 8388608.0;  // 66 * 2^-23
@@ -223,14 +228,14 @@ struct DecodeArgs {
   int32_t F;
   const uint16_t* latent_up;  // [d][L]
   uint8_t* aq;               // decode_aq_bytes(T*k, F): the GLU rows by slot, quantised
-  uint16_t* z;               // [T][L]
+  uint16_t* z;               // [T][L], all ones when the kernel starts
+  uint32_t* u;               // [T][R of lora] fp32 bits, likewise
   uint16_t* out;             // [T][d]
   float* y;                  // [T*k][L]
   int32_t* ctr;              // [32 * decode_counters(L)]
-  LoraSeg lora;              // of latent_up; u is this kernel's own
+  LoraSeg lora;              // of latent_up, its u unused
   const uint16_t* lora_a;    // [N][R][L]
   const float* lora_scale;   // [N]
-  float* u;                  // [T][R]
   // the caller's, nullable
   int32_t* idx;
   float* w;
