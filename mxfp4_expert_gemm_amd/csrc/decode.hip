@@ -179,6 +179,7 @@ __device__ __forceinline__ void dec_stream(const W (&w)[NS], const W (&wn)[NS], 
 struct DecodeLds {
   union {
     RouteLds route[DECODE_MAX_TOKENS];  // candidates and output of a token
+    unsigned long long slots[ROUTE_MAXI * WAVE];  // of an expert, while they are grouped
     struct {
       uint16_t tile[DEC_TILES][DECODE_MAX_TOKENS][34];  // GLU outputs of a pair of items
       float ys[2][DEC_SLOTS][16];                       // expert outputs of a down item, by slot
@@ -200,7 +201,7 @@ struct DecodeLds {
   // the block's gate / up chunk: (sequence << 16 | chunk) << 32 | items taken of it
   unsigned long long chunk;
   int tile_of[DEC_TILES], tile_n[DEC_TILES];  // the pair a tile is for, items of it there
-  int ditem[2];
+  unsigned long long ditem[2];  // (sequence + 1) << 32 | down item, as wave 0 learns of it
 };
 constexpr uint32_t DEC_NO_CHUNK = 0xFFFFFFFFu;
 constexpr size_t DEC_LDS = (160 * 1024 - sizeof(DecodeLds)) / 1024 * 1024;  // what is left for the launch to size
@@ -420,10 +421,11 @@ __device__ __forceinline__ void dec_group(const DecodeArgs& p, const RouteArgs& 
       if (lane == 0) S.ng = n;
     } else {  // a lane per slot: the first slot of an expert leads its group
       unsigned long long mine = 0;
-      for (int s = 0; s < n; ++s) {
-        const unsigned long long m = __ballot(e == __builtin_amdgcn_readlane(e, s));
-        if (e >= 0 && (m >> lane) & 1ull) mine = m;
-      }
+      if (e >= 0) S.slots[e] = 0ull;
+      wave_sync();
+      if (e >= 0) atomicOr(&S.slots[e], 1ull << lane);
+      wave_sync();
+      if (e >= 0) mine = S.slots[e];
       const unsigned long long below = (1ull << lane) - 1ull;
       const bool lead = e >= 0 && (mine & below) == 0ull;
       const unsigned long long leads = __ballot(lead);
@@ -527,7 +529,8 @@ __global__ void __launch_bounds__(DEC_THREADS) decode_kernel(DecodeArgs p) {
     const int c = chunks.item(), dn = downs.item();
     if (lane == 0) {
       S.chunk = (unsigned long long)(c < 0 ? DEC_NO_CHUNK : (uint32_t)c) << 32;
-      S.ditem[0] = dn;
+      S.ditem[0] = 1ull << 32 | (uint32_t)dn;
+      S.ditem[1] = 0ull;
     }
   }
   lds_barrier();
@@ -651,66 +654,85 @@ __global__ void __launch_bounds__(DEC_THREADS) decode_kernel(DecodeArgs p) {
     SBlock sb[1];
     uint4 ring[1][DEC_DN_PF];
     const bool fit = (F / 128) % DEC_DN_PF == 0;
-    int ditem = S.ditem[0], par = 0;
-    bool first = true;
-    for (;;) {
-      const int sc = ditem < 0 ? 0 : ditem / nrg, rg = ditem < 0 ? 0 : ditem - sc * nrg;
-      int s = DEC_SLOTS * sc + wave;
-      const bool mine = ditem >= 0 && s < n;
-      if (mine) {
-        w[0] = W::make(p.blob, __builtin_amdgcn_readfirstlane(S.sel[s]), L, F, MAT_DOWN, rg, lane);
-        prime_stream<W, 1, DEC_DN_PF>(w, sb, ring, F / 128);
+    // the block's seq-th item: wave 0 has claimed it and says so in the LDS
+    auto item_of = [&](int seq) -> int {
+      for (;;) {
+        const unsigned long long v = __hip_atomic_load(&S.ditem[seq & 1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        if (__builtin_amdgcn_readfirstlane((int)(v >> 32)) == seq + 1) return __builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+        __builtin_amdgcn_s_sleep(1);
       }
-      if (first) {
+    };
+    auto slot_of = [&](int item) { return item < 0 ? n : DEC_SLOTS * (item / nrg) + wave; };
+    auto make = [&](int item, int s) {
+      return W::make(p.blob, __builtin_amdgcn_readfirstlane(S.sel[s]), L, F, MAT_DOWN, item % nrg, lane);
+    };
+    int ditem = item_of(0), s = slot_of(ditem);
+    if (s < n) {
+      w[0] = make(ditem, s);
+      prime_stream<W, 1, DEC_DN_PF>(w, sb, ring, F / 128);
+    }
 #pragma unroll
-        for (int r = 0; r < UA; ++r) load_up(slab1 + wave + DEC_WAVES * r, r);
-        first = false;
-      }
-      if (ditem < 0) break;
-      if (wave == 0) downs.take();
-      if (mine)
-        for (int u = 0; u < 2; ++u) {
-          const bool again = u == 0 && s + DEC_WAVES < n;
-          wn[0] = again ? W::make(p.blob, __builtin_amdgcn_readfirstlane(S.sel[s + DEC_WAVES]), L, F, MAT_DOWN, rg, lane)
-                        : w[0];
-          int32_t* ready = line(p.ctr, C_EXPERT + S.sgrp[s]);
-          while (get(ready) < nrb) __builtin_amdgcn_s_sleep(1);
-          // the row by 8-byte agent-scope loads, SU of a lane in flight
-          constexpr int SU = 13;
-          const uint8_t* src = p.aq + (int64_t)s * arow;
-          for (int i0 = 8 * lane; i0 < arow; i0 += 8 * WAVE * SU) {
-            unsigned long long v[SU];
-#pragma unroll
-            for (int q = 0; q < SU; ++q) {
-              const int i = i0 + 8 * WAVE * q;
-              v[q] = get(reinterpret_cast<const unsigned long long*>(src + (i < arow ? i : 0)));
-            }
-#pragma unroll
-            for (int q = 0; q < SU; ++q) {
-              const int i = i0 + 8 * WAVE * q;
-              if (i < arow) *reinterpret_cast<unsigned long long*>(stage + i) = v[q];
-            }
+    for (int r = 0; r < UA; ++r) load_up(slab1 + wave + DEC_WAVES * r, r);
+    for (int seq = 0; ditem >= 0; ++seq) {
+      const int rg = ditem % nrg;
+      int nitem = -2;  // not asked yet
+      while (s < n) {
+        // the wave's next row: of this item, else of the block's next
+        const bool second = s < DEC_SLOTS * (ditem / nrg) + DEC_WAVES && s + DEC_WAVES < n;
+        if (!second) {
+          if (wave == 0) {  // it has rows of every item; claimed no earlier, for a block that may be free by then
+            downs.take();
+            const int nx = downs.item();
+            if (lane == 0)
+              __hip_atomic_store(&S.ditem[(seq + 1) & 1], (unsigned long long)(seq + 2) << 32 | (uint32_t)nx,
+                                 __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
           }
-          wave_sync();
-          f32x4 acc[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
-          dec_stream<W, 1, DEC_DN_PF>(w, wn, again && fit, sb, ring, dec_row(stage, F), nl == 0, F, g, acc);
-          if (g == 0) {
-            if (nsc == 1) S.ys[par][s][nl] = acc[0][0];
-            else put(p.y + (int64_t)s * L + 16 * rg + nl, acc[0][0]);
-          }
-          if (!again) break;
-          wave_sync();  // the next row may overwrite this one
-          w[0] = wn[0];
-          if (!fit) prime_stream<W, 1, DEC_DN_PF>(w, sb, ring, F / 128);
-          s += DEC_WAVES;
+          nitem = item_of(seq + 1);
         }
+        const int ns = second ? s + DEC_WAVES : slot_of(nitem);
+        const bool again = ns < n;
+        wn[0] = again ? make(second ? ditem : nitem, ns) : w[0];
+        int32_t* ready = line(p.ctr, C_EXPERT + S.sgrp[s]);
+        while (get(ready) < nrb) __builtin_amdgcn_s_sleep(1);
+        // the row by 8-byte agent-scope loads, SU of a lane in flight
+        constexpr int SU = 13;
+        const uint8_t* src = p.aq + (int64_t)s * arow;
+        for (int i0 = 8 * lane; i0 < arow; i0 += 8 * WAVE * SU) {
+          unsigned long long v[SU];
+#pragma unroll
+          for (int q = 0; q < SU; ++q) {
+            const int i = i0 + 8 * WAVE * q;
+            v[q] = get(reinterpret_cast<const unsigned long long*>(src + (i < arow ? i : 0)));
+          }
+#pragma unroll
+          for (int q = 0; q < SU; ++q) {
+            const int i = i0 + 8 * WAVE * q;
+            if (i < arow) *reinterpret_cast<unsigned long long*>(stage + i) = v[q];
+          }
+        }
+        wave_sync();
+        f32x4 acc[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
+        dec_stream<W, 1, DEC_DN_PF>(w, wn, again && fit, sb, ring, dec_row(stage, F), nl == 0, F, g, acc);
+        if (again && !fit) prime_stream<W, 1, DEC_DN_PF>(wn, sb, ring, F / 128);
+        if (g == 0) {
+          if (nsc == 1) S.ys[seq & 1][s][nl] = acc[0][0];
+          else put(p.y + (int64_t)s * L + 16 * rg + nl, acc[0][0]);
+        }
+        wave_sync();  // the next row may overwrite this one
+        w[0] = wn[0];
+        s = ns;
+        if (!second) break;
+      }
       if (nsc > 1) stores_done();
-      if (wave == 0) {
-        const int nx = downs.item();
-        if (lane == 0) S.ditem[par ^ 1] = nx;
+      if (nitem == -2) {  // no row of this item was the wave's
+        nitem = item_of(seq + 1);
+        s = slot_of(nitem);
+        if (s < n) {
+          w[0] = make(nitem, s);
+          prime_stream<W, 1, DEC_DN_PF>(w, sb, ring, F / 128);
+        }
       }
       lds_barrier();
-      ditem = S.ditem[par ^ 1];
       if (wave == 0) {
         // z[t][l] = bf16(sum_j w[t][j] y[t k + j][l]) in slot order, in fp64, once every slot's
         // outputs of these rows are there
@@ -726,7 +748,7 @@ __global__ void __launch_bounds__(DEC_THREADS) decode_kernel(DecodeArgs p) {
 #pragma unroll
               for (int u = 0; u < YU; ++u) {
                 const int sl = t * k + min(j0 + u, k - 1);
-                v[u] = nsc == 1 ? S.ys[par][sl][r] : get(p.y + (int64_t)sl * L + 16 * rg + r);
+                v[u] = nsc == 1 ? S.ys[seq & 1][sl][r] : get(p.y + (int64_t)sl * L + 16 * rg + r);
               }
 #pragma unroll
               for (int u = 0; u < YU; ++u)
@@ -736,7 +758,7 @@ __global__ void __launch_bounds__(DEC_THREADS) decode_kernel(DecodeArgs p) {
           }
         }
       }
-      par ^= 1;
+      ditem = nitem;
     }
   }
 
