@@ -121,24 +121,125 @@ struct Claims {
   }
 };
 
+// A weight stream as mfma_stream.h's, its addresses a wave-uniform base and a lane's 32-bit
+// offset: a step then costs scalar additions only.  The vector instructions per step are what
+// binds the down phase (1 KB of weights a step and stream) once loads are far enough ahead.
+struct DecW {
+  const uint8_t* c;  // codes
+  const uint8_t* s;  // scales
+};
+template <class W>
+struct DecLane;
+template <>
+struct DecLane<PackedW> {
+  uint32_t oc, os;
+  int nsc;
+  static constexpr int SIDE = 1;
+  __device__ __forceinline__ DecLane(int K, int lane) : oc(16 * lane), os(4 * lane), nsc((K / 128 + 3) / 4) {}
+  // 16 rows `grp` of matrix `mat` of expert e
+  __device__ __forceinline__ static DecW make(const uint8_t* blob, int e, int L, int F, int mat, int grp) {
+    const PackedW w = PackedW::make(blob, e, L, F, mat, grp, 0);
+    return {w.c, w.s};
+  }
+  __device__ __forceinline__ uint4 load(const DecW& w, int ks) const { return load_nt16(w.c + 1024 * ks + oc); }
+  __device__ __forceinline__ void sblock(const DecW& w, SBlock& b, int blk) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = 4 * blk + i;
+      const uint32_t v = *reinterpret_cast<const uint32_t*>(w.s + 256 * (t < nsc ? t : nsc - 1) + os);
+      b.d[i] = t < nsc ? v : 0x7F7F7F7Fu;
+    }
+  }
+  template <int J>
+  __device__ __forceinline__ uint32_t scale(const SBlock& b) const {
+    return b.d[J >> 2];
+  }
+};
+template <>
+struct DecLane<RecordW> {
+  uint32_t oc, os;
+  int nsb, n, g;
+  // a record's row gives 64 bytes a step: two steps' loads side by side read whole 128-byte lines
+  static constexpr int SIDE = 2;
+  __device__ __forceinline__ DecLane(int K, int lane)
+      : oc((lane & 15) * (K / 2) + 16 * (lane >> 4)), os((lane & 15) * (K / 32)), nsb(K / 32), n(lane & 15), g(lane >> 4) {}
+  __device__ __forceinline__ static DecW make(const uint8_t* blob, int e, int L, int F, int mat, int grp) {
+    const RecordW w = RecordW::make(blob, e, L, F, mat, grp, 0);
+    return {w.c, w.s};
+  }
+  __device__ __forceinline__ uint4 load(const DecW& w, int ks) const { return load_nt16(w.c + 64 * ks + oc); }
+  __device__ __forceinline__ void sblock(const DecW& w, SBlock& b, int blk) const {
+    const int off = 64 * blk + 16 * g;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int o = off + 4 * i;
+      const uint32_t v = *reinterpret_cast<const uint32_t*>(w.s + os + (uint32_t)(o < nsb ? o : nsb - 4));
+      b.d[i] = o < nsb ? v : 0x7F7F7F7Fu;
+    }
+  }
+  template <int J>
+  __device__ __forceinline__ uint32_t scale(const SBlock& b) const {
+    return (uint32_t)__shfl((int)b.d[J & 3], n + 16 * (J >> 2)) >> (8 * g);
+  }
+};
+template <int NS, int PF, class Ln>
+__device__ __forceinline__ void dec_prime(const Ln& ln, const DecW (&w)[NS], SBlock (&sb)[NS], uint4 (&ring)[NS][PF],
+                                          int nks) {
+#pragma unroll
+  for (int q = 0; q < NS; ++q) ln.sblock(w[q], sb[q], 0);
+#pragma unroll
+  for (int d = 0; d < PF; ++d)
+#pragma unroll
+    for (int q = 0; q < NS; ++q) ring[q][d] = ln.load(w[q], d < nks ? d : nks - 1);
+}
+
+// The activation operand of a lane: its tile row in the LDS, from 16 g on, or, for a row the
+// tile does not have, zeros that do not move on (DEC_ZEROS bytes of them: 16 K steps and the
+// second half of one), so that no step asks which it is.
+constexpr int DEC_ZEROS = 16 * 128 + 80;
+struct DecA {
+  const uint8_t *hi, *lo, *shi, *slo;
+  int on;
+  __device__ __forceinline__ DecA(bool on_, uint8_t* row, const uint8_t* zeros, int K, int g) : on(on_) {
+    hi = on_ ? row + 16 * g : zeros;
+    lo = on_ ? row + K + 16 * g : zeros;
+    shi = on_ ? row + 2 * K + g : zeros;
+    slo = on_ ? row + 2 * K + K / 32 + g : zeros;
+  }
+  __device__ __forceinline__ void advance() {  // by 16 K steps
+    hi += on ? 16 * 128 : 0;
+    lo += on ? 16 * 128 : 0;
+    shi += on ? 16 * 4 : 0;
+    slo += on ? 16 * 4 : 0;
+  }
+  template <int J>
+  __device__ __forceinline__ void read(AStep& a) const {
+    const uint4 h0 = *reinterpret_cast<const uint4*>(hi + 128 * J), h1 = *reinterpret_cast<const uint4*>(hi + 128 * J + 64);
+    const uint4 l0 = *reinterpret_cast<const uint4*>(lo + 128 * J), l1 = *reinterpret_cast<const uint4*>(lo + 128 * J + 64);
+    a.hi[0] = (int)h0.x; a.hi[1] = (int)h0.y; a.hi[2] = (int)h0.z; a.hi[3] = (int)h0.w;
+    a.hi[4] = (int)h1.x; a.hi[5] = (int)h1.y; a.hi[6] = (int)h1.z; a.hi[7] = (int)h1.w;
+    a.lo[0] = (int)l0.x; a.lo[1] = (int)l0.y; a.lo[2] = (int)l0.z; a.lo[3] = (int)l0.w;
+    a.lo[4] = (int)l1.x; a.lo[5] = (int)l1.y; a.lo[6] = (int)l1.z; a.lo[7] = (int)l1.w;
+    a.shi = shi[4 * J];
+    a.slo = slo[4 * J];
+  }
+};
+
 // stream_group with NS weight streams on one activation row group: acc[q] += A W_q^T over all K
-// steps, sb and ring filled by prime_stream.  With `chain` the ring goes on with the first
-// steps of wn as w's loads end, and wn's scales are in sb after, as prime_stream would leave
-// them (K / 128 a multiple of PF, so that the ring's slots fit).  Records take two steps'
-// loads at a time: a row of one gives 64 bytes a step, so two side by side read whole
-// 128-byte lines.
+// steps, sb and ring filled by dec_prime.  With `chain` the ring goes on with the first
+// steps of wn as w's loads end, and wn's scales are in sb after, as dec_prime would leave
+// them (K / 128 a multiple of PF, so that the ring's slots fit).
 template <class W, int NS, int PF>
-__device__ __forceinline__ void dec_stream(const W (&w)[NS], const W (&wn)[NS], bool chain, SBlock (&sb)[NS],
-                                           uint4 (&ring)[NS][PF], const ALds& ad, bool on, int K, int g,
-                                           f32x4 (&acc)[NS]) {
-  constexpr int SIDE = std::is_same<W, RecordW>::value ? 2 : 1;
+__device__ __forceinline__ void dec_stream(const DecLane<W>& ln, const DecW (&w)[NS], const DecW (&wn)[NS], bool chain,
+                                           SBlock (&sb)[NS], uint4 (&ring)[NS][PF], DecA ad, int K, f32x4 (&acc)[NS]) {
+  constexpr int SIDE = DecLane<W>::SIDE;
   const int nks = K / 128, nc = (nks + 15) / 16;
   SBlock sbn[NS];
   for (int c = 0; c < nc; ++c) {
 #pragma unroll
     for (int q = 0; q < NS; ++q) {
       const bool next = chain && c + 1 == nc;
-      (next ? wn[q] : w[q]).sblock(sbn[q], next ? 0 : c + 1 < nc ? c + 1 : c);
+      ln.sblock(next ? wn[q] : w[q], sbn[q], next ? 0 : c + 1 < nc ? c + 1 : c);
     }
     unroll_n<16 / SIDE>([&](auto jc) {
       constexpr int J2 = SIDE * decltype(jc)::value;
@@ -153,17 +254,17 @@ __device__ __forceinline__ void dec_stream(const W (&w)[NS], const W (&wn)[NS], 
           // that the ring's slot is for, or w's last again
           const int at = ks2 + h + PF;
           const bool next = chain && at >= nks;
-          ring[q][(J2 + h) % PF] = (next ? wn[q] : w[q]).load(next ? (at - nks) % PF : at < nks ? at : nks - 1);
+          ring[q][(J2 + h) % PF] = ln.load(next ? wn[q] : w[q], next ? (at - nks) % PF : at < nks ? at : nks - 1);
         }
       unroll_n<SIDE>([&](auto hc) {
         constexpr int H = decltype(hc)::value, J = J2 + H;
         const int ks = ks2 + H;
         if (ks < nks) {
           AStep a;
-          read_a(a, ad, on ? 0 : 1, 1, K, ks, g);
+          ad.template read<J>(a);
 #pragma unroll
           for (int q = 0; q < NS; ++q) {
-            const uint32_t sw = w[q].template scale<J>(sb[q]);
+            const uint32_t sw = ln.template scale<J>(sb[q]);
             const i32x8 b = as_b(cw[H][q]);
             acc[q] = mx_mfma<W::opsel(J)>(a.hi, b, acc[q], a.shi, sw);
             acc[q] = mx_mfma<W::opsel(J)>(a.lo, b, acc[q], a.slo, sw);
@@ -171,6 +272,7 @@ __device__ __forceinline__ void dec_stream(const W (&w)[NS], const W (&wn)[NS], 
         }
       });
     });
+    ad.advance();
 #pragma unroll
     for (int q = 0; q < NS; ++q) sb[q] = sbn[q];
   }
@@ -185,6 +287,7 @@ struct DecodeLds {
       float ys[2][DEC_SLOTS][16];                       // expert outputs of a down item, by slot
     };
   };
+  alignas(16) uint8_t zeros[DEC_ZEROS];
   uint32_t gmax[DEC_WAVES][WAVE];
   int wcnt[DEC_WAVES][16];
   float wup[DEC_WAVES];
@@ -502,6 +605,7 @@ __global__ void __launch_bounds__(DEC_THREADS) decode_kernel(DecodeArgs p) {
   ra.w = S.w;
   if (blockIdx.x != 0) ra.logits_out = nullptr;
   if (tid == 0) S.redo = 0u;  // read behind barriers
+  for (int i = tid; i < DEC_ZEROS / 4; i += DEC_THREADS) reinterpret_cast<uint32_t*>(S.zeros)[i] = 0u;
   auto ahead = [&]() {
     const int bytes = (slab1 - up0) * L * 2;
     for (int i = 1024 * wave; i < bytes; i += 1024 * DEC_WAVES)
@@ -563,20 +667,21 @@ __global__ void __launch_bounds__(DEC_THREADS) decode_kernel(DecodeArgs p) {
     }
   };
   {
-    W w[2], wn[2];
+    DecW w[2], wn[2];
     SBlock sb[2];
     uint4 ring[2][DEC_GU_PF];
+    const DecLane<W> ln(L, lane);
     const bool fit = (L / 128) % DEC_GU_PF == 0;
-    auto make = [&](W(&m)[2], const Half& x) {
+    auto make = [&](DecW(&m)[2], const Half& x) {
       const int grp = x.pair / nrb, r = 2 * (x.pair - grp * nrb) + x.h, e = __builtin_amdgcn_readfirstlane(S.gexp[grp]);
-      m[0] = W::make(p.blob, e, L, F, MAT_GATE, r, lane);
-      m[1] = W::make(p.blob, e, L, F, MAT_UP, r, lane);
+      m[0] = ln.make(p.blob, e, L, F, MAT_GATE, r);
+      m[1] = ln.make(p.blob, e, L, F, MAT_UP, r);
     };
     Half x, y;
     bool more = next_half(x);
     if (more) {
       make(w, x);
-      prime_stream<W, 2, DEC_GU_PF>(w, sb, ring, L / 128);
+      dec_prime(ln, w, sb, ring, L / 128);
     }
     while (more) {
       const int grp = x.pair / nrb, rb = x.pair - grp * nrb, nt = __builtin_amdgcn_readfirstlane(S.gn[grp]);
@@ -590,9 +695,9 @@ __global__ void __launch_bounds__(DEC_THREADS) decode_kernel(DecodeArgs p) {
       f32x4 acc[2];
 #pragma unroll
       for (int q = 0; q < 2; ++q) acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
-      dec_stream<W, 2, DEC_GU_PF>(w, wn, again && fit, sb, ring,
-                                  dec_row(smem + (on ? S.gslot[grp][nl] / k : 0) * hrow, L), on, L, g, acc);
-      if (again && !fit) prime_stream<W, 2, DEC_GU_PF>(wn, sb, ring, L / 128);
+      dec_stream<W, 2, DEC_GU_PF>(ln, w, wn, again && fit, sb, ring,
+                                  DecA(on, smem + (on ? S.gslot[grp][nl] / k : 0) * hrow, S.zeros, L, g), L, acc);
+      if (again && !fit) dec_prime(ln, wn, sb, ring, L / 128);
       // lane: row nl of the item, tokens 4 g + j of the expert
       const int ti = x.seq % DEC_TILES;
       while (__hip_atomic_load(&S.tile_of[ti], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) != x.seq)
@@ -650,9 +755,10 @@ __global__ void __launch_bounds__(DEC_THREADS) decode_kernel(DecodeArgs p) {
   };
   {
     const int n = T * k;
-    W w[1], wn[1];
+    DecW w[1], wn[1];
     SBlock sb[1];
     uint4 ring[1][DEC_DN_PF];
+    const DecLane<W> ln(F, lane);
     const bool fit = (F / 128) % DEC_DN_PF == 0;
     // the block's seq-th item: wave 0 has claimed it and says so in the LDS
     auto item_of = [&](int seq) -> int {
@@ -664,12 +770,12 @@ __global__ void __launch_bounds__(DEC_THREADS) decode_kernel(DecodeArgs p) {
     };
     auto slot_of = [&](int item) { return item < 0 ? n : DEC_SLOTS * (item / nrg) + wave; };
     auto make = [&](int item, int s) {
-      return W::make(p.blob, __builtin_amdgcn_readfirstlane(S.sel[s]), L, F, MAT_DOWN, item % nrg, lane);
+      return ln.make(p.blob, __builtin_amdgcn_readfirstlane(S.sel[s]), L, F, MAT_DOWN, item % nrg);
     };
     int ditem = item_of(0), s = slot_of(ditem);
     if (s < n) {
       w[0] = make(ditem, s);
-      prime_stream<W, 1, DEC_DN_PF>(w, sb, ring, F / 128);
+      dec_prime(ln, w, sb, ring, F / 128);
     }
 #pragma unroll
     for (int r = 0; r < UA; ++r) load_up(slab1 + wave + DEC_WAVES * r, r);
@@ -712,8 +818,8 @@ __global__ void __launch_bounds__(DEC_THREADS) decode_kernel(DecodeArgs p) {
         }
         wave_sync();
         f32x4 acc[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
-        dec_stream<W, 1, DEC_DN_PF>(w, wn, again && fit, sb, ring, dec_row(stage, F), nl == 0, F, g, acc);
-        if (again && !fit) prime_stream<W, 1, DEC_DN_PF>(wn, sb, ring, F / 128);
+        dec_stream<W, 1, DEC_DN_PF>(ln, w, wn, again && fit, sb, ring, DecA(nl == 0, stage, S.zeros, F, g), F, acc);
+        if (again && !fit) dec_prime(ln, wn, sb, ring, F / 128);
         if (g == 0) {
           if (nsc == 1) S.ys[seq & 1][s][nl] = acc[0][0];
           else put(p.y + (int64_t)s * L + 16 * rg + nl, acc[0][0]);
@@ -729,7 +835,7 @@ __global__ void __launch_bounds__(DEC_THREADS) decode_kernel(DecodeArgs p) {
         s = slot_of(nitem);
         if (s < n) {
           w[0] = make(nitem, s);
-          prime_stream<W, 1, DEC_DN_PF>(w, sb, ring, F / 128);
+          dec_prime(ln, w, sb, ring, F / 128);
         }
       }
       lds_barrier();
