@@ -72,6 +72,7 @@ __device__ __forceinline__ uint32_t fp4x2_to_bf16x2(uint32_t codes, float scale)
 
 // 16-byte load that does not allocate in the caches (streamed weights)
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint4 load_nt16(const void* p) {
   u32x4_t v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p));
   return make_uint4(v.x, v.y, v.z, v.w);
@@ -86,6 +87,8 @@ __device__ __forceinline__ uint4 load_nt16(const void* p) {
 
 constexpr int DPP_QUAD_1032 = 0xB1;   // quad_perm [1,0,3,2]
 constexpr int DPP_QUAD_2301 = 0x4E;   // quad_perm [2,3,0,1]
+constexpr int DPP_QUAD_3210 = 0x1B;   // quad_perm [3,2,1,0]
+constexpr int DPP_ROW_HALF_MIRROR = 0x141;  // lane l of eight: 7 - l
 constexpr int DPP_ROW_ROR4 = 0x124;
 constexpr int DPP_ROW_ROR8 = 0x128;
 constexpr int DPP_ROW_BCAST15 = 0x142;
@@ -157,6 +160,56 @@ __device__ __forceinline__ float wave_min_dpp(float v) {
   v = fminf(v, dpp_f32<DPP_ROW_BCAST15, 0xA>(v, hi));
   v = fminf(v, dpp_f32<DPP_ROW_BCAST31, 0xC>(v, hi));
   return readlane63(v);
+}
+
+// V sums over the 64 lanes at once (V a power of two): lane l returns the sum of v[l % V].  At
+// each of the first log2 V exchanges (lane bits 0, 1, ..) a lane keeps half of its values and
+// hands the other half over, so V sums take V - 1 + 6 - log2 V additions instead of 6 V.  The
+// additions of each sum are those of wave_sum_dpp, a tree over the lane bits from the lowest:
+// the results are the same bits.
+template <int BIT>
+__device__ __forceinline__ double lane_xor(double v) {  // lane l: v of lane l ^ BIT
+  static_assert(BIT == 1 || BIT == 2 || BIT == 4 || BIT == 8, "within a row of 16 lanes");
+  if constexpr (BIT == 1) return dpp_f64<DPP_QUAD_1032>(v, 0.0);
+  if constexpr (BIT == 2) return dpp_f64<DPP_QUAD_2301>(v, 0.0);
+  if constexpr (BIT == 4) return dpp_f64<DPP_ROW_HALF_MIRROR>(dpp_f64<DPP_QUAD_3210>(v, 0.0), 0.0);  // 7 ^ 3
+  return dpp_f64<DPP_ROW_ROR8>(v, 0.0);
+}
+template <int BIT>
+__device__ __forceinline__ double lane_xor_sum(double v) {  // v of lane l + v of lane l ^ BIT
+  if constexpr (BIT <= 8) {
+    return v + lane_xor<BIT>(v);
+  } else {  // the swaps give one operand the lanes with BIT clear, twice, the other those with it set
+    const uint2 a = __builtin_bit_cast(uint2, v);
+    u32x2_t x, y;
+    if constexpr (BIT == 16) {
+      x = __builtin_amdgcn_permlane16_swap(a.x, a.x, false, false);
+      y = __builtin_amdgcn_permlane16_swap(a.y, a.y, false, false);
+    } else {
+      x = __builtin_amdgcn_permlane32_swap(a.x, a.x, false, false);
+      y = __builtin_amdgcn_permlane32_swap(a.y, a.y, false, false);
+    }
+    return __builtin_bit_cast(double, make_uint2(x[0], y[0])) + __builtin_bit_cast(double, make_uint2(x[1], y[1]));
+  }
+}
+template <int V, int BIT = 1>
+__device__ __forceinline__ double wave_sums(double (&v)[V]) {
+  if constexpr (V == 1) {
+    return wave_sum_dpp(v[0]);
+  } else if constexpr (BIT < V) {
+    const bool up = (threadIdx.x & BIT) != 0;
+#pragma unroll
+    for (int i = 0; i < V / BIT / 2; ++i) {
+      const double keep = up ? v[2 * i + 1] : v[2 * i], give = up ? v[2 * i] : v[2 * i + 1];
+      v[i] = keep + lane_xor<BIT>(give);
+    }
+    return wave_sums<V, BIT * 2>(v);
+  } else if constexpr (BIT < WAVE) {
+    v[0] = lane_xor_sum<BIT>(v[0]);
+    return wave_sums<V, BIT * 2>(v);
+  } else {
+    return v[0];
+  }
 }
 
 // inclusive prefix sum over the 64 lanes: Hillis-Steele row shifts inside each row of

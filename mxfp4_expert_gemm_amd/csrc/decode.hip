@@ -578,13 +578,16 @@ __device__ __forceinline__ int dec_rank(const LoraSeg& l, int t, int& a) {
 
 // UC chunks of 512 latent columns cover an up row; a wave holds UA of them through the down
 // phase.
-template <class W, int UC, int UA>
+// ONE: one token.  Its phases run a few hundred instructions each and are met cold, so the code
+// for more tokens (the up phase's four at a time) costs it 2 us by its place alone: 87.7 us as a
+// kernel of its own against 89.9 (L 3584, packed), and nothing either way for two to eight.
+template <class W, int UC, int UA, bool ONE>
 __global__ void __launch_bounds__(DEC_THREADS) decode_kernel(DecodeArgs p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ DecodeLds S;
   const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
   const int nl = lane & 15, g = lane >> 4;
-  const int T = (int)p.r.T, k = p.r.k, L = p.r.L, F = p.F, d = p.r.d;
+  const int T = ONE ? 1 : (int)p.r.T, k = p.r.k, L = p.r.L, F = p.F, d = p.r.d;
   const int hrow = dec_row_bytes(L), arow = dec_row_bytes(F);
   uint8_t* stage = smem + p.stage_offset + wave * arow;
 
@@ -938,57 +941,77 @@ __global__ void __launch_bounds__(DEC_THREADS) decode_kernel(DecodeArgs p) {
     for (int i = tid; i < T * R; i += DEC_THREADS) ul[i] = __uint_as_float(await32(p.u + i));
     lds_barrier();
   }
-  // NR rows, DEC_WAVES apart, for every token: weights(r, q) is chunk q of the r-th
-  auto rows_up = [&](int row0, int end, auto nr, auto&& weights) {
-    constexpr int NR = decltype(nr)::value;
-    for (int t = 0; t < T; ++t) {
-      double acc[NR];
+  // NR rows, DEC_WAVES apart, for every token, TP at a time: weights(r, q) is chunk q of the r-th
+  auto rows_up = [&](int row0, int end, auto nr, auto tp, auto&& weights) {
+    constexpr int NR = decltype(nr)::value, TP = decltype(tp)::value;
+    for (int t0 = 0; t0 < T; t0 += TP) {
+      double acc[NR * TP];
 #pragma unroll
-      for (int r = 0; r < NR; ++r) acc[r] = 0.0;
+      for (int i = 0; i < NR * TP; ++i) acc[i] = 0.0;
 #pragma unroll
       for (int q = 0; q < UC; ++q) {
         const int col = 8 * (WAVE * q + lane);
         if (col < L) {
-          const uint4 x = *reinterpret_cast<const uint4*>(zs + t * L + col);
+          uint4 v[NR];
 #pragma unroll
-          for (int r = 0; r < NR; ++r) {
-            const uint4 v = weights(r, q);
-            float s = dot2(x.x, v.x, 0.f);
-            s = dot2(x.y, v.y, s);
-            s = dot2(x.z, v.z, s);
-            s = dot2(x.w, v.w, s);
-            acc[r] += (double)s;
-          }
+          for (int r = 0; r < NR; ++r) v[r] = weights(r, q);
+#pragma unroll
+          for (int t = 0; t < TP; ++t)
+            if (TP == 1 || t0 + t < T) {
+              const uint4 x = *reinterpret_cast<const uint4*>(zs + (t0 + t) * L + col);
+#pragma unroll
+              for (int r = 0; r < NR; ++r) {
+                float s = dot2(x.x, v[r].x, 0.f);
+                s = dot2(x.y, v[r].y, s);
+                s = dot2(x.z, v[r].z, s);
+                s = dot2(x.w, v[r].w, s);
+                acc[r * TP + t] += (double)s;
+              }
+            }
         }
       }
-      if (lora) {
-        int a;
-        const int rk = dec_rank(p.lora, t, a);
+      if (lora)
+#pragma unroll
+        for (int t = 0; t < TP; ++t)
+          if (TP == 1 || t0 + t < T) {
+            int a;
+            const int rk = dec_rank(p.lora, t0 + t, a);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+              const int row = min(row0 + DEC_WAVES * r, end - 1);
+              const uint16_t* B = bfit ? bl + ((row - up0) * T + t0 + t) * R : p.lora.B + ((int64_t)a * d + row) * R;
+              for (int i = lane; i < rk; i += WAVE)
+                acc[r * TP + t] += (double)ul[(t0 + t) * R + i] * (double)bf16f(B[i]);
+            }
+          }
+      if constexpr (TP == 1) {
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-          const int row = min(row0 + DEC_WAVES * r, end - 1);
-          const uint16_t* B = bfit ? bl + ((row - up0) * T + t) * R : p.lora.B + ((int64_t)a * d + row) * R;
-          for (int i = lane; i < rk; i += WAVE) acc[r] += (double)ul[t * R + i] * (double)bf16f(B[i]);
+          const double v = wave_sum_dpp(acc[r]);
+          if (lane == 0 && row0 + DEC_WAVES * r < end)
+            p.out[(int64_t)t0 * d + row0 + DEC_WAVES * r] = f64_to_bf16(v);
         }
-      }
-#pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        const double v = wave_sum_dpp(acc[r]);
-        if (lane == 0 && row0 + DEC_WAVES * r < end) p.out[(int64_t)t * d + row0 + DEC_WAVES * r] = f64_to_bf16(v);
+      } else {
+        const double v = wave_sums<NR * TP>(acc);  // lane r TP + t
+        const int row = row0 + DEC_WAVES * (lane / TP), t = t0 + lane % TP;
+        if (lane < NR * TP && row < end && t < T) p.out[(int64_t)t * d + row] = f64_to_bf16(v);
       }
     }
   };
-  for (int row = slab1 + wave; row < up1; row += DEC_WAVES * UA) {
-    rows_up(row, up1, std::integral_constant<int, UA>{}, [&](int r, int q) { return wr[r][q]; });
-    if (row + DEC_WAVES * UA < up1)
+  auto up_all = [&](auto tp) {
+    for (int row = slab1 + wave; row < up1; row += DEC_WAVES * UA) {
+      rows_up(row, up1, std::integral_constant<int, UA>{}, tp, [&](int r, int q) { return wr[r][q]; });
+      if (row + DEC_WAVES * UA < up1)
 #pragma unroll
-      for (int r = 0; r < UA; ++r) load_up(row + DEC_WAVES * (UA + r), r);
-  }
-  for (int row = up0 + wave; row < slab1; row += DEC_WAVES * 2)
-    rows_up(row, slab1, std::integral_constant<int, 2>{}, [&](int r, int q) {
-      const int at = min(row + DEC_WAVES * r, slab1 - 1) - up0;
-      return *reinterpret_cast<const uint4*>(slab + at * L + 8 * (WAVE * q + lane));
-    });
+        for (int r = 0; r < UA; ++r) load_up(row + DEC_WAVES * (UA + r), r);
+    }
+    for (int row = up0 + wave; row < slab1; row += DEC_WAVES * 2)
+      rows_up(row, slab1, std::integral_constant<int, 2>{}, tp, [&](int r, int q) {
+        const int at = min(row + DEC_WAVES * r, slab1 - 1) - up0;
+        return *reinterpret_cast<const uint4*>(slab + at * L + 8 * (WAVE * q + lane));
+      });
+  };
+  up_all(std::integral_constant<int, ONE ? 1 : 4>{});
 }
 
 // ------------------------------------------------------------------------- host
@@ -1006,14 +1029,22 @@ static int cu_count() {
   return n;
 }
 
-template <class W, int UC, int UA>
+template <class W, int UC, int UA, bool ONE>
 static hipError_t launch_decode_as(const DecodeArgs& a, unsigned grid, size_t lds, hipStream_t st) {
   static const hipError_t e =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(&decode_kernel<W, UC, UA>),
+      hipFuncSetAttribute(reinterpret_cast<const void*>(&decode_kernel<W, UC, UA, ONE>),
                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)DEC_LDS);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((decode_kernel<W, UC, UA>), dim3(grid), dim3(DEC_THREADS), lds, st, a);
+  hipLaunchKernelGGL((decode_kernel<W, UC, UA, ONE>), dim3(grid), dim3(DEC_THREADS), lds, st, a);
   return hipGetLastError();
+}
+
+template <class W>
+static hipError_t launch_decode_for(const DecodeArgs& a, unsigned grid, size_t lds, hipStream_t st) {
+  const bool wide = a.r.L > 7 * 512;
+  if (a.r.T == 1)
+    return wide ? launch_decode_as<W, 14, 1, true>(a, grid, lds, st) : launch_decode_as<W, 7, 2, true>(a, grid, lds, st);
+  return wide ? launch_decode_as<W, 14, 1, false>(a, grid, lds, st) : launch_decode_as<W, 7, 2, false>(a, grid, lds, st);
 }
 
 hipError_t launch_decode(const DecodeArgs& args, bool packed, hipStream_t st) {
@@ -1039,9 +1070,7 @@ hipError_t launch_decode(const DecodeArgs& args, bool packed, hipStream_t st) {
   const int64_t slab = (int64_t)((DEC_LDS - used) / ((size_t)L * 2));
   a.slab_rows = (int32_t)(slab < a.up_rows ? slab : a.up_rows);
   const size_t lds = used + (size_t)a.slab_rows * L * 2;
-  const bool wide = L > 7 * 512;
-  if (packed) return wide ? launch_decode_as<PackedW, 14, 1>(a, grid, lds, st) : launch_decode_as<PackedW, 7, 2>(a, grid, lds, st);
-  return wide ? launch_decode_as<RecordW, 14, 1>(a, grid, lds, st) : launch_decode_as<RecordW, 7, 2>(a, grid, lds, st);
+  return packed ? launch_decode_for<PackedW>(a, grid, lds, st) : launch_decode_for<RecordW>(a, grid, lds, st);
 }
 
 }  // namespace moe

@@ -44,7 +44,7 @@ struct DenseParams {
 // LORA: the last segment's rows also take their adapters' term, sum_r B[a_t][row][r] u[t][r].
 // Lane l holds ranks l and l + 64 of each token; the products (exact in fp64) join the lane's
 // fp64 sum before the wave reduction, so the term costs two loads a lane and token, issued
-// before the weight row's, and no rounding of its own.
+// behind the weight row's (they wait for the adapter's id and rank), and no rounding of its own.
 template <int NCH, int G, bool LORA>
 __global__ void __launch_bounds__(256) dense_gemv_kernel(DenseParams p) {
   constexpr int XN = G * NCH * 64;            // 16-byte pieces of the block's token rows
@@ -80,6 +80,14 @@ __global__ void __launch_bounds__(256) dense_gemv_kernel(DenseParams p) {
     xv[u] = *reinterpret_cast<const uint4*>(p.x + t * K + (col < K ? col : 0));
     if (col >= K || t0 + g >= p.T) xv[u] = make_uint4(0, 0, 0, 0);
   }
+  uint4 wr[NCH];
+  const uint16_t* wrow = s.W + row * K;
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    const int col = 8 * (64 * c + lane);
+    wr[c] = load_nt16(wrow + (col < K ? col : 0));
+    if (col >= K) wr[c] = make_uint4(0, 0, 0, 0);
+  }
   uint16_t lb[LORA ? G : 1][2];
   float lu[LORA ? G : 1][2];
   if constexpr (LORA) {
@@ -101,14 +109,6 @@ __global__ void __launch_bounds__(256) dense_gemv_kernel(DenseParams p) {
         }
       }
     }
-  }
-  uint4 wr[NCH];
-  const uint16_t* wrow = s.W + row * K;
-#pragma unroll
-  for (int c = 0; c < NCH; ++c) {
-    const int col = 8 * (64 * c + lane);
-    wr[c] = load_nt16(wrow + (col < K ? col : 0));
-    if (col >= K) wr[c] = make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
   for (int u = 0; u < XPT; ++u)
@@ -139,13 +139,10 @@ __global__ void __launch_bounds__(256) dense_gemv_kernel(DenseParams p) {
         for (int h = 0; h < 2; ++h) acc[g] += (double)lu[g][h] * (double)bf16f(lb[g][h]);
     }
     uint16_t* out = reinterpret_cast<uint16_t*>(s.out);
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      double v = wave_sum_dpp(acc[g]);
-      if (valid && lane == 0 && t0 + g < p.T) {
-        for (int a = 0; a < s.add_rows; ++a) v += (double)s.add[((t0 + g) * s.add_rows + a) * s.rows + row];
-        out[(t0 + g) * s.rows + row] = f64_to_bf16(v);
-      }
+    double v = wave_sums<G>(acc);  // lane g: token g
+    if (valid && lane < G && t0 + lane < p.T) {
+      for (int a = 0; a < s.add_rows; ++a) v += (double)s.add[((t0 + lane) * s.add_rows + a) * s.rows + row];
+      out[(t0 + lane) * s.rows + row] = f64_to_bf16(v);
     }
     return;
   }
@@ -175,11 +172,8 @@ __global__ void __launch_bounds__(256) dense_gemv_kernel(DenseParams p) {
     }
   }
   float* out = reinterpret_cast<float*>(s.out);
-#pragma unroll
-  for (int g = 0; g < G; ++g) {
-    double v = wave_sum_dpp(acc[g]);
-    if (valid && lane == 0 && t0 + g < p.T) out[(t0 + g) * s.rows + row] = (float)v;
-  }
+  const double logit = wave_sums<G>(acc);  // lane g: token g
+  if (valid && lane < G && t0 + lane < p.T) out[(t0 + lane) * s.rows + row] = (float)logit;
   wn = wave_sum_dpp(wn);
   const bool wany = __any(wsub != 0u);
   if (valid && lane == 0 && blockIdx.y == 0) s.wnorm[row] = wany ? __builtin_inff() : sqrtf(wn);
@@ -220,11 +214,10 @@ static hipError_t launch_nch_g(const DenseParams& p, hipStream_t st) {
 template <int NCH>
 static hipError_t launch_nch(const DenseParams& p, hipStream_t st) {
   // tokens per block: a weight row is read once for G of them (results do not depend on it).
-  // Four from three tokens on, where a row is long enough that reading it twice costs more
-  // than the unused fourth (4480 x 7168: 4 tokens 36 us with one a block, 19.4 with four;
-  // 3 tokens 28 and 20.5; 1024 x 2048: 3 tokens 3.4 with two, 3.8 with four), else two
-  // (4480 x 7168: 2 tokens 19.7 and 13.5 us).
-  if (p.T >= 4 || (p.T == 3 && NCH > 4)) return launch_nch_g<NCH, 4>(p, st);
+  // Four from three tokens on, the fourth unused if need be (4480 x 7168: 4 tokens 36 us with
+  // one a block, 18.0 with four; 3 tokens 28 and 19.6; 1024 x 2048: 3 tokens 3.7 with two, 3.4
+  // with four), else two (4480 x 7168: 2 tokens 19.7 and 13.2 us).
+  if (p.T >= 3) return launch_nch_g<NCH, 4>(p, st);
   if (p.T >= 2) return launch_nch_g<NCH, 2>(p, st);
   return launch_nch_g<NCH, 1>(p, st);
 }
