@@ -68,49 +68,84 @@ __device__ __forceinline__ u32x4_t keep_ranks(u32x4_t v, int valid) {
 }
 
 // The adapters' term of a wave's tile (16 WM tokens from tb, 16 WN rows from nb), added to
-// its accumulators: per 16 tokens, each adapter met among them multiplies all 16 rows of u
-// by its B (hi and lo terms of u: 16 significant bits, against the 8 of the output), and
-// the rows that name it take the product.  Taken by a select, not by zeroed operands: an
-// infinity in one request's adapter must not reach another request's row.  Tokens of one
-// request usually stand together, so most tiles meet one adapter or two.
+// its accumulators: each adapter met among the tokens multiplies, per 16 tokens that hold one
+// of its own, all 16 rows of u by its B (hi and lo terms of u: 16 significant bits, against
+// the 8 of the output), and the rows that name it take the product.  Taken by a select, not by
+// zeroed operands: an infinity in one request's adapter must not reach another request's row.
+// What it costs is the wait for B, 16 bytes a lane from the L2 or further: the pieces of U
+// adapters are loaded together, four but for 64 rows a wave, where two spill 26 registers
+// (4096 tokens, 32 adapters of rank 32, 3584 -> 7168: 503 us, one 444; one adapter on each run
+// of tokens: 279 and 251).  Tokens of one request usually stand together, so most tiles meet
+// one adapter or two; a batch of single tokens can bring a new one with each (512 -> 256, 256
+// tokens with 64 adapters: 81.6 us when every 16 tokens fetched their adapters one by one in
+// tiles of 128 x 128, 14.7 now).
 template <int WM, int WN>
 __device__ __forceinline__ void lora_expand(const DenseMfmaArgs& p, int64_t tb, int nb, f32x4_t (&acc)[WM][WN]) {
+  constexpr int U = WN == 4 ? 1 : 4;
   const LoraSeg& l = p.lora;
   const int lane = lane_id(), nl = lane & 15, g = lane >> 4;
   const int RP = rank_pad(l.R);
+  int64_t tc[WM];
 #pragma unroll
-  for (int i = 0; i < WM; ++i) {
-    const int64_t t = tb + 16 * i + nl;
-    const int64_t tc = t < p.T ? t : p.T - 1;
-    int a = l.adapter[tc];
-    if (t >= p.T || (uint32_t)a >= (uint32_t)l.N) a = -1;
-    for (uint32_t todo = (uint32_t)__ballot(a >= 0) & 0xFFFFu; todo;) {
-      const int ad = __builtin_amdgcn_readlane(a, __ffs((int)todo) - 1);
-      const uint32_t same = (uint32_t)__ballot(a == ad) & 0xFFFFu;
-      todo &= ~same;
-      const int rk = l.rank ? min(l.rank[ad], l.R) : l.R;
-      const uint16_t* B = l.B + (int64_t)ad * p.N * l.R;
-      f32x4_t d[WN];
+  for (int i = 0; i < WM; ++i) tc[i] = min(tb + 16 * i + nl, p.T - 1);
+  int a = -1;  // lane: token tb + lane
+  if (lane < 16 * WM && tb + lane < p.T) a = l.adapter[tb + lane];
+  for (unsigned long long todo = __ballot((uint32_t)a < (uint32_t)l.N); todo;) {
+    unsigned long long same[U];
+    int rk[U], top = 0;
+    const uint16_t* B[U];
 #pragma unroll
-      for (int jn = 0; jn < WN; ++jn) d[jn] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      for (int r0 = 0; r0 < rk; r0 += 32) {
-        const int r = r0 + 8 * g;
-        const bf16x8_t hi = *reinterpret_cast<const bf16x8_t*>(l.uhi + tc * RP + r);
-        const bf16x8_t lo = *reinterpret_cast<const bf16x8_t*>(l.ulo + tc * RP + r);
+    for (int u = 0; u < U; ++u) {
+      same[u] = 0;
+      rk[u] = 0;
+      B[u] = l.B;
+      if (todo) {
+        const int ad = __builtin_amdgcn_readlane(a, __ffsll((long long)todo) - 1);
+        same[u] = __ballot(a == ad);
+        todo &= ~same[u];
+        rk[u] = l.rank ? min(l.rank[ad], l.R) : l.R;
+        B[u] = l.B + (int64_t)ad * p.N * l.R;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) top = max(top, rk[u]);
+    for (int r0 = 0; r0 < top; r0 += 32) {
+      const int r = r0 + 8 * g;
+      u32x4_t b[U][WN];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int jn = 0; jn < WN; ++jn) {
-          const int n = nb + 16 * jn + nl < p.N ? nb + 16 * jn + nl : p.N - 1;
-          u32x4_t v = {0u, 0u, 0u, 0u};
-          if (r < rk) v = keep_ranks(*reinterpret_cast<const u32x4_t*>(B + (int64_t)n * l.R + r), rk - r);
-          const bf16x8_t b = __builtin_bit_cast(bf16x8_t, v);
-          d[jn] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, b, d[jn], 0, 0, 0);
-          d[jn] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, b, d[jn], 0, 0, 0);
+          const int n = min(nb + 16 * jn + nl, p.N - 1);
+          b[u][jn] = u32x4_t{0u, 0u, 0u, 0u};
+          if (r < rk[u]) b[u][jn] = *reinterpret_cast<const u32x4_t*>(B[u] + (int64_t)n * l.R + r);
         }
+      bf16x8_t hi[WM], lo[WM];
+#pragma unroll
+      for (int i = 0; i < WM; ++i) {
+        hi[i] = *reinterpret_cast<const bf16x8_t*>(l.uhi + tc[i] * RP + r);
+        lo[i] = *reinterpret_cast<const bf16x8_t*>(l.ulo + tc[i] * RP + r);
       }
 #pragma unroll
-      for (int jn = 0; jn < WN; ++jn)
+      for (int u = 0; u < U; ++u) {
+        if (r0 >= rk[u]) continue;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][jn][j] += (same >> (4 * g + j)) & 1u ? d[jn][j] : 0.f;
+        for (int jn = 0; jn < WN; ++jn) b[u][jn] = keep_ranks(b[u][jn], rk[u] - r);
+#pragma unroll
+        for (int i = 0; i < WM; ++i) {
+          const uint32_t rows = (uint32_t)(same[u] >> (16 * i)) & 0xFFFFu;
+          if (!rows) continue;
+#pragma unroll
+          for (int jn = 0; jn < WN; ++jn) {
+            const bf16x8_t v = __builtin_bit_cast(bf16x8_t, b[u][jn]);
+            f32x4_t d = {0.f, 0.f, 0.f, 0.f};
+            d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi[i], v, d, 0, 0, 0);
+            d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo[i], v, d, 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][jn][j] += (rows >> (4 * g + j)) & 1u ? d[j] : 0.f;
+          }
+        }
+      }
     }
   }
 }
@@ -488,7 +523,15 @@ static hipError_t launch_dm_dma(const DenseMfmaArgs& a0, hipStream_t st) {
 // the second for smaller grids (prefill4k's router, 448 blocks: 0.12 against 0.14 ms).
 static bool dm_dma_pays(int64_t T, int32_t N, int BM, int BN) { return ceil_div(T, BM) * ceil_div(N, BN) >= 768; }
 
-// Tile of a batch below 256 tokens: the largest of 64 x 64, 64 x 32 and 32 x 32 (tokens x
+// Blocks from which a projection takes tiles of 128 x 128, a block and a half per CU: below,
+// the smaller tiles' grid fills more of the chip than their extra reads cost (with an adapter
+// of rank 16 on each token, four in turn; 7168 -> 3584: 256 tokens, 56 blocks, 98.5 us and with
+// the smaller tiles 45.1; 512 tokens, 112 blocks, 109.6 and 70.9; 1536, 336 blocks, 153 and 157;
+// 2048, 448 blocks, 162 and 188; 3584 -> 7168: 256 tokens 59.7 and 36.7; 768, 336 blocks, 91.6
+// and 89.2; 1024, 448 blocks, 92.9 and 102.7).
+constexpr int64_t DM_BIG_BLOCKS = 384;
+
+// Tile of a smaller batch: the largest of 64 x 64, 64 x 32 and 32 x 32 (tokens x
 // rows) that still gives the grid about one block per CU, since a few dozen blocks (the
 // router at 64 tokens has 14 tiles of 64 x 64) leave most of the chip idle.  Every shape
 // runs the same K-tile arithmetic, so the results do not depend on the choice.
@@ -501,7 +544,7 @@ static int small_tile(int64_t T, int32_t N) {
 // the latent projections, with the adapters' term or without
 template <bool LORA>
 static hipError_t launch_projection(const DenseMfmaArgs& a, hipStream_t st) {
-  if (a.T >= 256)
+  if (ceil_div(a.T, 128) * ceil_div(a.N, 128) >= DM_BIG_BLOCKS)
     return dm_dma_pays(a.T, a.N, 128, 128) ? launch_dm_dma<4, 4, false, 2, LORA>(a, st)
                                            : launch_dm<4, 4, 2, false, LORA>(a, st);
   switch (small_tile(a.T, a.N)) {
