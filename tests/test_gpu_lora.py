@@ -31,8 +31,8 @@ def check(got, x, W, lo, ids, rank, what):
 
 # T, n_in, n_out, adapters, max rank, order, ragged ranks.  Below 32 tokens (or n_in no
 # multiple of 64) the GEMV with 4, 2 or 1 tokens a block; from 32 the small matrix-core tiles,
-# from 256 the 128 x 128 ones, and the LDS-direct ones from 768 tiles; the first product by
-# rows up to 4096 (token, rank) pairs, grouped above.
+# the 128 x 128 ones from 384 of them on, and the LDS-direct ones from 768; the first product
+# by rows up to 512 tokens and 16384 (token, rank) pairs, grouped above.
 CASES = [
     (1, 32, 1, 1, 8, "mixed", False),
     (1, 7168, 3584, 3, 16, "mixed", True),
@@ -51,6 +51,11 @@ CASES = [
     (300, 96, 129, 300, 128, "mixed", True),
     (1021, 640, 1100, 5, 128, "segments", True),
     (1000, 2560, 96, 40, 56, "mixed", True),
+    (200, 192, 130, 20, 128, "segments", True),
+    (512, 320, 257, 33, 32, "mixed", True),
+    (513, 320, 257, 33, 8, "mixed", False),
+    (1500, 320, 5000, 9, 40, "segments", True),
+    (2049, 128, 3201, 600, 128, "mixed", True),
     (4096, 128, 3201, 1000, 16, "mixed", True),
     (4099, 576, 3250, 6, 96, "segments", True),
 ]
