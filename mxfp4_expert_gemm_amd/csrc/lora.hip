@@ -21,7 +21,7 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int LT_TOK = 64;       // tokens per matrix-core tile
 constexpr int LT_SLICES = 8;     // at most so many K slices
-constexpr int LT_MIN_K = 512;    // at least so much K per slice
+constexpr int LT_MIN_K = 256;    // at least so much K per slice
 
 struct LoraWs {
   float* u;         // [T][R]
@@ -186,17 +186,22 @@ __global__ void __launch_bounds__(1024) lora_group_kernel(const int32_t* __restr
   });
 }
 
-// Tile blockIdx.x, K slice blockIdx.y: wave w has tokens 16w .. 16w+15 of the tile and all
-// RB blocks of 16 ranks.  Operands come straight from global memory in the instruction's
-// order (lane l: row l%16, eight K values of block l/16): the tile's token rows are read
-// once, the adapter's rows by four waves through the L1.
+// Tile blockIdx.x, K slice blockIdx.y, ranks from 16 RB blockIdx.z: wave w has tokens
+// 16w .. 16w+15 of the tile and all RB blocks of 16 ranks.  Operands come straight from global memory in the instruction's
+// order (lane l: row l%16, eight K values of block l/16): a block of ranks reads the tile's
+// token rows once, the adapter's rows by four waves through the L1.  A wave has up to 24 KB
+// of loads under way, 16 rows of 64 bytes each, and their latency is what bounds it: 41 us at
+// 4096 x 7168, rank 32 (59 MB of x: 1.4 TB/s), of 283 with the projection.  Blocks of 16,
+// 32, 64 or 128 ranks, 8 or 16 slices and 256 or 512 of K at least are within 5% of each other in
+// the whole projection; 32 and 256 were never behind (600 tokens of rank 64, 3584 -> 7168: 82.6
+// against 86.8 us with 64 and 512).
 template <int RB>
 __global__ void __launch_bounds__(256) lora_shrink_mfma_kernel(LoraArgs p, LoraWs w, int slices) {
   if ((int)blockIdx.x >= *w.ntiles) return;
   const int4 tile = w.tiles[blockIdx.x];
   const int lane = lane_id(), wave = threadIdx.x / WAVE, nl = lane & 15, g = lane >> 4;
   if (16 * wave >= tile.z) return;
-  const int rk = token_rank(p, tile.x);
+  const int rk = token_rank(p, tile.x), rank0 = 16 * RB * blockIdx.z;
   const int row = 16 * wave + nl;
   const int64_t t = w.perm[tile.y + (row < tile.z ? row : tile.z - 1)];
   // slices are whole steps of 32
@@ -206,13 +211,13 @@ __global__ void __launch_bounds__(256) lora_shrink_mfma_kernel(LoraArgs p, LoraW
   const uint16_t* A[RB];
 #pragma unroll
   for (int b = 0; b < RB; ++b) {
-    const int r = min(16 * b + nl, p.R - 1);
+    const int r = min(rank0 + 16 * b + nl, p.R - 1);
     A[b] = p.A + ((int64_t)tile.x * p.R + r) * p.K + 8 * g;
   }
   f32x4_t acc[RB];
 #pragma unroll
   for (int b = 0; b < RB; ++b) acc[b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  constexpr int U = RB <= 2 ? 8 : RB <= 4 ? 4 : 2;  // steps in flight
+  constexpr int U = 8;  // steps in flight
   for (int s = s0; s < s1; s += U) {
     bf16x8_t xv[U], av[U][RB];
 #pragma unroll
@@ -237,8 +242,10 @@ __global__ void __launch_bounds__(256) lora_shrink_mfma_kernel(LoraArgs p, LoraW
     if (m >= tile.z) continue;
     const int64_t tm = w.perm[tile.y + m];
 #pragma unroll
-    for (int b = 0; b < RB; ++b)
-      if (16 * b + nl < p.R) out[tm * p.R + 16 * b + nl] = 16 * b + nl < rk ? acc[b][j] : 0.f;
+    for (int b = 0; b < RB; ++b) {
+      const int r = rank0 + 16 * b + nl;
+      if (r < p.R) out[tm * p.R + r] = r < rk ? acc[b][j] : 0.f;
+    }
   }
 }
 
@@ -262,7 +269,7 @@ __global__ void __launch_bounds__(256) lora_join_kernel(LoraArgs p, LoraWs w, in
 
 template <int RB>
 static void launch_shrink_mfma(const LoraArgs& a, const LoraWs& w, int slices, hipStream_t st) {
-  const dim3 grid((unsigned)lora_max_tiles(a.T, a.N), (unsigned)slices);
+  const dim3 grid((unsigned)lora_max_tiles(a.T, a.N), (unsigned)slices, (unsigned)ceil_div(a.R, 16 * RB));
   hipLaunchKernelGGL(lora_shrink_mfma_kernel<RB>, grid, dim3(256), 0, st, a, w, slices);
 }
 
@@ -286,12 +293,10 @@ hipError_t launch_lora_shrink(const LoraArgs& a, void* ws, LoraSeg* seg, hipStre
   }
   const int slices = lora_slices(a.T, a.K, a.N);
   hipLaunchKernelGGL(lora_group_kernel, dim3(1), dim3(1024), 0, st, a.adapter, a.T, a.N, w.perm, w.tiles, w.ntiles);
-  switch ((a.R + 15) / 16) {
-    case 1: launch_shrink_mfma<1>(a, w, slices, st); break;
-    case 2: launch_shrink_mfma<2>(a, w, slices, st); break;
-    case 3: case 4: launch_shrink_mfma<4>(a, w, slices, st); break;
-    default: launch_shrink_mfma<8>(a, w, slices, st); break;
-  }
+  if (a.R <= 16)
+    launch_shrink_mfma<1>(a, w, slices, st);
+  else
+    launch_shrink_mfma<2>(a, w, slices, st);
   int64_t blocks = ceil_div(a.T * rank_pad(a.R), 256);
   if (blocks > 4096) blocks = 4096;
   hipLaunchKernelGGL(lora_join_kernel, dim3((unsigned)blocks), dim3(256), 0, st, a, w, slices);
