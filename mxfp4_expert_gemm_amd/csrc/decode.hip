@@ -27,9 +27,27 @@
 // and per row group.  What one wave hands to another is written through to the memory side
 // (agent-scope stores), and, where it is counted, waited for before; the reader's loads are
 // agent-scope too.  A hand-over takes 0.8 us.  z and the adapters' u need no count: their
-// words start as all ones, which none of them can be (a bf16 NaN here is 0x7FC0, and an fp32
-// NaN's low bits are zeros), and a reader asks again until a word is another.  The launch
+// words start as all ones, which none of them can be (a NaN is written as 0x7FC0 or
+// 0x7FC00000), and a reader asks again until a word is another.  The launch
 // before sets counters and words.
+//
+// Measured (7168-wide tokens, latent 3584, FFN 3072, 16 of 896 experts; packed experts but where
+// records are named).  One token reads 397 MB in 87.7 us, 4.5 TB/s: 12.7 us the first launch;
+// in the second the routing and the first chunk end at 10.5, a block's gate / up at 40 in the
+// median and 53 at the latest, its down at 63 and 69, z is there at 71, and the up rows, which
+// are on chip by then, take 3.  The first 10 us and the last 5 stream little, the blocks' spread
+// at the two hand-overs costs as much again: that is what bounds it.  Against the five launches
+// of moe_layer_forward, in graphs on one card, here / there in us:
+//   tokens                    1           2           3           4
+//   packed experts         90.3 / 80.8  150 / 141   208 / 196   256 / 233
+//   checkpoint records      120 / 117   197 / 208   278 / 299   335 / 368
+// and eight MXFP8 tokens of a middle layer (2048, 1024, 512, 8 of 64, packed) 53.6 / 57.5, one
+// token of it 31.2 / 23.8, four of a tiny layer over records 27.4 / 27.3, one over packed experts
+// 22.9 / 21.1.  So it is for records, for many rows of few experts, and where five launches
+// cost the host more than the card; several blocks a CU, which cover one another's spread, are
+// worth more than three launches where the packed streams set the pace.
+// Slower: a wave per down item; the latent rows and the routing in this launch too; more steps in
+// flight per stream; counters without shards (one token 125 us).
 //
 // The arithmetic of every value is that of the kernels moe_layer_forward runs on a batch of
 // this size (dense_gemv_kernel, the routing, stream_group, the fp64 combine), in the same
@@ -935,7 +953,8 @@ __global__ void __launch_bounds__(DEC_THREADS) decode_kernel(DecodeArgs p) {
         }
         v = (float)(wave_sum_dpp(acc) * (double)p.lora_scale[a]);
       }
-      if (lane == 0) put(p.u + ui, __float_as_uint(v));
+      // a NaN with a payload (a scale's) must not become the word that means "not there yet"
+      if (lane == 0) put(p.u + ui, v != v ? 0x7FC00000u : __float_as_uint(v));
       load_a();
     }
     for (int i = tid; i < T * R; i += DEC_THREADS) ul[i] = __uint_as_float(await32(p.u + i));

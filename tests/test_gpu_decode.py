@@ -144,6 +144,16 @@ def test_ties_and_pruned_experts(T):
     same_as_forward(layer)
 
 
+@pytest.mark.parametrize("word", [-1, 0x7FFFFFFF, 0x7F800001, 0x7F800000, 1, -2 ** 31])
+def test_adapter_scales_of_any_bits(word):
+    """Scales that are NaN with every payload, infinite, subnormal, a negative zero."""
+    layer = Layer(3, 512, 256, 128, 8, 2, adapters=(2, 16, "both"))
+    layer.up["scale"] = torch.tensor([word, word], dtype=torch.int32).view(torch.float32)
+    layer.upload()
+    assert torch.equal(layer.up["scale"].view(torch.int32), torch.tensor([word, word], dtype=torch.int32))
+    same_as_forward(layer)
+
+
 def test_subnormal_and_extreme_scales():
     layer = Layer(4, 256, 128, 256, 8, 2)
     n = 128 * 256 // 2 + 128 * 256 // 32
