@@ -324,6 +324,26 @@ def layer_decode_workspace_size(cfg: MoEConfig, k: int, down: Optional[LoraArg] 
     return int(n.value)
 
 
+def _decode_shapes(cfg: MoEConfig, k: int, x, router_w, latent_down, latent_up, blob, bias, out, routing):
+    """The tensors of a layer_decode call hold what the kernels read and write."""
+    T, d, L, E = cfg.num_tokens, cfg.d_model, cfg.d_latent, cfg.num_experts
+    for name, t, shape in (("x", x, (T, d)), ("router_w", router_w, (E, d)), ("latent_down", latent_down, (L, d)),
+                           ("latent_up", latent_up, (d, L)), ("out", out, (T, d))):
+        if t is not None and (tuple(t.shape) != shape or t.element_size() != 2):
+            raise ValueError(f"{name} must be a bf16 tensor of shape {shape}")
+    each = packed_expert_bytes if cfg.expert_layout == LAYOUT_PACKED else expert_bytes
+    if blob.numel() * blob.element_size() < E * each(L, cfg.d_ffn):
+        raise ValueError(f"expert_blob is smaller than {E} experts")
+    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) not in ((E,), (T, E))):
+        raise ValueError(f"bias must be an fp32 tensor of shape {(E,)} or {(T, E)}")
+    for name, n, dtype in (("topk_idx", T * k, torch.int32), ("topk_w", T * k, torch.float32),
+                           ("logits", T * E, torch.float32), ("expert_counts", E, torch.int32),
+                           ("expert_offsets", E + 1, torch.int32), ("perm", T * k, torch.int32)):
+        t = (routing or {}).get(name)
+        if t is not None and (t.dtype != dtype or t.numel() < n):
+            raise ValueError(f"routing[{name!r}] must hold {n} {dtype} values")
+
+
 def layer_decode(x, router_w, latent_down, latent_up, expert_blob, k: int, *, d_ffn: int,
                  bias: Optional[torch.Tensor] = None, renormalize: bool = True, act: int = ACT_SILU,
                  out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
@@ -331,12 +351,15 @@ def layer_decode(x, router_w, latent_down, latent_up, expert_blob, k: int, *, d_
                  act_format: int = ACT_FMT_BF16, lora_down: Optional[Lora] = None,
                  lora_up: Optional[Lora] = None) -> torch.Tensor:
     """layer_forward for a decode step of at most DECODE_MAX_TOKENS tokens and DECODE_MAX_ROWS
-    routed rows (moe_layer_decode): the same result, bit for bit, in two launches."""
+    routed rows (moe_layer_decode): the same result, bit for bit, in two launches.  Faster than
+    layer_forward with checkpoint records from two tokens on, with many rows on few experts, and
+    where the host cannot keep five launches ahead of the GPU; not for packed experts otherwise."""
     T, d = x.shape
     L = latent_down.shape[0]
     cfg = make_config(T, d, L, d_ffn, router_w.shape[0], act=act, renormalize=renormalize, bias=bias, packed=packed,
                       act_format=act_format)
-    _same_device(x, router_w, latent_down, latent_up, expert_blob, out, workspace)
+    _decode_shapes(cfg, k, x, router_w, latent_down, latent_up, expert_blob, bias, out, routing)
+    _same_device(x, router_w, latent_down, latent_up, expert_blob, bias, out, workspace, *(routing or {}).values())
     down = None if lora_down is None else _lora(lora_down, T, d, L, x.device)
     up = None if lora_up is None else _lora(lora_up, T, L, d, x.device)
     if out is None:
@@ -347,7 +370,7 @@ def layer_decode(x, router_w, latent_down, latent_up, expert_blob, k: int, *, d_
     ref = lambda a: None if a is None else ctypes.byref(a)
     _check(lib().moe_layer_decode(_p(x), _p(router_w), _p(latent_down), _p(latent_up), _p(expert_blob), k,
                                   ctypes.byref(cfg), _p(bias), ref(down), ref(up), _p(out), ref(r), _p(workspace),
-                                  workspace.numel(), _stream(stream)), "moe_layer_decode")
+                                  workspace.numel() * workspace.element_size(), _stream(stream)), "moe_layer_decode")
     return out
 
 

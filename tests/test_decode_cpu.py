@@ -4,6 +4,7 @@ import ctypes
 import os
 
 import pytest
+import torch
 
 import mxfp4_expert_gemm_amd as moe
 from test_lora_cpu import FAKE, GB, arg
@@ -68,3 +69,22 @@ def test_refusals():
     assert call(c, up=arg(a=None)) == -1
     assert call(c, down=arg(adapter=FAKE + 2)) == -1
     assert call(c, routing=moe.RoutingOut(saliency=FAKE + 7 * GB)) == -2
+
+
+def test_binding_refuses_wrong_shapes():
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    c = moe.make_config(4, 256, 128, 128, 8)
+    good = dict(x=bf(4, 256), router_w=bf(8, 256), latent_down=bf(128, 256), latent_up=bf(256, 128),
+                blob=torch.zeros(8 * moe.expert_bytes(128, 128), dtype=torch.uint8), bias=None, out=None, routing=None)
+    chk = lambda **kw: moe._decode_shapes(c, 2, **{**good, **kw})
+    chk()
+    chk(bias=torch.zeros(8), out=bf(4, 256), routing=dict(topk_idx=i32(4, 2), perm=i32(8), logits=None))
+    chk(bias=torch.zeros(4, 8))
+    for bad in (dict(x=bf(4, 256).float()), dict(router_w=bf(8, 128)), dict(latent_down=bf(256, 128)),
+                dict(latent_up=bf(128, 256)), dict(blob=good["blob"][:-1]), dict(bias=torch.zeros(7)),
+                dict(bias=torch.zeros(8).double()), dict(out=bf(3, 256)), dict(out=bf(4, 256).float()),
+                dict(routing=dict(topk_idx=i32(7))), dict(routing=dict(topk_idx=i32(8).long())),
+                dict(routing=dict(expert_offsets=i32(8))), dict(routing=dict(topk_w=i32(8)))):
+        with pytest.raises(ValueError):
+            chk(**bad)
