@@ -37,10 +37,10 @@
 // median and 53 at the latest, its down at 63 and 69, z is there at 71, and the up rows, which
 // are on chip by then, take 3.  The first 10 us and the last 5 stream little, the blocks' spread
 // at the two hand-overs costs as much again: that is what bounds it.  Against the five launches
-// of moe_layer_forward, in graphs on one card, here / there in us:
+// of moe_layer_forward, in graphs of 50 steps on experts of their own, here / there in us:
 //   tokens                    1           2           3           4
-//   packed experts         90.3 / 80.8  150 / 141   208 / 196   256 / 233
-//   checkpoint records      120 / 117   197 / 208   278 / 299   335 / 368
+//   packed experts         90.3 / 83.9  152 / 144   213 / 204   258 / 240
+//   checkpoint records      123 / 119   203 / 212   281 / 304   350 / 375
 // and eight MXFP8 tokens of a middle layer (2048, 1024, 512, 8 of 64, packed) 53.6 / 57.5, one
 // token of it 31.2 / 23.8, four of a tiny layer over records 27.4 / 27.3, one over packed experts
 // 22.9 / 21.1.  So it is for records, for many rows of few experts, and where five launches
@@ -1084,6 +1084,9 @@ hipError_t launch_decode(const DecodeArgs& args, bool packed, hipStream_t st) {
   a.stage_offset = hq + rows <= DEC_LDS ? (int32_t)hq : 0;
   size_t used = a.stage_offset + rows;
   if (used < hq) used = hq;
+  const size_t zu = (size_t)T * ((size_t)L * 2 + (a.lora.B ? (size_t)a.lora.R * 4 : 0));  // z and u come over both
+  if (used < zu) used = zu;
+  used = align_up(used, 16);
   if (used > DEC_LDS) return hipErrorInvalidValue;
   a.slab_offset = (int32_t)used;
   const int64_t slab = (int64_t)((DEC_LDS - used) / ((size_t)L * 2));

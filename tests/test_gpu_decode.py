@@ -144,6 +144,15 @@ def test_ties_and_pruned_experts(T):
     same_as_forward(layer)
 
 
+@pytest.mark.parametrize("T,d,L,F,E,k", [(8, 256, 128, 128, 8, 2), (7, 640, 128, 128, 4, 1), (8, 224, 7168, 7168, 2, 1)])
+def test_adapters_of_more_ranks_than_the_layer_is_wide(T, d, L, F, E, k):
+    """u of 128 ranks takes more room than the rows it follows in the LDS."""
+    layer = Layer(T, d, L, F, E, k, adapters=(5, 128, "up"))
+    layer.rank = torch.full((5,), 128, dtype=torch.int32)
+    layer.upload()
+    same_as_forward(layer)
+
+
 @pytest.mark.parametrize("word", [-1, 0x7FFFFFFF, 0x7F800001, 0x7F800000, 1, -2 ** 31])
 def test_adapter_scales_of_any_bits(word):
     """Scales that are NaN with every payload, infinite, subnormal, a negative zero."""
