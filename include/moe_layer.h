@@ -437,9 +437,9 @@ moe_status moe_layer_forward_lora(const void* x, const void* router_w, const voi
  * MOE_DECODE_MAX_ROWS, in two launches (three with lora_down) instead of five or more.  The
  * result, routing outputs included, is that of moe_layer_forward / moe_layer_forward_lora bit
  * for bit.  It is the faster of the two with checkpoint records from two tokens on (7168-wide
- * tokens, 16 of 896 experts: 197 against 208 us, four tokens 335 against 368), with many rows on
+ * tokens, 16 of 896 experts: 203 against 212 us, four tokens 350 against 375), with many rows on
  * few experts, and where the host cannot keep five launches ahead of the GPU; with packed
- * experts the launches of moe_layer_forward take less otherwise (one token 81 against 90 us).
+ * experts the launches of moe_layer_forward take less otherwise (one token 84 against 90 us).
  *  - lora_down, lora_up: nullable adapters on the latent projections.
  *  - Larger batches, cfg->num_shared > 0 and routing->saliency return MOE_ERR_UNSUPPORTED.
  *  - Workspace: moe_layer_decode_workspace_size bytes, 16-byte aligned, needing no clearing;
