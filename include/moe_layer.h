@@ -443,7 +443,8 @@ moe_status moe_layer_forward_lora(const void* x, const void* router_w, const voi
  *  - lora_down, lora_up: nullable adapters on the latent projections.
  *  - Larger batches, cfg->num_shared > 0 and routing->saliency return MOE_ERR_UNSUPPORTED.
  *  - Workspace: moe_layer_decode_workspace_size bytes, 16-byte aligned, needing no clearing;
- *    calls that may overlap in time need workspaces of their own.
+ *    calls that may overlap in time need workspaces of their own (else a call may take some
+ *    seconds and give NaN or wrong values).
  *  - The second launch's blocks hand work over within the launch; a block waits only for
  *    blocks that already run, so it shares the GPU with any other work. */
 #define MOE_DECODE_MAX_TOKENS 8

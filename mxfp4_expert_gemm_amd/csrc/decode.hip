@@ -104,14 +104,27 @@ __device__ __forceinline__ bool missing16(unsigned long long v) {  // a 16-bit l
   const unsigned long long t = ~v;
   return ((t - 0x0001000100010001ull) & ~t & 0x8000800080008000ull) != 0ull;
 }
-__device__ __forceinline__ unsigned long long await16(const uint16_t* p) {
+// A wait ends after so many polls (a few seconds) too, and with it every later one of the
+// block: only a call that shares its workspace with one that overlaps it can wait for what
+// never comes, and it then ends, with NaN outputs, instead of holding the GPU.
+constexpr int DEC_POLLS = 1 << 22;
+template <class F>
+__device__ __forceinline__ bool wait_for(int* late, F&& there) {
+  for (int n = 0; !there(); ++n) {
+    if (n == DEC_POLLS) __hip_atomic_store(late, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    if (__hip_atomic_load(late, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP)) return false;
+    __builtin_amdgcn_s_sleep(2);
+  }
+  return true;
+}
+__device__ __forceinline__ unsigned long long await16(int* late, const uint16_t* p) {  // NaN where it is late
   unsigned long long v;
-  while (missing16(v = get(reinterpret_cast<const unsigned long long*>(p)))) __builtin_amdgcn_s_sleep(2);
+  wait_for(late, [&] { return !missing16(v = get(reinterpret_cast<const unsigned long long*>(p))); });
   return v;
 }
-__device__ __forceinline__ uint32_t await32(const uint32_t* p) {
+__device__ __forceinline__ uint32_t await32(int* late, const uint32_t* p) {
   uint32_t v;
-  while ((v = get(p)) == 0xFFFFFFFFu) __builtin_amdgcn_s_sleep(2);
+  wait_for(late, [&] { return (v = get(p)) != 0xFFFFFFFFu; });
   return v;
 }
 
@@ -319,6 +332,7 @@ struct DecodeLds {
   int gn[DECODE_MAX_ROWS];
   uint8_t gslot[DECODE_MAX_ROWS][DECODE_MAX_TOKENS];
   int ng;
+  int late;  // a wait was given up
   // the block's gate / up chunk: (sequence << 16 | chunk) << 32 | items taken of it
   unsigned long long chunk;
   int tile_of[DEC_TILES], tile_n[DEC_TILES];  // the pair a tile is for, items of it there
@@ -625,7 +639,10 @@ __global__ void __launch_bounds__(DEC_THREADS) decode_kernel(DecodeArgs p) {
   ra.idx = S.sel;
   ra.w = S.w;
   if (blockIdx.x != 0) ra.logits_out = nullptr;
-  if (tid == 0) S.redo = 0u;  // read behind barriers
+  if (tid == 0) {  // read behind barriers
+    S.redo = 0u;
+    S.late = 0;
+  }
   for (int i = tid; i < DEC_ZEROS / 4; i += DEC_THREADS) reinterpret_cast<uint32_t*>(S.zeros)[i] = 0u;
   auto ahead = [&]() {
     const int bytes = (slab1 - up0) * L * 2;
@@ -820,7 +837,7 @@ __global__ void __launch_bounds__(DEC_THREADS) decode_kernel(DecodeArgs p) {
         const bool again = ns < n;
         wn[0] = again ? make(second ? ditem : nitem, ns) : w[0];
         int32_t* ready = line(p.ctr, C_EXPERT + S.sgrp[s]);
-        while (get(ready) < nrb) __builtin_amdgcn_s_sleep(1);
+        const bool there = wait_for(&S.late, [&] { return get(ready) >= nrb; });
         // the row by 8-byte agent-scope loads, SU of a lane in flight
         constexpr int SU = 13;
         const uint8_t* src = p.aq + (int64_t)s * arow;
@@ -841,6 +858,7 @@ __global__ void __launch_bounds__(DEC_THREADS) decode_kernel(DecodeArgs p) {
         f32x4 acc[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
         dec_stream<W, 1, DEC_DN_PF>(ln, w, wn, again && fit, sb, ring, DecA(nl == 0, stage, S.zeros, F, g), F, acc);
         if (again && !fit) dec_prime(ln, wn, sb, ring, F / 128);
+        if (!there) acc[0][0] = __builtin_nanf("");
         if (g == 0) {
           if (nsc == 1) S.ys[seq & 1][s][nl] = acc[0][0];
           else put(p.y + (int64_t)s * L + 16 * rg + nl, acc[0][0]);
@@ -928,7 +946,7 @@ __global__ void __launch_bounds__(DEC_THREADS) decode_kernel(DecodeArgs p) {
       }
   }
   for (int i = 4 * tid; i < T * L; i += 4 * DEC_THREADS)
-    *reinterpret_cast<unsigned long long*>(zs + i) = await16(p.z + i);
+    *reinterpret_cast<unsigned long long*>(zs + i) = await16(&S.late, p.z + i);
   lds_barrier();
   if (lora) {
     while (ui >= 0) {
@@ -957,7 +975,7 @@ __global__ void __launch_bounds__(DEC_THREADS) decode_kernel(DecodeArgs p) {
       if (lane == 0) put(p.u + ui, v != v ? 0x7FC00000u : __float_as_uint(v));
       load_a();
     }
-    for (int i = tid; i < T * R; i += DEC_THREADS) ul[i] = __uint_as_float(await32(p.u + i));
+    for (int i = tid; i < T * R; i += DEC_THREADS) ul[i] = __uint_as_float(await32(&S.late, p.u + i));
     lds_barrier();
   }
   // NR rows, DEC_WAVES apart, for every token, TP at a time: weights(r, q) is chunk q of the r-th
