@@ -233,6 +233,16 @@ moe_status run_router_and_down(const moe_config& c, const void* x, const void* r
 }
 
 // ---- adapters: their checks, and the first product into the workspace
+// moe_linear_lora takes the matrix cores below 32 tokens too, where the GEMV, which reads the
+// weights once for four tokens, would read 32 MB of them more than once over; 4 to 5 us is
+// what the matrix-core tiles cost beyond one reading.  Whole calls with adapters of rank 16, GEMV
+// and matrix cores: 7168 -> 3584 4 tokens 22.7 and 24.7 us, 5 tokens 36.8 and 25.5, 31 tokens 120
+// and 26.8; 3584 -> 7168 5 tokens 34.3 and 20.3; 2048 -> 1024 5 tokens 8.2 and 11.9, 31 tokens
+// 13.4 and 12.6; 512 -> 512 31 tokens 8.2 and 9.2.  (Entry points without adapters, and the layer,
+// keep the GEMV below 32: their results are older.)
+bool lora_takes_mfma(int64_t T, int32_t n_in, int32_t n_out) {
+  return T < 32 && n_in % 64 == 0 && (ceil_div(T, 4) - 1) * n_in * n_out >= (int64_t)1 << 24;
+}
 moe_status check_lora(const moe_lora* a) {
   if (a->num_adapters < 1 || a->max_rank < 8 || a->max_rank % 8) return MOE_ERR_INVALID_ARG;
   if (a->num_adapters > LORA_MAX_ADAPTERS || a->max_rank > LORA_MAX_RANK) return MOE_ERR_UNSUPPORTED;
@@ -1087,6 +1097,8 @@ moe_status moe_linear_lora(const void* in, const void* W, const moe_lora* lora, 
   s.out = out;
   s.wnorm = nullptr;
   s.xnorm = nullptr;
+  if (lora_takes_mfma(num_tokens, n_in, n_out))
+    return dev(launch_dense_mfma(static_cast<const uint16_t*>(in), num_tokens, n_in, s, st, &seg));
   return dev(launch_dense(static_cast<const uint16_t*>(in), num_tokens, n_in, &s, 1, st, &seg));
 }
 

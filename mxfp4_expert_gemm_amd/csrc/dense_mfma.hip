@@ -557,7 +557,7 @@ static hipError_t launch_projection(const DenseMfmaArgs& a, hipStream_t st) {
 hipError_t launch_dense_mfma(const uint16_t* x, int64_t T, int32_t K, const DenseSeg& s, hipStream_t st,
                              const LoraSeg* lora) {
   if (T == 0) return hipSuccess;
-  if (!dense_uses_mfma(T, K) || s.rows <= 0) return hipErrorInvalidValue;
+  if (K % DM_BK || s.rows <= 0) return hipErrorInvalidValue;
   DenseMfmaArgs a;
   a.x = x;
   a.W = s.W;

@@ -29,8 +29,8 @@ def check(got, x, W, lo, ids, rank, what):
     assert off.max() <= 0, (what, off.max().item())
 
 
-# T, n_in, n_out, adapters, max rank, order, ragged ranks.  Below 32 tokens (or n_in no
-# multiple of 64) the GEMV with 4, 2 or 1 tokens a block; from 32 the small matrix-core tiles,
+# T, n_in, n_out, adapters, max rank, order, ragged ranks.  Below 32 tokens (for large matrices
+# below 5; or n_in no multiple of 64) the GEMV with 4, 2 or 1 tokens a block; then the small tiles,
 # the 128 x 128 ones from 384 of them on, and the LDS-direct ones from 768; the first product
 # by rows up to 512 tokens and 16384 (token, rank) pairs, grouped above.
 CASES = [
@@ -39,6 +39,12 @@ CASES = [
     (2, 3584, 7168, 5, 128, "mixed", True),
     (3, 8192, 65, 2, 24, "mixed", False),
     (5, 512, 130, 7, 40, "mixed", True),
+    (4, 7168, 3584, 3, 16, "mixed", False),
+    (5, 7168, 3584, 3, 40, "mixed", True),
+    (9, 8192, 1025, 9, 8, "mixed", False),
+    (17, 3584, 7168, 17, 128, "mixed", True),
+    (31, 7168, 3584, 4, 16, "segments", True),
+    (31, 8160, 700, 4, 16, "mixed", True),
     (16, 256, 128, 4, 8, "mixed", True),
     (31, 4096, 64, 1024, 16, "mixed", False),
     (32, 64, 33, 3, 8, "segments", True),
