@@ -52,6 +52,7 @@
 // The arithmetic of every value is that of the kernels moe_layer_forward runs on a batch of
 // this size (dense_gemv_kernel, the routing, stream_group, the fp64 combine), in the same
 // order: the outputs are bit-identical.
+#include "decode_chunks.h"
 #include "mfma_stream.h"
 #include "route_token.h"
 
@@ -62,8 +63,9 @@ constexpr int DEC_WAVES = DEC_THREADS / WAVE;
 constexpr int DEC_GU_PF = 4;   // K steps in flight, of a gate and an up stream
 constexpr int DEC_DN_PF = 8;   // of a down stream
 constexpr int DEC_SLOTS = 2 * DEC_WAVES;  // routed rows of a down item: two a wave
-constexpr int DEC_TILES = 16;  // pairs of gate / up items a block may have open
 constexpr int DEC_SHARDS = 32;
+constexpr int DEC_MAX_DIM = 7168;  // of latent and FFN
+static_assert(DECODE_MAX_ROWS * (DEC_MAX_DIM / 32) < 0xFFFF, "pairs and chunks fit the halves of a GateUpPlan head");
 static_assert(DECODE_MAX_TOKENS <= DEC_WAVES && DECODE_MAX_ROWS <= WAVE, "a wave per token, a lane per routed row");
 
 // a staged activation row: hi codes, lo codes, hi scales, lo scales
@@ -104,9 +106,12 @@ __device__ __forceinline__ bool missing16(unsigned long long v) {  // a 16-bit l
   const unsigned long long t = ~v;
   return ((t - 0x0001000100010001ull) & ~t & 0x8000800080008000ull) != 0ull;
 }
-// A wait ends after so many polls (a few seconds) too, and with it every later one of the
-// block: only a call that shares its workspace with one that overlaps it can wait for what
-// never comes, and it then ends, with NaN outputs, instead of holding the GPU.
+// A wait for another block, or for a tile, ends after so many polls (a few seconds) too, and with
+// it every later one of the block: only a call that shares its workspace with one that overlaps
+// it can wait for what never comes, and it then ends, with NaN outputs, instead of holding
+// the GPU.  (The other waits in a block are for a wave that is claiming, which waits for
+// nothing itself, and for wave 0's next down item, which it claims behind waits of this kind at
+// most.)
 constexpr int DEC_POLLS = 1 << 22;
 template <class F>
 __device__ __forceinline__ bool wait_for(int* late, F&& there) {
@@ -333,12 +338,10 @@ struct DecodeLds {
   uint8_t gslot[DECODE_MAX_ROWS][DECODE_MAX_TOKENS];
   int ng;
   int late;  // a wait was given up
-  // the block's gate / up chunk: (sequence << 16 | chunk) << 32 | items taken of it
-  unsigned long long chunk;
+  unsigned long long chunk;  // the block's gate / up chunk, a word of GateUpPlan
   int tile_of[DEC_TILES], tile_n[DEC_TILES];  // the pair a tile is for, items of it there
   unsigned long long ditem[2];  // (sequence + 1) << 32 | down item, as wave 0 learns of it
 };
-constexpr uint32_t DEC_NO_CHUNK = 0xFFFFFFFFu;
 constexpr size_t DEC_LDS = (160 * 1024 - sizeof(DecodeLds)) / 1024 * 1024;  // what is left for the launch to size
 
 // route_token as a call: its registers are not reserved in the kernel, where it runs only
@@ -657,20 +660,17 @@ __global__ void __launch_bounds__(DEC_THREADS) decode_kernel(DecodeArgs p) {
   else if (T <= 4) dec_route<8>(p, ra, S, smem, before, ahead);
   else dec_route<16>(p, ra, S, smem, before, ahead);
   dec_group(p, ra, S);
-  // chunks of consecutive pairs, about half as many items as waves or as many: a CU's waves
-  // then read one stretch of memory
   if (wave == 0) wave_sync();
   lds_barrier();
-  const int ng = S.ng, nrb = F / 32, pairs = ng * nrb;
-  const int rounds = max(1, (int)ceil_div(pairs, (int64_t)gridDim.x * (DEC_WAVES / 2)));
-  const int cp = (int)ceil_div(pairs, (int64_t)gridDim.x * rounds);
-  chunks.n = (pairs + cp - 1) / cp;
+  const int nrb = F / 32;
+  const GateUpPlan plan(S.ng * nrb, (int)gridDim.x, DEC_WAVES);
+  chunks.n = plan.n;
   const int nrg = L / 16, nsc = (T * k + DEC_SLOTS - 1) / DEC_SLOTS;
   downs.n = nrg * nsc;
   if (wave == 0) {
     const int c = chunks.item(), dn = downs.item();
     if (lane == 0) {
-      S.chunk = (unsigned long long)(c < 0 ? DEC_NO_CHUNK : (uint32_t)c) << 32;
+      S.chunk = (unsigned long long)GateUpPlan::first(c) << 32;
       S.ditem[0] = 1ull << 32 | (uint32_t)dn;
       S.ditem[1] = 0ull;
     }
@@ -685,20 +685,20 @@ __global__ void __launch_bounds__(DEC_THREADS) decode_kernel(DecodeArgs p) {
     for (;;) {
       unsigned long long v = 0;
       if (lane == 0) v = atomicAdd(&S.chunk, 1ull);
-      const uint32_t id = (uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32));
-      const int at = __builtin_amdgcn_readfirstlane((int)(uint32_t)v);
-      if (id == DEC_NO_CHUNK) return false;
-      if (at < 2 * cp) {
-        x.pair = (int)(id & 0xFFFFu) * cp + at / 2;
-        x.seq = (int)(id >> 16) * cp + at / 2;
-        x.h = at & 1;
-        if (x.pair < pairs) return true;
-      } else if (at == 2 * cp) {  // the wave that finds it spent brings the next
+      const uint32_t head = (uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32));
+      const ChunkPlace at = plan.place(head, (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v));
+      if (at.what == ChunkPlace::NONE) return false;
+      if (at.what == ChunkPlace::ITEM) {
+        x.pair = at.pair;
+        x.seq = at.seq;
+        x.h = at.half;
+        return true;
+      }
+      if (at.what == ChunkPlace::NEXT) {
         chunks.take();
-        const int c = chunks.item();
-        const uint32_t nid = c < 0 ? DEC_NO_CHUNK : ((id >> 16) + 1) << 16 | (uint32_t)c;
+        const uint32_t next = plan.next(head, chunks.item());
         if (lane == 0)
-          __hip_atomic_store(&S.chunk, (unsigned long long)nid << 32, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+          __hip_atomic_store(&S.chunk, (unsigned long long)next << 32, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
       } else {
         __builtin_amdgcn_s_sleep(1);
       }
@@ -738,8 +738,12 @@ __global__ void __launch_bounds__(DEC_THREADS) decode_kernel(DecodeArgs p) {
       if (again && !fit) dec_prime(ln, wn, sb, ring, L / 128);
       // lane: row nl of the item, tokens 4 g + j of the expert
       const int ti = x.seq % DEC_TILES;
-      while (__hip_atomic_load(&S.tile_of[ti], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) != x.seq)
-        __builtin_amdgcn_s_sleep(1);  // a pair of the block's 16 before this one is still open
+      // the pair 16 before this one is complete; given up, the pair is not counted, and the rows
+      // that need it become NaN
+      const bool open = wait_for(&S.late, [&] {
+        return __hip_atomic_load(&S.tile_of[ti], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) == x.seq;
+      });
+      if (!__builtin_amdgcn_readfirstlane(open)) break;
       uint16_t(*at)[34] = S.tile[ti];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -1087,7 +1091,7 @@ static hipError_t launch_decode_for(const DecodeArgs& a, unsigned grid, size_t l
 hipError_t launch_decode(const DecodeArgs& args, bool packed, hipStream_t st) {
   DecodeArgs a = args;
   const int T = (int)a.r.T, n = T * a.r.k, L = a.r.L, F = a.F;
-  if (T < 1 || T > DECODE_MAX_TOKENS || n > DECODE_MAX_ROWS || L % 128 || F % 128 || L > 7168 || F > 7168 ||
+  if (T < 1 || T > DECODE_MAX_TOKENS || n > DECODE_MAX_ROWS || L % 128 || F % 128 || L > DEC_MAX_DIM || F > DEC_MAX_DIM ||
       a.r.E > ROUTE_MAXI * WAVE || a.r.d % 8)
     return hipErrorInvalidValue;
   // one block per CU, fewer where no phase has that many items
