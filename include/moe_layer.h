@@ -410,8 +410,8 @@ moe_status moe_linear_lora_workspace_size(int64_t num_tokens, int32_t n_in, cons
 /* The projection of moe_linear_bf16 with an adapter per token:
  *   u[t][r]   = sum_i a[id_t][r][i] in[t][i]                                   (fp32)
  *   out[t][o] = bf16(sum_i in[t][i] W[o][i] + scale[id_t] sum_r b[id_t][o][r] u[t][r])
- * with one rounding, of the whole sum (on the matrix cores scale u enters the second
- * product with 16 significant bits; they take large matrices from 5 tokens, others from 32).
+ * with one rounding, of the whole sum.  The sums are fp64 ones of fp32 pieces for few tokens and
+ * fp32 ones on the matrix cores, which take large matrices from 5 tokens, others from 32.
  * n_in a multiple of 32, at most 8192; any n_out;
  * num_tokens up to 2^24.  in, out and workspace must not overlap; workspace 16-byte
  * aligned, of at least moe_linear_lora_workspace_size bytes, needing no clearing. */

@@ -69,19 +69,22 @@ __device__ __forceinline__ u32x4_t keep_ranks(u32x4_t v, int valid) {
 
 // The adapters' term of a wave's tile (16 WM tokens from tb, 16 WN rows from nb), added to
 // its accumulators: each adapter met among the tokens multiplies, per 16 tokens that hold one
-// of its own, all 16 rows of u by its B (hi and lo terms of u: 16 significant bits, against
-// the 8 of the output), and the rows that name it take the product.  Taken by a select, not by
-// zeroed operands: an infinity in one request's adapter must not reach another request's row.
+// of its own, all 16 rows of u by its B (u in U_TERMS terms, all 24 bits of its fp32 sums: the
+// adapter's term may cancel against itself or the projection), and the rows that name it take
+// the product.  Taken by a select, not by zeroed operands: an infinity in one request's adapter
+// must not reach another request's row.
 // What it costs is the wait for B, 16 bytes a lane from the L2 or further: the pieces of U
-// adapters are loaded together, four but for 64 rows a wave, where two spill 26 registers
+// adapters are loaded together, four but for 64 rows a wave, where two spill 34 registers
 // (4096 tokens, 32 adapters of rank 32, 3584 -> 7168: 503 us, one 444; one adapter on each run
 // of tokens: 279 and 251).  Tokens of one request usually stand together, so most tiles meet
 // one adapter or two; a batch of single tokens can bring a new one with each (512 -> 256, 256
 // tokens with 64 adapters: 81.6 us when every 16 tokens fetched their adapters one by one in
-// tiles of 128 x 128, 14.7 now).
+// tiles of 128 x 128, 14.7 now).  The third term of u costs 2% of a call where the ranks are
+// most (1021 tokens, 5 adapters to rank 128: 109 against 107 us), nothing measurable elsewhere.
 template <int WM, int WN>
 __device__ __forceinline__ void lora_expand(const DenseMfmaArgs& p, int64_t tb, int nb, f32x4_t (&acc)[WM][WN]) {
   constexpr int U = WN == 4 ? 1 : 4;
+  constexpr int IG = WM < 2 ? WM : 2;  // 16-token groups whose u is held at once: four spill 25 registers
   const LoraSeg& l = p.lora;
   const int lane = lane_id(), nl = lane & 15, g = lane >> 4;
   const int RP = rank_pad(l.R);
@@ -120,29 +123,34 @@ __device__ __forceinline__ void lora_expand(const DenseMfmaArgs& p, int64_t tb, 
           b[u][jn] = u32x4_t{0u, 0u, 0u, 0u};
           if (r < rk[u]) b[u][jn] = *reinterpret_cast<const u32x4_t*>(B[u] + (int64_t)n * l.R + r);
         }
-      bf16x8_t hi[WM], lo[WM];
 #pragma unroll
-      for (int i = 0; i < WM; ++i) {
-        hi[i] = *reinterpret_cast<const bf16x8_t*>(l.uhi + tc[i] * RP + r);
-        lo[i] = *reinterpret_cast<const bf16x8_t*>(l.ulo + tc[i] * RP + r);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (r0 >= rk[u]) continue;
+      for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int jn = 0; jn < WN; ++jn) b[u][jn] = keep_ranks(b[u][jn], rk[u] - r);
 #pragma unroll
-        for (int i = 0; i < WM; ++i) {
-          const uint32_t rows = (uint32_t)(same[u] >> (16 * i)) & 0xFFFFu;
-          if (!rows) continue;
+      for (int i0 = 0; i0 < WM; i0 += IG) {
+        bf16x8_t ut[IG][U_TERMS];
 #pragma unroll
-          for (int jn = 0; jn < WN; ++jn) {
-            const bf16x8_t v = __builtin_bit_cast(bf16x8_t, b[u][jn]);
-            f32x4_t d = {0.f, 0.f, 0.f, 0.f};
-            d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi[i], v, d, 0, 0, 0);
-            d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo[i], v, d, 0, 0, 0);
+        for (int i = 0; i < IG; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][jn][j] += (rows >> (4 * g + j)) & 1u ? d[j] : 0.f;
+          for (int m = 0; m < U_TERMS; ++m)
+            ut[i][m] = *reinterpret_cast<const bf16x8_t*>(l.ut + (m * p.T + tc[i0 + i]) * RP + r);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (r0 >= rk[u]) continue;
+#pragma unroll
+          for (int i = 0; i < IG; ++i) {
+            const uint32_t rows = (uint32_t)(same[u] >> (16 * (i0 + i))) & 0xFFFFu;
+            if (!rows) continue;
+#pragma unroll
+            for (int jn = 0; jn < WN; ++jn) {
+              const bf16x8_t v = __builtin_bit_cast(bf16x8_t, b[u][jn]);
+              f32x4_t d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int m = 0; m < U_TERMS; ++m) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ut[i][m], v, d, 0, 0, 0);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) acc[i0 + i][jn][j] += (rows >> (4 * g + j)) & 1u ? d[j] : 0.f;
+            }
           }
         }
       }

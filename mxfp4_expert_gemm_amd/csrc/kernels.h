@@ -20,10 +20,10 @@ struct LoraSeg {
   const int32_t* adapter = nullptr;    // [T]; ids outside [0, N) have no term
   const int32_t* rank = nullptr;       // nullable [N]
   const float* u = nullptr;            // [T][R], the GEMV's operand
-  const uint16_t* uhi = nullptr;       // [T][rank_pad(R)] bf16, the matrix cores' operand: u = uhi + ulo
-  const uint16_t* ulo = nullptr;
+  const uint16_t* ut = nullptr;        // [U_TERMS][T][rank_pad(R)] bf16, the matrix cores' operand: u is their sum
   int32_t N = 0, R = 0;
 };
+constexpr int U_TERMS = 3;  // of eight bits each: all 24 of an fp32 value
 constexpr int LORA_MAX_RANK = 128;
 constexpr int LORA_MAX_ADAPTERS = 1024;
 // ranks on the matrix cores come in K steps of 32

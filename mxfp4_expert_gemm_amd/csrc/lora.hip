@@ -10,7 +10,7 @@
 // Many: the tokens are grouped by adapter and a tile of up to 64 of them runs on the matrix
 // cores (v_mfma_f32_16x16x32_bf16), the K range cut into slices so that the grid fills the
 // chip; the slices' fp32 partials are added in slice order by the kernel that also splits u
-// into the two bf16 terms the matrix-core projection reads.
+// into the bf16 terms the matrix-core projection reads.
 #include "common.h"
 #include "kernels.h"
 
@@ -25,8 +25,7 @@ constexpr int LT_MIN_K = 256;    // at least so much K per slice
 
 struct LoraWs {
   float* u;         // [T][R]
-  uint16_t* uhi;    // [T][rank_pad(R)]
-  uint16_t* ulo;
+  uint16_t* ut;     // [U_TERMS][T][rank_pad(R)]
   int32_t* perm;    // [T] tokens grouped by adapter
   int4* tiles;      // {adapter, first place in perm, tokens, 0}
   int32_t* ntiles;
@@ -60,8 +59,7 @@ static LoraWs lora_ws(void* ws, int64_t T, int32_t K, int32_t N, int32_t R) {
   };
   const size_t t = (size_t)T, rp = (size_t)rank_pad(R);
   l.u = reinterpret_cast<float*>(take(t * (size_t)R * 4));
-  l.uhi = reinterpret_cast<uint16_t*>(take(t * rp * 2));
-  l.ulo = reinterpret_cast<uint16_t*>(take(t * rp * 2));
+  l.ut = reinterpret_cast<uint16_t*>(take(U_TERMS * t * rp * 2));
   l.perm = nullptr;
   l.tiles = nullptr;
   l.ntiles = nullptr;
@@ -83,14 +81,22 @@ __device__ __forceinline__ int token_rank(const LoraArgs& p, int a) {
   return p.rank ? max(0, min(p.rank[a], p.R)) : p.R;
 }
 
-// u in the forms the projections read: fp32, and hi + lo bf16 terms (lo 0 where hi is not
-// finite, so that an infinity stays one)
-__device__ __forceinline__ void put_u(const LoraWs& w, int64_t t, int r, int R, float v) {
-  if (r < R) w.u[t * R + r] = v;
-  const uint16_t hi = f32_to_bf16(v);
-  const float back = bf16f(hi);
-  w.uhi[t * rank_pad(R) + r] = hi;
-  w.ulo[t * rank_pad(R) + r] = fabsf(back) <= 0x1.fffffep127f ? f32_to_bf16(v - back) : (uint16_t)0;
+// u in the forms the projections read: fp32, and three bf16 terms whose sum it is.  Each term is
+// the top half of what the earlier ones leave (exact differences), so the terms of a value have one
+// sign, and a finite value above the largest bf16 stays finite; an infinity or NaN is its first term
+// alone.
+__device__ __forceinline__ void put_u(const LoraArgs& p, const LoraWs& w, int64_t t, int r, float v) {
+  if (r < p.R) w.u[t * p.R + r] = v;
+  const int RP = rank_pad(p.R);
+  uint16_t* at = w.ut + t * RP + r;
+  const bool finite = fabsf(v) <= 0x1.fffffep127f;
+  float rest = v;
+#pragma unroll
+  for (int i = 0; i < U_TERMS; ++i) {
+    const uint16_t top = v != v && i == 0 ? (uint16_t)0x7FC0 : (uint16_t)(__float_as_uint(rest) >> 16);
+    at[(int64_t)i * p.T * RP] = top;
+    rest = finite ? rest - bf16f(top) : 0.f;
+  }
 }
 
 // A wave per (token, rank), ranks up to rank_pad(R).  Chunk partials of eight exact products
@@ -127,7 +133,7 @@ __global__ void __launch_bounds__(256) lora_shrink_rows_kernel(LoraArgs p, LoraW
     }
     v = (float)(wave_sum_dpp(acc) * (double)p.scale[a]);
   }
-  if (lane == 0) put_u(w, t, r, p.R, v);
+  if (lane == 0) put_u(p, w, t, r, v);
 }
 
 // The tokens grouped by adapter (those without one left out) and cut into tiles, by one
@@ -263,7 +269,7 @@ __global__ void __launch_bounds__(256) lora_join_kernel(LoraArgs p, LoraWs w, in
       for (int s = 0; s < slices; ++s) v += w.part[((int64_t)s * p.T + t) * p.R + r];
       v *= p.scale[a];
     }
-    put_u(w, t, r, p.R, v);
+    put_u(p, w, t, r, v);
   }
 }
 
@@ -282,8 +288,7 @@ hipError_t launch_lora_shrink(const LoraArgs& a, void* ws, LoraSeg* seg, hipStre
   seg->adapter = a.adapter;
   seg->rank = a.rank;
   seg->u = w.u;
-  seg->uhi = w.uhi;
-  seg->ulo = w.ulo;
+  seg->ut = w.ut;
   seg->N = a.N;
   seg->R = a.R;
   if (!lora_grouped(a.T, a.R)) {
