@@ -67,12 +67,17 @@ __device__ __forceinline__ u32x4_t keep_ranks(u32x4_t v, int valid) {
   return v;
 }
 
+// the top bit of each bf16 half that is an infinity or NaN, and the pair without those halves
+__device__ __forceinline__ uint32_t not_finite2(uint32_t v) { return ((v & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u; }
+__device__ __forceinline__ uint32_t finite2(uint32_t v) { return v & ~((not_finite2(v) >> 15) * 0xFFFFu); }
+
 // The adapters' term of a wave's tile (16 WM tokens from tb, 16 WN rows from nb), added to
 // its accumulators: each adapter met among the tokens multiplies, per 16 tokens that hold one
 // of its own, all 16 rows of u by its B (u in U_TERMS terms, all 24 bits of its fp32 sums: the
 // adapter's term may cancel against itself or the projection), and the rows that name it take
 // the product.  Taken by a select, not by zeroed operands: an infinity in one request's adapter
-// must not reach another request's row.
+// must not reach another request's row.  An infinity or NaN in B meets the first term of u only,
+// which is zero where u is; the later ones may be zero or not, and would make a NaN of it.
 // What it costs is the wait for B, 16 bytes a lane from the L2 or further: the pieces of U
 // adapters are loaded together, four but for 64 rows a wave, where two spill 34 registers
 // (4096 tokens, 32 adapters of rank 32, 3584 -> 7168: 503 us, one 444; one adapter on each run
@@ -80,11 +85,11 @@ __device__ __forceinline__ u32x4_t keep_ranks(u32x4_t v, int valid) {
 // one adapter or two; a batch of single tokens can bring a new one with each (512 -> 256, 256
 // tokens with 64 adapters: 81.6 us when every 16 tokens fetched their adapters one by one in
 // tiles of 128 x 128, 14.7 now).  The third term of u costs 2% of a call where the ranks are
-// most (1021 tokens, 5 adapters to rank 128: 109 against 107 us), nothing measurable elsewhere.
+// most (1021 tokens, 5 adapters to rank 128: 109 against 107 us), 1% at 4096 tokens of rank 32.
 template <int WM, int WN>
 __device__ __forceinline__ void lora_expand(const DenseMfmaArgs& p, int64_t tb, int nb, f32x4_t (&acc)[WM][WN]) {
   constexpr int U = WN == 4 ? 1 : 4;
-  constexpr int IG = WM < 2 ? WM : 2;  // 16-token groups whose u is held at once: four spill 25 registers
+  constexpr int IG = WM < 2 ? WM : 2;  // 16-token groups whose u is held at once: four spill
   const LoraSeg& l = p.lora;
   const int lane = lane_id(), nl = lane & 15, g = lane >> 4;
   const int RP = rank_pad(l.R);
@@ -127,6 +132,16 @@ __device__ __forceinline__ void lora_expand(const DenseMfmaArgs& p, int64_t tb, 
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int jn = 0; jn < WN; ++jn) b[u][jn] = keep_ranks(b[u][jn], rk[u] - r);
+      bool odd[U];  // B holds values that are not finite
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        uint32_t bits = 0;
+#pragma unroll
+        for (int jn = 0; jn < WN; ++jn)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) bits |= not_finite2(b[u][jn][i]);
+        odd[u] = __any(bits != 0u);
+      }
 #pragma unroll
       for (int i0 = 0; i0 < WM; i0 += IG) {
         bf16x8_t ut[IG][U_TERMS];
@@ -144,10 +159,17 @@ __device__ __forceinline__ void lora_expand(const DenseMfmaArgs& p, int64_t tb, 
             if (!rows) continue;
 #pragma unroll
             for (int jn = 0; jn < WN; ++jn) {
-              const bf16x8_t v = __builtin_bit_cast(bf16x8_t, b[u][jn]);
+              u32x4_t v = b[u][jn];
               f32x4_t d = {0.f, 0.f, 0.f, 0.f};
+              d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ut[i][0], __builtin_bit_cast(bf16x8_t, v), d, 0, 0, 0);
+              if (odd[u]) {
+                asm volatile("" : "+v"(v));  // here, not ahead for all of them: that spills
 #pragma unroll
-              for (int m = 0; m < U_TERMS; ++m) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ut[i][m], v, d, 0, 0, 0);
+                for (int j = 0; j < 4; ++j) v[j] = finite2(v[j]);
+              }
+#pragma unroll
+              for (int m = 1; m < U_TERMS; ++m)
+                d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ut[i][m], __builtin_bit_cast(bf16x8_t, v), d, 0, 0, 0);
 #pragma unroll
               for (int j = 0; j < 4; ++j) acc[i0 + i][jn][j] += (rows >> (4 * g + j)) & 1u ? d[j] : 0.f;
             }

@@ -49,3 +49,28 @@ def test_u_between_the_largest_bf16_and_fp32(T, n_in, n_out, sign):
     want = torch.tensor(u * 2.0 ** -120).bfloat16().float()  # 2^8 (1 - 2^-11), rounded to 2^8
     out = run(x, W, a, b, ids)
     assert (out[ids == 1] == want).all() and (out[ids == 0] == 0.0).all()
+
+
+@pytest.mark.parametrize("T,n_in,n_out", SHAPES)
+def test_infinities_in_the_second_matrix(T, n_in, n_out):
+    """Infinite entries of b times a u that bf16 holds exactly, that needs more bits of either sign,
+    and that is zero; both infinities in one sum; a NaN.  Value, sign and class as the formula's."""
+    inf, nan = float("inf"), float("nan")
+    x, W = torch.zeros((T, n_in)), torch.zeros((n_out, n_in))
+    x[:, :2] = torch.tensor([2.0 ** 10, 1.0])
+    W[:, 1] = 0.5
+    a, b, ids = small_lora(T, n_in, n_out)
+    a[1, :5, :2] = torch.tensor([[0.0, 4.0], [1.0, 3.0], [-1.0, 3.0], [1.0, -3.0], [0.0, 0.0]])  # 4, 1027, -1021, 1021, 0
+    rows = [[inf, 1, 0, 0, 0], [0, inf, 1, 0, 0], [0, 1, inf, 0, 0], [0, 0, 0, inf, 0], [1, 0, 0, 0, inf],
+            [0, -inf, 0, 0, 0], [0, inf, -inf, 0, 0], [0, inf, inf, 0, 0], [nan, 1, 0, 0, 0], [1, 1, 1, 1, 0]]
+    b[1, :, :5] = torch.tensor(rows, dtype=torch.float32)[torch.arange(n_out) % len(rows)]
+    # 4 inf; 1027 inf; -1021 inf; 1021 inf; 0 inf; -1027 inf; 1027 inf + -1021 -inf; 1027 inf - 1021 inf; NaN; the sum
+    want = torch.tensor([inf, inf, -inf, inf, nan, -inf, inf, nan, nan, 0.5 + 4 + 1027 - 1021 + 1021]).bfloat16().float()
+    want = want[torch.arange(n_out) % len(rows)]
+    out = run(x, W, a, b, ids)
+    for t in range(T):
+        if ids[t] == 1:
+            assert torch.equal(out[t].isnan(), want.isnan()), t
+            assert torch.equal(torch.nan_to_num(out[t], 7.0), torch.nan_to_num(want, 7.0)), t
+        else:
+            assert (out[t] == 0.5).all()
