@@ -7,9 +7,14 @@ may be torch.bfloat16 or int16/uint16 tensors holding bf16 bit patterns.
 The library is built in-tree by ``python -m mxfp4_expert_gemm_amd.build``; if
 it is missing, importing this package's functions raises instead of falling
 back to any other implementation.
+
+A call runs on the current stream, or on the one passed as ``stream``.  What it allocates itself
+(``out``, ``workspace``) belongs to that stream, as with torch's own operators: the caller orders
+other streams behind it, and records them on an ``out`` that they use.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import NamedTuple, Optional
@@ -162,6 +167,12 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _on(stream=None):
+    """Where a call allocates: memory of the stream that its kernels use, so that neither what
+    ran in it before nor what comes after a workspace is dropped can overlap them."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def make_config(num_tokens: int, d_model: int, d_latent: int, d_ffn: int, num_experts: int, *,
                 act: int = ACT_SILU, renormalize: bool = True, bias: Optional[torch.Tensor] = None,
                 packed: bool = False, act_format: int = ACT_FMT_BF16, num_shared: int = 0,
@@ -246,13 +257,14 @@ def linear_lora(inp: torch.Tensor, W: torch.Tensor, lora: Lora, *, out: Optional
         raise ValueError(f"inp and W must be bf16, W [n_out, {n_in}]")
     _same_device(inp, W, out, workspace)
     arg = _lora(lora, T, n_in, n_out, inp.device)
-    if out is None:
-        out = torch.empty((T, n_out), dtype=inp.dtype, device=inp.device)
-    elif tuple(out.shape) != (T, n_out) or out.element_size() != 2:
+    if out is not None and (tuple(out.shape) != (T, n_out) or out.element_size() != 2):
         raise ValueError(f"out must be a 2-byte [{T}, {n_out}] tensor")
-    if workspace is None:
-        workspace = torch.empty(linear_lora_workspace_size(T, n_in, arg.num_adapters, arg.max_rank),
-                                dtype=torch.uint8, device=inp.device)
+    with _on(stream):
+        if out is None:
+            out = torch.empty((T, n_out), dtype=inp.dtype, device=inp.device)
+        if workspace is None:
+            workspace = torch.empty(linear_lora_workspace_size(T, n_in, arg.num_adapters, arg.max_rank),
+                                    dtype=torch.uint8, device=inp.device)
     _check(lib().moe_linear_lora(_p(inp), _p(W), ctypes.byref(arg), T, n_in, n_out, _p(out), _p(workspace),
                                  workspace.numel() * workspace.element_size(), _stream(stream)), "moe_linear_lora")
     return out
@@ -282,14 +294,16 @@ def layer_forward(x, router_w, latent_down, latent_up, expert_blob, k: int, *, d
     cfg = make_config(T, d, L, d_ffn, E, act=act, renormalize=renormalize, bias=bias, packed=packed,
                       act_format=act_format, num_shared=num_shared, d_ffn_shared=d_ffn_shared)
     if out is None:
-        out = torch.empty((T, d), dtype=x.dtype, device=x.device)
+        with _on(stream):
+            out = torch.empty((T, d), dtype=x.dtype, device=x.device)
     if lora_down is not None or lora_up is not None:
         _same_device(x, out, workspace)
         down = None if lora_down is None else _lora(lora_down, T, d, L, x.device)
         up = None if lora_up is None else _lora(lora_up, T, L, d, x.device)
         if workspace is None:
-            workspace = torch.empty(max(layer_lora_workspace_size(cfg, k, down, up), 256), dtype=torch.uint8,
-                                    device=x.device)
+            with _on(stream):
+                workspace = torch.empty(max(layer_lora_workspace_size(cfg, k, down, up), 256), dtype=torch.uint8,
+                                        device=x.device)
         r = _routing(routing)
         ref = lambda a: None if a is None else ctypes.byref(a)
         _check(lib().moe_layer_forward_lora(_p(x), _p(router_w), _p(latent_down), _p(latent_up), _p(expert_blob), k,
@@ -298,7 +312,8 @@ def layer_forward(x, router_w, latent_down, latent_up, expert_blob, k: int, *, d
                                             _stream(stream)), "moe_layer_forward_lora")
         return out
     if workspace is None:
-        workspace = alloc_workspace(cfg, k, x.device)
+        with _on(stream):
+            workspace = alloc_workspace(cfg, k, x.device)
     r = _routing(routing)
     if num_shared > 0:
         _check(lib().moe_layer_forward_shared(_p(x), _p(router_w), _p(latent_down), _p(latent_up), _p(expert_blob),
@@ -362,10 +377,11 @@ def layer_decode(x, router_w, latent_down, latent_up, expert_blob, k: int, *, d_
     _same_device(x, router_w, latent_down, latent_up, expert_blob, bias, out, workspace, *(routing or {}).values())
     down = None if lora_down is None else _lora(lora_down, T, d, L, x.device)
     up = None if lora_up is None else _lora(lora_up, T, L, d, x.device)
-    if out is None:
-        out = torch.empty((T, d), dtype=x.dtype, device=x.device)
-    if workspace is None:
-        workspace = torch.empty(layer_decode_workspace_size(cfg, k, down, up), dtype=torch.uint8, device=x.device)
+    with _on(stream):
+        if out is None:
+            out = torch.empty((T, d), dtype=x.dtype, device=x.device)
+        if workspace is None:
+            workspace = torch.empty(layer_decode_workspace_size(cfg, k, down, up), dtype=torch.uint8, device=x.device)
     r = _routing(routing)
     ref = lambda a: None if a is None else ctypes.byref(a)
     _check(lib().moe_layer_decode(_p(x), _p(router_w), _p(latent_down), _p(latent_up), _p(expert_blob), k,
@@ -421,12 +437,13 @@ def layer_forward_streamed(x, router_w, latent_down, latent_up, expert_blob_host
     L = latent_down.shape[0]
     cfg = make_config(T, d, L, d_ffn, E, act=act, renormalize=renormalize, bias=bias, packed=packed,
                       act_format=act_format)
-    if out is None:
-        out = torch.empty((T, d), dtype=x.dtype, device=x.device)
-    if workspace is None:
-        workspace = alloc_workspace(cfg, k, x.device)
-    if expert_slots is None:
-        expert_slots = alloc_expert_slots(cfg, k, x.device)
+    with _on(stream):
+        if out is None:
+            out = torch.empty((T, d), dtype=x.dtype, device=x.device)
+        if workspace is None:
+            workspace = alloc_workspace(cfg, k, x.device)
+        if expert_slots is None:
+            expert_slots = alloc_expert_slots(cfg, k, x.device)
     r = _routing(routing)
     _check(lib().moe_layer_forward_streamed(_p(x), _p(router_w), _p(latent_down), _p(latent_up),
                                             expert_blob_host.data_ptr(), k, ctypes.byref(cfg), _p(bias),
@@ -445,10 +462,11 @@ def layer_forward_profiled(x, router_w, latent_down, latent_up, expert_blob, k: 
     T, d = x.shape
     cfg = make_config(T, d, latent_down.shape[0], d_ffn, router_w.shape[0], renormalize=renormalize, bias=bias,
                       packed=packed, act_format=act_format)
-    if out is None:
-        out = torch.empty((T, d), dtype=x.dtype, device=x.device)
-    if workspace is None:
-        workspace = alloc_workspace(cfg, k, x.device)
+    with _on(stream):
+        if out is None:
+            out = torch.empty((T, d), dtype=x.dtype, device=x.device)
+        if workspace is None:
+            workspace = alloc_workspace(cfg, k, x.device)
     r = _routing(routing)
     _check(lib().moe_layer_forward_profiled(_p(x), _p(router_w), _p(latent_down), _p(latent_up), _p(expert_blob), k,
                                             ctypes.byref(cfg), _p(bias), _p(out), ctypes.byref(r) if r else None,
