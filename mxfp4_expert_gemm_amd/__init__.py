@@ -216,12 +216,15 @@ def _routing(r: Optional[dict]) -> Optional[RoutingOut]:
                                               "perm", "saliency")])
 
 
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)  # bf16 values, or their bit patterns
+
+
 def _lora(lo: Lora, T: int, n_in: int, n_out: int, device) -> LoraArg:
     """The adapters as the library takes them, their shapes, types and device checked."""
-    if lo.a.dim() != 3 or lo.a.shape[2] != n_in or lo.a.element_size() != 2:
+    if lo.a.dim() != 3 or lo.a.shape[2] != n_in or lo.a.dtype not in _BF16:
         raise ValueError(f"a must be a bf16 [N, R, {n_in}] tensor")
     N, R = lo.a.shape[:2]
-    if tuple(lo.b.shape) != (N, n_out, R) or lo.b.element_size() != 2:
+    if tuple(lo.b.shape) != (N, n_out, R) or lo.b.dtype not in _BF16:
         raise ValueError(f"b must be a bf16 [{N}, {n_out}, {R}] tensor")
     for name, t, shape, dtype in (("scale", lo.scale, (N,), torch.float32), ("adapter", lo.adapter, (T,), torch.int32),
                                   ("rank", lo.rank, (N,), torch.int32)):
@@ -253,12 +256,12 @@ def linear_lora(inp: torch.Tensor, W: torch.Tensor, lora: Lora, *, out: Optional
     out[t] = bf16(W inp[t] + scale b (a inp[t])) with the adapter that lora.adapter[t] names."""
     T, n_in = inp.shape
     n_out = W.shape[0]
-    if tuple(W.shape) != (n_out, n_in) or W.element_size() != 2 or inp.element_size() != 2:
+    if tuple(W.shape) != (n_out, n_in) or W.dtype not in _BF16 or inp.dtype not in _BF16:
         raise ValueError(f"inp and W must be bf16, W [n_out, {n_in}]")
     _same_device(inp, W, out, workspace)
     arg = _lora(lora, T, n_in, n_out, inp.device)
-    if out is not None and (tuple(out.shape) != (T, n_out) or out.element_size() != 2):
-        raise ValueError(f"out must be a 2-byte [{T}, {n_out}] tensor")
+    if out is not None and (tuple(out.shape) != (T, n_out) or out.dtype not in _BF16):
+        raise ValueError(f"out must be a bf16 [{T}, {n_out}] tensor")
     with _on(stream):
         if out is None:
             out = torch.empty((T, n_out), dtype=inp.dtype, device=inp.device)
@@ -297,7 +300,9 @@ def layer_forward(x, router_w, latent_down, latent_up, expert_blob, k: int, *, d
         with _on(stream):
             out = torch.empty((T, d), dtype=x.dtype, device=x.device)
     if lora_down is not None or lora_up is not None:
-        _same_device(x, out, workspace)
+        _decode_shapes(cfg, k, x, router_w, latent_down, latent_up, expert_blob, bias, out, routing)
+        _same_device(x, router_w, latent_down, latent_up, expert_blob, bias, shared_blob, out, workspace,
+                     *(routing or {}).values())
         down = None if lora_down is None else _lora(lora_down, T, d, L, x.device)
         up = None if lora_up is None else _lora(lora_up, T, L, d, x.device)
         if workspace is None:
@@ -340,11 +345,12 @@ def layer_decode_workspace_size(cfg: MoEConfig, k: int, down: Optional[LoraArg] 
 
 
 def _decode_shapes(cfg: MoEConfig, k: int, x, router_w, latent_down, latent_up, blob, bias, out, routing):
-    """The tensors of a layer_decode call hold what the kernels read and write."""
+    """The tensors of a layer_decode call, or of a layer_forward call with adapters, hold what the
+    kernels read and write."""
     T, d, L, E = cfg.num_tokens, cfg.d_model, cfg.d_latent, cfg.num_experts
     for name, t, shape in (("x", x, (T, d)), ("router_w", router_w, (E, d)), ("latent_down", latent_down, (L, d)),
                            ("latent_up", latent_up, (d, L)), ("out", out, (T, d))):
-        if t is not None and (tuple(t.shape) != shape or t.element_size() != 2):
+        if t is not None and (tuple(t.shape) != shape or t.dtype not in _BF16):
             raise ValueError(f"{name} must be a bf16 tensor of shape {shape}")
     each = packed_expert_bytes if cfg.expert_layout == LAYOUT_PACKED else expert_bytes
     if blob.numel() * blob.element_size() < E * each(L, cfg.d_ffn):
@@ -353,7 +359,8 @@ def _decode_shapes(cfg: MoEConfig, k: int, x, router_w, latent_down, latent_up, 
         raise ValueError(f"bias must be an fp32 tensor of shape {(E,)} or {(T, E)}")
     for name, n, dtype in (("topk_idx", T * k, torch.int32), ("topk_w", T * k, torch.float32),
                            ("logits", T * E, torch.float32), ("expert_counts", E, torch.int32),
-                           ("expert_offsets", E + 1, torch.int32), ("perm", T * k, torch.int32)):
+                           ("expert_offsets", E + 1, torch.int32), ("perm", T * k, torch.int32),
+                           ("saliency", E, torch.float64)):
         t = (routing or {}).get(name)
         if t is not None and (t.dtype != dtype or t.numel() < n):
             raise ValueError(f"routing[{name!r}] must hold {n} {dtype} values")
