@@ -29,6 +29,7 @@ namespace moe {
 struct DenseParams {
   const uint16_t* x;
   int64_t T;
+  int64_t t_base;  // first token of this launch
   int32_t K;
   int32_t nseg;
   DenseSeg seg[2];
@@ -63,7 +64,7 @@ __global__ void __launch_bounds__(256) dense_gemv_kernel(DenseParams p) {
   const bool valid = !second || (p.nseg >= 2 && row < p.seg[1].rows);
   if (!valid) row = s.rows - 1;
   const int32_t K = p.K;
-  const int64_t t0 = (int64_t)blockIdx.y * G;
+  const int64_t t0 = p.t_base + (int64_t)blockIdx.y * G;
   if (blockIdx.y == 0) {
     for (int i = blockIdx.x * 256 + threadIdx.x; i < p.clear.nzero; i += gridDim.x * 256) p.clear.zero[32 * i] = 0;
     for (int i = blockIdx.x * 256 + threadIdx.x; i < p.clear.nones; i += gridDim.x * 256)
@@ -200,15 +201,22 @@ __global__ void __launch_bounds__(256) dense_gemv_kernel(DenseParams p) {
 }
 
 template <int NCH, int G>
-static hipError_t launch_nch_g(const DenseParams& p, hipStream_t st) {
+static hipError_t launch_nch_g(DenseParams p, hipStream_t st) {
   int64_t rows = p.seg[0].rows + (p.nseg > 1 ? p.seg[1].rows : 0);
-  if (ceil_div(p.T, G) > 65535 || ceil_div(rows, 4) > 0x7FFFFFFF) return hipErrorInvalidValue;
-  dim3 grid((unsigned)ceil_div(rows, 4), (unsigned)ceil_div(p.T, G));
-  if (p.lora.B)
-    hipLaunchKernelGGL((dense_gemv_kernel<NCH, G, true>), grid, dim3(256), 0, st, p);
-  else
-    hipLaunchKernelGGL((dense_gemv_kernel<NCH, G, false>), grid, dim3(256), 0, st, p);
-  return hipGetLastError();
+  if (ceil_div(rows, 4) > 0x7FFFFFFF) return hipErrorInvalidValue;
+  constexpr int64_t MAX_Y = 65535;  // the grid's second dimension; more tokens take more launches
+  const int64_t groups = ceil_div(p.T, G);
+  for (int64_t g0 = 0; g0 < groups; g0 += MAX_Y) {
+    p.t_base = g0 * G;
+    const dim3 grid((unsigned)ceil_div(rows, 4), (unsigned)(groups - g0 < MAX_Y ? groups - g0 : MAX_Y));
+    if (p.lora.B)
+      hipLaunchKernelGGL((dense_gemv_kernel<NCH, G, true>), grid, dim3(256), 0, st, p);
+    else
+      hipLaunchKernelGGL((dense_gemv_kernel<NCH, G, false>), grid, dim3(256), 0, st, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <int NCH>
