@@ -221,12 +221,16 @@ static hipError_t launch_nch_g(DenseParams p, hipStream_t st) {
 
 template <int NCH>
 static hipError_t launch_nch(const DenseParams& p, hipStream_t st) {
-  // tokens per block: a weight row is read once for G of them (results do not depend on it).
-  // Four from three tokens on, the fourth unused if need be (4480 x 7168: 4 tokens 36 us with
-  // one a block, 18.0 with four; 3 tokens 28 and 19.6; 1024 x 2048: 3 tokens 3.7 with two, 3.4
-  // with four), else two (4480 x 7168: 2 tokens 19.7 and 13.2 us).
-  if (p.T >= 3) return launch_nch_g<NCH, 4>(p, st);
-  if (p.T >= 2) return launch_nch_g<NCH, 2>(p, st);
+  // Tokens per block: a weight row is read once for G of them (results do not depend on it).  As
+  // many as leave a wave for each of the card's 1024 SIMDs, or two where a wave has four tokens:
+  // fewer waves than that take longer, each, than they save in reads.  One, two and four a block,
+  // us: 7168 wide, 3584 rows 2 tokens 15.1, 10.2, 16.4, 3 tokens 21.0, 17.2, 15.9, 8 tokens 49.6,
+  // 29.1, 24.9; 896 rows 3 tokens 6.0, 6.3, 6.8, 4 tokens 7.2, 5.8, 6.8, 8 tokens 10.8, 8.4, 8.0; 4096
+  // wide, 512 rows 4 tokens 3.4, 3.7, 5.0, 8 tokens 4.5, 4.0, 5.0, 16 tokens 6.2, 5.3, 5.5; 2048 wide, 2048
+  // rows 4 tokens 5.6, 4.5, 4.0.
+  const int64_t rows = p.seg[0].rows + (p.nseg > 1 ? p.seg[1].rows : 0);
+  if (p.T >= 3 && rows * ceil_div(p.T, 4) >= 2048) return launch_nch_g<NCH, 4>(p, st);
+  if (p.T >= 2 && rows * ceil_div(p.T, 2) >= 1024) return launch_nch_g<NCH, 2>(p, st);
   return launch_nch_g<NCH, 1>(p, st);
 }
 
