@@ -553,13 +553,22 @@ static hipError_t launch_dm_dma(const DenseMfmaArgs& a0, hipStream_t st) {
 // the second for smaller grids (prefill4k's router, 448 blocks: 0.12 against 0.14 ms).
 static bool dm_dma_pays(int64_t T, int32_t N, int BM, int BN) { return ceil_div(T, BM) * ceil_div(N, BN) >= 768; }
 
-// Blocks from which a projection takes tiles of 128 x 128, a block and a half per CU: below,
-// the smaller tiles' grid fills more of the chip than their extra reads cost (with an adapter
-// of rank 16 on each token, four in turn; 7168 -> 3584: 256 tokens, 56 blocks, 98.5 us and with
-// the smaller tiles 45.1; 512 tokens, 112 blocks, 109.6 and 70.9; 1536, 336 blocks, 153 and 157;
-// 2048, 448 blocks, 162 and 188; 3584 -> 7168: 256 tokens 59.7 and 36.7; 768, 336 blocks, 91.6
-// and 89.2; 1024, 448 blocks, 92.9 and 102.7).
-constexpr int64_t DM_BIG_BLOCKS = 384;
+// Whether a projection takes tiles of 128 x 128, or the smaller ones, whose grid fills more of the
+// chip for more reads.  Four 64 x 64 tiles replace one, and a CU runs them one after another:
+// 192 blocks leave it 3 of the small, which take less than one of the large, 256 leave it 4, 320
+// leave it 5 against two of the large, 384 leave it 6.  So large from 193 to 256 blocks, and from 321
+// on; narrow inputs, which are done before the reads tell, only from 384.  Small and large, us, with
+// an adapter of rank 16 on each token behind the semicolon: 7168 -> 1024, 192 blocks 69.2, 77.3;
+// 101, 111; 256 blocks 88.7, 79.3; 131, 119; 320 blocks 110, 121; 153, 160; 336 blocks 128, 119; 172,
+// 159.  2048 -> 1024, 192 blocks 24.1, 28.0; 44.2, 49.1; 256 blocks 30.0, 28.7; 54.2, 52.2; 320 blocks
+// 36.5, 40.8; 61.9, 64.8.  512 -> 1024, 256 blocks 12.4, 13.3; 31.9, 30.2; 336 blocks 16.4, 17.4; 38.6,
+// 36.4; 384 blocks 17.7, 17.8; 39.7, 37.5.  256 tokens 7168 -> 3584, 56 blocks, 33.1, 76.7.  Below 256
+// tokens the large tiles' rows past the batch weigh more (160 tokens 3584 -> 16384, 256 blocks,
+// 37.6, 44.0).
+static bool big_tiles(int64_t T, int32_t K, int32_t N) {
+  const int64_t blocks = ceil_div(T, 128) * ceil_div(N, 128);
+  return blocks >= 384 || (T >= 256 && K >= 2048 && (blocks > 320 || (blocks > 192 && blocks <= 256)));
+}
 
 // Tile of a smaller batch: the largest of 64 x 64, 64 x 32 and 32 x 32 (tokens x
 // rows) that still gives the grid about one block per CU, since a few dozen blocks (the
@@ -574,7 +583,7 @@ static int small_tile(int64_t T, int32_t N) {
 // the latent projections, with the adapters' term or without
 template <bool LORA>
 static hipError_t launch_projection(const DenseMfmaArgs& a, hipStream_t st) {
-  if (ceil_div(a.T, 128) * ceil_div(a.N, 128) >= DM_BIG_BLOCKS)
+  if (big_tiles(a.T, a.K, a.N))
     return dm_dma_pays(a.T, a.N, 128, 128) ? launch_dm_dma<4, 4, false, 2, LORA>(a, st)
                                            : launch_dm<4, 4, 2, false, LORA>(a, st);
   switch (small_tile(a.T, a.N)) {
