@@ -32,7 +32,10 @@
  *    scale bytes (rows x cols/32; scale s means 2^(s-127), 255 is NaN).
  *  - rounding points: h = bf16(x W_d^T); g, u fp32; a = bf16(act(g) * u);
  *    y fp32; z = bf16(sum_j w_j y_j); out = bf16(z W_u^T); round to nearest
- *    even.  act = SiLU; the SiTU formula is not on the pages, so
+ *    even.  g, u and y are sums of the block-scaled matrix cores, which drop
+ *    what lies 13 binary places below the largest of eight neighbouring
+ *    products: at most 7 2^-13 of the sum of the products' absolute values,
+ *    2^-14 to 2^-17 of it as measured.  act = SiLU; the SiTU formula is not on the pages, so
  *    MOE_ACT_SITU returns MOE_ERR_UNSUPPORTED.
  *
  * Conventions for every entry point:
@@ -391,7 +394,9 @@ moe_status moe_linear_bf16(const void* in, const void* W, int64_t num_tokens, in
  *    different ranks share one stack.  rank NULL: every adapter has max_rank.  A value
  *    outside 0..max_rank counts as the nearer end.
  *  - A token whose id lies outside [0, num_adapters) (-1, say) has no adapter: its row is
- *    the projection alone.
+ *    the projection alone, by the kernels that the call takes: bit for bit the row of
+ *    moe_linear_bf16 (or moe_layer_forward) with as many tokens, except where moe_linear_lora
+ *    takes the matrix cores below 32 tokens: there it is moe_linear_bf16's row in a call of 32.
  *  - Rows do not mix: an infinity or NaN in one adapter reaches only its own tokens. */
 typedef struct {
   const void* a;          /* bf16 [num_adapters][max_rank][n_in], 16-byte aligned */
@@ -438,9 +443,9 @@ moe_status moe_layer_forward_lora(const void* x, const void* router_w, const voi
  * MOE_DECODE_MAX_ROWS, in two launches (three with lora_down) instead of five or more.  The
  * result, routing outputs included, is that of moe_layer_forward / moe_layer_forward_lora bit
  * for bit.  It is the faster of the two with checkpoint records from two tokens on (7168-wide
- * tokens, 16 of 896 experts: 203 against 212 us, four tokens 350 against 375), with many rows on
+ * tokens, 16 of 896 experts: 200 against 211 us, four tokens 351 against 376), with many rows on
  * few experts, and where the host cannot keep five launches ahead of the GPU; with packed
- * experts the launches of moe_layer_forward take less otherwise (one token 84 against 90 us).
+ * experts the launches of moe_layer_forward take less otherwise (one token 85 against 90 us).
  *  - lora_down, lora_up: nullable adapters on the latent projections.
  *  - Larger batches, cfg->num_shared > 0 and routing->saliency return MOE_ERR_UNSUPPORTED.
  *  - Workspace: moe_layer_decode_workspace_size bytes, 16-byte aligned, needing no clearing;

@@ -238,8 +238,9 @@ moe_status run_router_and_down(const moe_config& c, const void* x, const void* r
 // what the matrix-core tiles cost beyond one reading.  Whole calls with adapters of rank 16, GEMV
 // and matrix cores: 7168 -> 3584 4 tokens 22.7 and 24.7 us, 5 tokens 36.8 and 25.5, 31 tokens 120
 // and 26.8; 3584 -> 7168 5 tokens 34.3 and 20.3; 2048 -> 1024 5 tokens 8.2 and 11.9, 31 tokens
-// 13.4 and 12.6; 512 -> 512 31 tokens 8.2 and 9.2.  (Entry points without adapters, and the layer,
-// keep the GEMV below 32: their results are older.)
+// 13.4 and 12.6; 512 -> 512 31 tokens 8.2 and 9.2.  (moe_linear_bf16 and the layer, whose results
+// without adapters others rely on, keep the GEMV below 32; with adapters the layer takes the same
+// kernels, so that a token without one gets the same bits.)
 bool lora_takes_mfma(int64_t T, int32_t n_in, int32_t n_out) {
   return T < 32 && n_in % 64 == 0 && (ceil_div(T, 4) - 1) * n_in * n_out >= (int64_t)1 << 24;
 }

@@ -30,20 +30,25 @@
 // words start as all ones, which none of them can be (a NaN is written as 0x7FC0 or
 // 0x7FC00000), and a reader asks again until a word is another.  The launch
 // before sets counters and words.
+// That a relaxed agent-scope store has reached the memory side once vmcnt is zero, that later
+// additions are seen behind it, and that a load issued after a polled value came back reads no
+// older data, is how this chip works and what the order of the instructions here relies on.  The
+// language's memory model would ask for release and acquire, which write back and invalidate a
+// whole L2 each.
 //
 // Measured (7168-wide tokens, latent 3584, FFN 3072, 16 of 896 experts; packed experts but where
-// records are named).  One token reads 397 MB in 87.7 us, 4.5 TB/s: 12.7 us the first launch;
+// records are named).  One token reads 397 MB in 86.3 us, 4.6 TB/s: 12.7 us the first launch;
 // in the second the routing and the first chunk end at 10.5, a block's gate / up at 40 in the
 // median and 53 at the latest, its down at 63 and 69, z is there at 71, and the up rows, which
 // are on chip by then, take 3.  The first 10 us and the last 5 stream little, the blocks' spread
 // at the two hand-overs costs as much again: that is what bounds it.  Against the five launches
 // of moe_layer_forward, in graphs of 50 steps on experts of their own, here / there in us:
 //   tokens                    1           2           3           4
-//   packed experts         90.3 / 83.9  152 / 144   213 / 204   258 / 240
-//   checkpoint records      123 / 119   203 / 212   281 / 304   350 / 375
+//   packed experts         90.1 / 85.4  153 / 145   212 / 203   263 / 244
+//   checkpoint records      122 / 119   200 / 211   285 / 305   351 / 376
 // and eight MXFP8 tokens of a middle layer (2048, 1024, 512, 8 of 64, packed) 53.6 / 57.5, one
-// token of it 31.2 / 23.8, four of a tiny layer over records 27.4 / 27.3, one over packed experts
-// 22.9 / 21.1.  So it is for records, for many rows of few experts, and where five launches
+// token of it 30.4 / 24.0, four of a tiny layer over records 27.4 / 27.3, one over packed experts
+// 22.5 / 21.3.  So it is for records, for many rows of few experts, and where five launches
 // cost the host more than the card; several blocks a CU, which cover one another's spread, are
 // worth more than three launches where the packed streams set the pace.
 // Slower: a wave per down item; the latent rows and the routing in this launch too; more steps in

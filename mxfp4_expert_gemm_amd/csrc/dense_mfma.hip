@@ -79,13 +79,14 @@ __device__ __forceinline__ uint32_t finite2(uint32_t v) { return v & ~((not_fini
 // must not reach another request's row.  An infinity or NaN in B meets the first term of u only,
 // which is zero where u is; the later ones may be zero or not, and would make a NaN of it.
 // What it costs is the wait for B, 16 bytes a lane from the L2 or further: the pieces of U
-// adapters are loaded together, four but for 64 rows a wave, where two spill 34 registers
-// (4096 tokens, 32 adapters of rank 32, 3584 -> 7168: 503 us, one 444; one adapter on each run
-// of tokens: 279 and 251).  Tokens of one request usually stand together, so most tiles meet
+// adapters are loaded together, four but for 64 rows a wave, where two take all 256 registers
+// (4096 tokens, 32 adapters of rank 32, 3584 -> 7168: 449 us, one 456; one adapter on each run
+// of tokens: 244 and 239).  Tokens of one request usually stand together, so most tiles meet
 // one adapter or two; a batch of single tokens can bring a new one with each (512 -> 256, 256
 // tokens with 64 adapters: 81.6 us when every 16 tokens fetched their adapters one by one in
-// tiles of 128 x 128, 14.7 now).  The third term of u costs 2% of a call where the ranks are
-// most (1021 tokens, 5 adapters to rank 128: 109 against 107 us), 1% at 4096 tokens of rank 32.
+// tiles of 128 x 128, 14.7 now).  The third term of u and the look for values that are not finite
+// cost 1 to 2% of a call (1021 tokens, 5 adapters to rank 128: 109 against 107 us; 4096 tokens of
+// rank 32 286 against 284).
 template <int WM, int WN>
 __device__ __forceinline__ void lora_expand(const DenseMfmaArgs& p, int64_t tb, int nb, f32x4_t (&acc)[WM][WN]) {
   constexpr int U = WN == 4 ? 1 : 4;

@@ -45,7 +45,8 @@ static int lora_slices(int64_t T, int32_t K, int32_t N) {
 // a wave per pair reads x R times and A T times through the L2.  Whole projections with 4
 // adapters, one after another over the tokens, 7168 -> 3584, first and second form: 64 tokens of
 // rank 128 34.9 and 57.9 us, 256 of rank 64 55.5 and 68.5, 512 of rank 16 68.9 and 70.7, 512 of
-// rank 64 144 and 144 (with 64 adapters 304 and 279), 1024 of rank 16 127 and 114.
+// rank 64 144 and 144 (with 64 adapters 304 and 279), 1024 of rank 16 127 and 114; the projections in
+// tiles of 64 x 64 throughout.
 static bool lora_grouped(int64_t T, int32_t R) { return T > 512 || T * R > 16384; }
 
 static LoraWs lora_ws(void* ws, int64_t T, int32_t K, int32_t N, int32_t R) {

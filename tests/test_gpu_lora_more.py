@@ -63,3 +63,17 @@ def test_rows_without_an_adapter_on_large_matrices(T, n_in, n_out):
     want = moe.linear_bf16(as_many, W)[:T] if 5 <= T < 32 else moe.linear_bf16(x, W)
     none = [t for t in range(T) if ids[t] < 0]
     assert torch.equal(got[none], want[none])
+
+
+def test_no_tokens():
+    """Calls without a token return empty outputs and touch nothing."""
+    d, L, F, E, k, N, R = 256, 128, 128, 8, 2, 3, 8
+    blob, w, down, up = layer_inputs(0, d, L, F, E, N, R, 5)
+    ids = torch.zeros(0, dtype=torch.int32)
+    dev = {n: t.cuda() for n, t in w.items()}
+    lo = dict(lora_down=dev_lora(down, ids), lora_up=dev_lora(up, ids))
+    assert moe.linear_lora(dev["x"], dev["latent_down"], lo["lora_down"]).shape == (0, L)
+    for fn in (moe.layer_forward, moe.layer_decode):
+        out = fn(dev["x"], dev["router_w"], dev["latent_down"], dev["latent_up"], torch.from_numpy(blob).cuda(), k, d_ffn=F, **lo)
+        assert out.shape == (0, d)
+    torch.cuda.synchronize()
