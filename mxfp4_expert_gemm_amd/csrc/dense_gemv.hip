@@ -65,7 +65,8 @@ __global__ void __launch_bounds__(256) dense_gemv_kernel(DenseParams p) {
   if (!valid) row = s.rows - 1;
   const int32_t K = p.K;
   const int64_t t0 = p.t_base + (int64_t)blockIdx.y * G;
-  if (blockIdx.y == 0) {
+  // asked of the kernel's arguments first: the grid's size comes from memory, 0.12 us for every launch
+  if (p.clear.nzero > 0 && blockIdx.y == 0) {
     for (int i = blockIdx.x * 256 + threadIdx.x; i < p.clear.nzero; i += gridDim.x * 256) p.clear.zero[32 * i] = 0;
     for (int i = blockIdx.x * 256 + threadIdx.x; i < p.clear.nones; i += gridDim.x * 256)
       p.clear.ones[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
