@@ -170,7 +170,11 @@ def _stream(stream=None):
 def _on(stream=None):
     """Where a call allocates: memory of the stream that its kernels use, so that neither what
     ran in it before nor what comes after a workspace is dropped can overlap them."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):  # anything that holds a cuda_stream
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    return torch.cuda.stream(stream)
 
 
 def make_config(num_tokens: int, d_model: int, d_latent: int, d_ffn: int, num_experts: int, *,

@@ -41,3 +41,18 @@ def test_linear_lora(T, R):
 def test_layer(T, fn, adapters):
     layer = Layer(T, 512, 256, 256, 16, 4, packed=True, adapters=adapters)
     beside(lambda s: layer.call(fn, stream=s), layer.call(fn))
+
+
+def test_a_stream_of_another_kind():
+    """Only the stream's pointer is asked for."""
+    side = torch.cuda.Stream()
+
+    class Handle:
+        cuda_stream = side.cuda_stream
+
+    layer = Layer(3, 512, 256, 256, 16, 4, packed=True)
+    want = layer.call(moe.layer_forward)
+    side.wait_stream(torch.cuda.current_stream())
+    out = layer.call(moe.layer_forward, stream=Handle())
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(out.view(torch.int16), want.view(torch.int16))
