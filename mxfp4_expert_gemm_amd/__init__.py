@@ -317,8 +317,9 @@ def layer_forward(x, router_w, latent_down, latent_up, expert_blob, k: int, *, d
         ref = lambda a: None if a is None else ctypes.byref(a)
         _check(lib().moe_layer_forward_lora(_p(x), _p(router_w), _p(latent_down), _p(latent_up), _p(expert_blob), k,
                                             ctypes.byref(cfg), _p(bias), _p(shared_blob) if num_shared > 0 else None,
-                                            ref(down), ref(up), _p(out), ref(r), _p(workspace), workspace.numel(),
-                                            _stream(stream)), "moe_layer_forward_lora")
+                                            ref(down), ref(up), _p(out), ref(r), _p(workspace),
+                                            workspace.numel() * workspace.element_size(), _stream(stream)),
+               "moe_layer_forward_lora")
         return out
     if workspace is None:
         with _on(stream):

@@ -55,3 +55,25 @@ def test_layer(name, fn):
 def test_layer_with_adapters_refuses_what_does_not_fit(bad):
     with pytest.raises(ValueError, match="must be|must hold|smaller"):
         moe.layer_forward(**layer_args(**bad), d_ffn=128, lora_up=lora(128, 256))
+
+
+@pytest.mark.parametrize("dtype", [torch.uint8, torch.int32, torch.float64])
+def test_a_workspace_counts_in_bytes(monkeypatch, dtype):
+    seen = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: seen.append((name, a)) or 0
+
+    real = moe.lib()
+    a = layer_args()
+    monkeypatch.setattr(moe, "lib", lambda: Lib())
+    monkeypatch.setattr(moe, "expert_bytes", real.moe_expert_bytes)
+    monkeypatch.setattr(moe, "_p", lambda t: None if t is None else t.data_ptr())
+    monkeypatch.setattr(moe, "_stream", lambda s: None)
+    monkeypatch.setattr(moe, "_same_device", lambda *t: None)
+    ws = torch.empty(800, dtype=dtype)
+    for fn in (moe.layer_forward, moe.layer_decode):
+        fn(**a, d_ffn=128, lora_up=lora(128, 256), workspace=ws)
+    moe.linear_lora(a["x"], bf(64, 256), lora(), workspace=ws)
+    assert [args[args.index(ws.data_ptr()) + 1] for _, args in seen] == [800 * ws.element_size()] * 3
