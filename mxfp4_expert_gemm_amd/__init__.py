@@ -38,7 +38,8 @@ EXPORTS = ["moe_expert_bytes", "moe_packed_expert_bytes", "moe_pack_experts", "m
            "moe_layer_forward_streamed", "moe_layer_forward_noalloc", "moe_reap_keep_bias",
            "moe_permute_workspace_size", "moe_linear_lora_workspace_size", "moe_linear_lora",
            "moe_layer_lora_workspace_size", "moe_layer_forward_lora", "moe_layer_decode_workspace_size",
-           "moe_layer_decode"]
+           "moe_layer_decode", "moe_gated_ffn_workspace_size", "moe_gated_ffn",
+           "moe_gated_ffn_backward_workspace_size", "moe_gated_ffn_backward"]
 
 
 class MoEError(RuntimeError):
@@ -137,6 +138,10 @@ def lib():
             "moe_layer_forward_lora": (ctypes.c_int, [vp, vp, vp, vp, vp, i32, cfgp, vp, vp, lp, lp, vp, rp, vp, sz,
                                                       vp]),
             "moe_layer_decode_workspace_size": (ctypes.c_int, [cfgp, i32, lp, lp, ctypes.POINTER(sz)]),
+            "moe_gated_ffn_workspace_size": (ctypes.c_int, [i64, i32, i32, ctypes.POINTER(sz)]),
+            "moe_gated_ffn": (ctypes.c_int, [vp, vp, vp, vp, i64, i32, i32, vp, vp, vp, vp, sz, vp]),
+            "moe_gated_ffn_backward_workspace_size": (ctypes.c_int, [i64, i32, i32, ctypes.POINTER(sz)]),
+            "moe_gated_ffn_backward": (ctypes.c_int, [vp] * 7 + [i64, i32, i32] + [vp] * 5 + [sz, vp]),
             "moe_layer_decode": (ctypes.c_int, [vp, vp, vp, vp, vp, i32, cfgp, vp, lp, lp, vp, rp, vp, sz, vp]),
         }
         for name, (res, args) in sig.items():
@@ -574,6 +579,84 @@ def linear_bf16(inp: torch.Tensor, W: torch.Tensor) -> torch.Tensor:
     return out
 
 
+def _bf16_shaped(**tensors):
+    """Each value is (tensor or None, shape): a bf16 tensor of that shape."""
+    for name, (t, shape) in tensors.items():
+        if t is not None and (tuple(t.shape) != shape or t.dtype not in _BF16):
+            raise ValueError(f"{name} must be a bf16 tensor of shape {shape}")
+
+
+def gated_ffn_workspace_size(num_tokens: int, d_model: int, d_ffn: int, backward: bool = False) -> int:
+    n = ctypes.c_size_t(0)
+    name = "moe_gated_ffn_backward_workspace_size" if backward else "moe_gated_ffn_workspace_size"
+    _check(getattr(lib(), name)(num_tokens, d_model, d_ffn, ctypes.byref(n)), name)
+    return int(n.value)
+
+
+def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor, *,
+              out: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+              up: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The dense gated feed-forward block (moe_gated_ffn): out = bf16(w_down (silu(w_gate x) w_up x)) for
+    x [T, d], w_gate and w_up [F, d], w_down [d, F].  gate and up [T, F], when given, receive the two
+    projections for gated_ffn_backward."""
+    T, d = x.shape
+    F = w_gate.shape[0]
+    _bf16_shaped(x=(x, (T, d)), w_gate=(w_gate, (F, d)), w_up=(w_up, (F, d)), w_down=(w_down, (d, F)), out=(out, (T, d)),
+                 gate=(gate, (T, F)), up=(up, (T, F)))
+    if (gate is None) != (up is None):
+        raise ValueError("gate and up are kept together")
+    _same_device(x, w_gate, w_up, w_down, out, gate, up, workspace)
+    with _on(stream):
+        if out is None:
+            out = torch.empty((T, d), dtype=x.dtype, device=x.device)
+        if workspace is None:
+            workspace = torch.empty(gated_ffn_workspace_size(T, d, F), dtype=torch.uint8, device=x.device)
+    _check(lib().moe_gated_ffn(_p(x), _p(w_gate), _p(w_up), _p(w_down), T, d, F, _p(out), _p(gate), _p(up),
+                               _p(workspace), workspace.numel() * workspace.element_size(), _stream(stream)),
+           "moe_gated_ffn")
+    return out
+
+
+class GatedFfnGrads(NamedTuple):
+    """What gated_ffn_backward gives: each shaped like what it is the gradient of, None where not asked for."""
+    dx: Optional[torch.Tensor]
+    dw_gate: Optional[torch.Tensor]
+    dw_up: Optional[torch.Tensor]
+    dw_down: Optional[torch.Tensor]
+
+
+def gated_ffn_backward(dout: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
+                       w_down: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, *, want_dx: bool = True,
+                       want_dw: bool = True, out: Optional[GatedFfnGrads] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None) -> GatedFfnGrads:
+    """The gradients of gated_ffn (moe_gated_ffn_backward) for dout [T, d], from its inputs and the gate
+    and up that it kept.  want_dx / want_dw leave one half out; out holds tensors to write them to."""
+    T, d = x.shape
+    F = w_gate.shape[0]
+    if not (want_dx or want_dw):
+        raise ValueError("want_dx or want_dw")
+    _bf16_shaped(dout=(dout, (T, d)), x=(x, (T, d)), w_gate=(w_gate, (F, d)), w_up=(w_up, (F, d)),
+                 w_down=(w_down, (d, F)), gate=(gate, (T, F)), up=(up, (T, F)))
+    shapes = dict(dx=(T, d) if want_dx else None, dw_gate=(F, d) if want_dw else None,
+                  dw_up=(F, d) if want_dw else None, dw_down=(d, F) if want_dw else None)
+    given = GatedFfnGrads(None, None, None, None) if out is None else out
+    for name, t in given._asdict().items():
+        if t is not None and shapes[name] is None:
+            raise ValueError(f"{name} is given and not wanted")
+        _bf16_shaped(**{name: (t, shapes[name])})
+    _same_device(x, dout, w_gate, w_up, w_down, gate, up, workspace, *given)
+    with _on(stream):
+        made = {n: t if t is not None or shapes[n] is None else torch.empty(shapes[n], dtype=x.dtype, device=x.device)
+                for n, t in given._asdict().items()}
+        if workspace is None:
+            workspace = torch.empty(gated_ffn_workspace_size(T, d, F, backward=True), dtype=torch.uint8, device=x.device)
+    got = GatedFfnGrads(**made)
+    _check(lib().moe_gated_ffn_backward(_p(dout), _p(x), _p(w_gate), _p(w_up), _p(w_down), _p(gate), _p(up), T, d, F,
+                                        *map(_p, got), _p(workspace), workspace.numel() * workspace.element_size(),
+                                        _stream(stream)), "moe_gated_ffn_backward")
+    return got
+
+
 def reap_saliency(y: torch.Tensor, topk_w: torch.Tensor, perm: torch.Tensor, expert_offsets: torch.Tensor,
                   num_experts: int, saliency: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Adds the REAP score sums of these routed rows to saliency (fp64 [E], zeros if None)."""
@@ -602,4 +685,5 @@ __all__ = ["lib", "MoEConfig", "RoutingOut", "MoEError", "make_config", "expert_
            "linear_bf16", "reap_saliency", "reap_prune_bias", "ACT_SILU", "ACT_SITU", "ROUTE_EXACT_ALL", "EXPORTS",
            "LIB_PATH", "expert_slots_bytes", "alloc_expert_slots", "layer_forward_streamed", "layer_forward_noalloc",
            "NOALLOC_SCRATCH_BYTES", "Lora", "linear_lora", "linear_lora_workspace_size", "layer_lora_workspace_size",
-           "layer_decode", "layer_decode_workspace_size", "DECODE_MAX_TOKENS", "DECODE_MAX_ROWS"]
+           "layer_decode", "layer_decode_workspace_size", "DECODE_MAX_TOKENS", "DECODE_MAX_ROWS",
+           "gated_ffn", "gated_ffn_backward", "gated_ffn_workspace_size", "GatedFfnGrads"]

@@ -18,6 +18,7 @@ constexpr int MAX_E = 1024;    // experts held in registers by the routing wave
 constexpr int MAX_DIM = 8192;  // columns a GEMV wave holds in registers
 constexpr int MAX_EXPERT_DIM = 7168;  // latent / FFN width whose staged activation rows fit LDS
 constexpr int MAX_SHARED = 8;
+constexpr int MAX_FFN_DIM = 32768;  // dense block: a tile's row offsets stay within 32 bits
 
 // Experts run as grouped GEMMs over 64-row tiles once they hold 8 routed rows on
 // average; below that, the streaming kernels that read each expert once per 4 rows.
@@ -113,6 +114,27 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return na && nb && x < y + nb && y < x + na;
+}
+
+// what a call reads or writes; a null pointer is not given
+struct Span {
+  const void* p;
+  size_t n;
+};
+// every span 16-byte aligned, and no output over an input or another output
+template <size_t NI, size_t NO>
+bool spans_fit(const Span (&in)[NI], const Span (&out)[NO]) {
+  for (const Span& s : in)
+    if (!aligned16(s.p)) return false;
+  for (size_t i = 0; i < NO; ++i) {
+    if (!aligned16(out[i].p)) return false;
+    if (!out[i].p) continue;
+    for (const Span& s : in)
+      if (s.p && overlap(out[i].p, out[i].n, s.p, s.n)) return false;
+    for (size_t j = 0; j < i; ++j)
+      if (out[j].p && overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return false;
+  }
+  return true;
 }
 
 moe_status check_config(const moe_config* c, int32_t k) {
@@ -1101,6 +1123,94 @@ moe_status moe_linear_lora(const void* in, const void* W, const moe_lora* lora, 
   if (lora_takes_mfma(num_tokens, n_in, n_out))
     return dev(launch_dense_mfma(static_cast<const uint16_t*>(in), num_tokens, n_in, s, st, &seg));
   return dev(launch_dense(static_cast<const uint16_t*>(in), num_tokens, n_in, &s, 1, st, &seg));
+}
+
+// ---- the dense gated block
+static moe_status check_ffn(int64_t T, int32_t d, int32_t F) {
+  if (T < 0 || d <= 0 || F <= 0 || d % 8 || F % 8) return MOE_ERR_INVALID_ARG;
+  if (T > (int64_t)1 << 24 || d > MAX_FFN_DIM || F > MAX_FFN_DIM) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status moe_gated_ffn_workspace_size(int64_t num_tokens, int32_t d_model, int32_t d_ffn, size_t* bytes) {
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_ffn(num_tokens, d_model, d_ffn));
+  *bytes = num_tokens == 0 ? 0 : ffn_layout(num_tokens, d_model, d_ffn).total;
+  return MOE_OK;
+}
+
+moe_status moe_gated_ffn(const void* x, const void* w_gate, const void* w_up, const void* w_down, int64_t num_tokens,
+                         int32_t d_model, int32_t d_ffn, void* out, void* gate, void* up, void* workspace,
+                         size_t workspace_bytes, moe_stream_t stream) {
+  MOE_TRY(check_ffn(num_tokens, d_model, d_ffn));
+  if (num_tokens == 0) return MOE_OK;
+  const size_t T = (size_t)num_tokens, d = (size_t)d_model, F = (size_t)d_ffn;
+  const size_t need = ffn_layout(num_tokens, d_model, d_ffn).total;
+  if (!x || !w_gate || !w_up || !w_down || !out || !gate != !up) return MOE_ERR_INVALID_ARG;
+  const Span in[] = {{x, 2 * T * d}, {w_gate, 2 * F * d}, {w_up, 2 * F * d}, {w_down, 2 * F * d}};
+  const Span to[] = {{out, 2 * T * d}, {gate, 2 * T * F}, {up, 2 * T * F}, {workspace, need}};
+  if (!spans_fit(in, to)) return MOE_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < need) return MOE_ERR_WORKSPACE;
+  FfnArgs a;
+  a.x = static_cast<const uint16_t*>(x);
+  a.w_gate = static_cast<const uint16_t*>(w_gate);
+  a.w_up = static_cast<const uint16_t*>(w_up);
+  a.w_down = static_cast<const uint16_t*>(w_down);
+  a.T = num_tokens;
+  a.d = d_model;
+  a.F = d_ffn;
+  a.out = static_cast<uint16_t*>(out);
+  a.gate = static_cast<uint16_t*>(gate);
+  a.up = static_cast<uint16_t*>(up);
+  return dev(launch_ffn(a, workspace, reinterpret_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_gated_ffn_backward_workspace_size(int64_t num_tokens, int32_t d_model, int32_t d_ffn, size_t* bytes) {
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_ffn(num_tokens, d_model, d_ffn));
+  *bytes = num_tokens == 0 ? 0 : ffn_backward_layout(num_tokens, d_model, d_ffn).total;
+  return MOE_OK;
+}
+
+moe_status moe_gated_ffn_backward(const void* dout, const void* x, const void* w_gate, const void* w_up,
+                                  const void* w_down, const void* gate, const void* up, int64_t num_tokens,
+                                  int32_t d_model, int32_t d_ffn, void* dx, void* dw_gate, void* dw_up, void* dw_down,
+                                  void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  MOE_TRY(check_ffn(num_tokens, d_model, d_ffn));
+  if (!dw_gate != !dw_up || !dw_gate != !dw_down || (num_tokens > 0 && !dx && !dw_gate)) return MOE_ERR_INVALID_ARG;
+  const size_t T = (size_t)num_tokens, d = (size_t)d_model, F = (size_t)d_ffn;
+  const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (num_tokens == 0) {
+    for (void* w : {dw_gate, dw_up, dw_down}) {
+      if (!w) continue;
+      if (!aligned16(w)) return MOE_ERR_INVALID_ARG;
+      MOE_TRY(zero_i32(static_cast<int32_t*>(w), d_model * (d_ffn / 2), st));
+    }
+    return MOE_OK;
+  }
+  const size_t need = ffn_backward_layout(num_tokens, d_model, d_ffn).total;
+  if (!dout || !x || !w_gate || !w_up || !w_down || !gate || !up) return MOE_ERR_INVALID_ARG;
+  const Span in[] = {{dout, 2 * T * d}, {x, 2 * T * d}, {w_gate, 2 * F * d}, {w_up, 2 * F * d}, {w_down, 2 * F * d},
+                     {gate, 2 * T * F}, {up, 2 * T * F}};
+  const Span to[] = {{dx, 2 * T * d}, {dw_gate, 2 * F * d}, {dw_up, 2 * F * d}, {dw_down, 2 * F * d}, {workspace, need}};
+  if (!spans_fit(in, to)) return MOE_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < need) return MOE_ERR_WORKSPACE;
+  FfnBackArgs a;
+  a.dout = static_cast<const uint16_t*>(dout);
+  a.x = static_cast<const uint16_t*>(x);
+  a.w_gate = static_cast<const uint16_t*>(w_gate);
+  a.w_up = static_cast<const uint16_t*>(w_up);
+  a.w_down = static_cast<const uint16_t*>(w_down);
+  a.gate = static_cast<const uint16_t*>(gate);
+  a.up = static_cast<const uint16_t*>(up);
+  a.T = num_tokens;
+  a.d = d_model;
+  a.F = d_ffn;
+  a.dx = static_cast<uint16_t*>(dx);
+  a.dw_gate = static_cast<uint16_t*>(dw_gate);
+  a.dw_up = static_cast<uint16_t*>(dw_up);
+  a.dw_down = static_cast<uint16_t*>(dw_down);
+  return dev(launch_ffn_backward(a, workspace, st));
 }
 
 }  // extern "C"

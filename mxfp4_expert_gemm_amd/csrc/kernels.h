@@ -253,4 +253,25 @@ hipError_t launch_decode(const DecodeArgs& a, bool packed, hipStream_t st);
 hipError_t launch_combine(const float* y, const float* w, int64_t T, int32_t k, int32_t L, uint16_t* z,
                           hipStream_t st);
 
+// ---- ffn.hip: the dense gated block and its backward pass
+struct FfnLayout {
+  size_t a, dgu, part, total;  // workspace: GLU rows, dG | dU, pieces of split sums
+};
+struct FfnArgs {
+  const uint16_t *x, *w_gate, *w_up, *w_down;  // [T][d], [F][d], [F][d], [d][F]
+  int64_t T;
+  int32_t d, F;
+  uint16_t *out, *gate, *up;  // [T][d]; nullable [T][F]
+};
+struct FfnBackArgs {
+  const uint16_t *dout, *x, *w_gate, *w_up, *w_down, *gate, *up;
+  int64_t T;
+  int32_t d, F;
+  uint16_t *dx, *dw_gate, *dw_up, *dw_down;  // nullable (dw_gate and dw_up together)
+};
+FfnLayout ffn_layout(int64_t T, int32_t d, int32_t F);
+FfnLayout ffn_backward_layout(int64_t T, int32_t d, int32_t F);
+hipError_t launch_ffn(const FfnArgs& p, void* ws, hipStream_t st);
+hipError_t launch_ffn_backward(const FfnBackArgs& p, void* ws, hipStream_t st);
+
 }  // namespace moe

@@ -186,14 +186,14 @@ __device__ __forceinline__ void read_a(AStep& a, const ALds& d, int m, int ntok,
 // argument + 32 and the product g e^g scaled back by 2^-32 (an fp32 multiply, which keeps
 // subnormal results).  NaN and infinities behave as in the exact formula: g = +inf gives
 // +inf, g = -inf NaN.
-__device__ __forceinline__ uint16_t glu_bf16(float g, float u) {
+__device__ __forceinline__ float silu_f32(float g) {
   const float x = -fabsf(g) * 1.44269504088896341f;  // log2 of e^-|g|
   const bool tiny = x < -120.f;
   const float e2 = __builtin_amdgcn_exp2f(tiny ? x + 32.f : x);  // e^-|g|, times 2^32 when tiny
   const float sc = tiny ? 0x1p-32f : 1.f;
   const float r = __builtin_amdgcn_rcpf(1.f + e2 * sc);
-  const float s = (g >= 0.f ? g : (g * e2) * sc) * r;
-  return f32_to_bf16(s * u);
+  return (g >= 0.f ? g : (g * e2) * sc) * r;
 }
+__device__ __forceinline__ uint16_t glu_bf16(float g, float u) { return f32_to_bf16(silu_f32(g) * u); }
 
 }  // namespace moe
