@@ -490,6 +490,39 @@ moe_status moe_gated_ffn_backward(const void* dout, const void* x, const void* w
                                   int32_t d_model, int32_t d_ffn, void* dx, void* dw_gate, void* dw_up, void* dw_down,
                                   void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
+/* ---- between two blocks of a residual stream ---- */
+
+/* The norm after a block, its gate and residual scale, the sum into the stream, and the norm
+ * before the next block, in one launch.  For each token, with rms(v) = sqrt(mean v^2 + eps):
+ *   v      = y / rms(y) * post_weight      (post_weight NULL: v = y)
+ *   out    = bf16(residual + scale * gate * v)       (gate NULL: 1)
+ *   normed = bf16(out / rms(out) * pre_weight), of the rounded out
+ * y, residual, out, normed bf16 [T][d]; post_weight, pre_weight bf16 [d]; gate bf16 [d]
+ * (gate_row_stride 0: one for all tokens) or [T][d] (gate_row_stride d).  y NULL: the norm alone,
+ * normed of residual, and post_weight, gate and out are NULL; pre_weight NULL: no normed.  Statistics
+ * and sums are fp32 (squares of values past 2^63 leave its range).  The K3 port's eps is fp32's,
+ * 2^-23 (kimi-k3-mlx digest, the choice of the RMSNorm eps).  d a multiple of 8, at most 8192; T up to
+ * 2^24; every pointer 16-byte aligned.  out may be residual itself; otherwise outputs overlap
+ * nothing. */
+moe_status moe_block_norms(const void* y, const void* residual, const void* post_weight, const void* pre_weight,
+                           const void* gate, int64_t gate_row_stride, int64_t num_tokens, int32_t d_model, float scale,
+                           float eps, void* out, void* normed, moe_stream_t stream);
+
+/* The gradients of that step, from the gradients dout of out and dnormed of normed (either may be
+ * NULL: zero) and the out that the forward pass gave (the residual where y is NULL; NULL without
+ * pre_weight):
+ *   dresidual, dy      bf16 [T][d]
+ *   dpost_weight, dpre_weight   fp32 [d], summed over the tokens in a fixed order
+ *   dgate              fp32 [d] for a gate of all tokens, bf16 [T][d] for one of each
+ * Any of them may be NULL; one whose input is NULL has to be.  dresidual may be dout itself.
+ * num_tokens 0 sets the fp32 gradients to zero. */
+moe_status moe_block_norms_backward_workspace_size(int64_t num_tokens, int32_t d_model, size_t* bytes);
+moe_status moe_block_norms_backward(const void* dout, const void* dnormed, const void* y, const void* out,
+                                    const void* post_weight, const void* pre_weight, const void* gate,
+                                    int64_t gate_row_stride, int64_t num_tokens, int32_t d_model, float scale, float eps,
+                                    void* dresidual, void* dy, float* dpost_weight, float* dpre_weight, void* dgate,
+                                    void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -39,7 +39,8 @@ EXPORTS = ["moe_expert_bytes", "moe_packed_expert_bytes", "moe_pack_experts", "m
            "moe_permute_workspace_size", "moe_linear_lora_workspace_size", "moe_linear_lora",
            "moe_layer_lora_workspace_size", "moe_layer_forward_lora", "moe_layer_decode_workspace_size",
            "moe_layer_decode", "moe_gated_ffn_workspace_size", "moe_gated_ffn",
-           "moe_gated_ffn_backward_workspace_size", "moe_gated_ffn_backward"]
+           "moe_gated_ffn_backward_workspace_size", "moe_gated_ffn_backward", "moe_block_norms",
+           "moe_block_norms_backward_workspace_size", "moe_block_norms_backward"]
 
 
 class MoEError(RuntimeError):
@@ -106,6 +107,7 @@ def lib():
             raise ImportError(f"{LIB_PATH} is missing: build it with `python -m mxfp4_expert_gemm_amd.build`")
         L = ctypes.CDLL(LIB_PATH)
         vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+        f32 = ctypes.c_float
         cfgp, rp = ctypes.POINTER(MoEConfig), ctypes.POINTER(RoutingOut)
         lp = ctypes.POINTER(LoraArg)
         sig = {
@@ -142,6 +144,9 @@ def lib():
             "moe_gated_ffn": (ctypes.c_int, [vp, vp, vp, vp, i64, i32, i32, vp, vp, vp, vp, sz, vp]),
             "moe_gated_ffn_backward_workspace_size": (ctypes.c_int, [i64, i32, i32, ctypes.POINTER(sz)]),
             "moe_gated_ffn_backward": (ctypes.c_int, [vp] * 7 + [i64, i32, i32] + [vp] * 5 + [sz, vp]),
+            "moe_block_norms": (ctypes.c_int, [vp] * 5 + [i64, i64, i32, f32, f32, vp, vp, vp]),
+            "moe_block_norms_backward_workspace_size": (ctypes.c_int, [i64, i32, ctypes.POINTER(sz)]),
+            "moe_block_norms_backward": (ctypes.c_int, [vp] * 7 + [i64, i64, i32, f32, f32] + [vp] * 6 + [sz, vp]),
             "moe_layer_decode": (ctypes.c_int, [vp, vp, vp, vp, vp, i32, cfgp, vp, lp, lp, vp, rp, vp, sz, vp]),
         }
         for name, (res, args) in sig.items():
@@ -657,6 +662,110 @@ def gated_ffn_backward(dout: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor
     return got
 
 
+NORM_EPS = 2.0 ** -23  # fp32's, as the K3 port takes it
+
+
+def _gate_stride(gate, T: int, d: int) -> int:
+    """0 for one gate row of all tokens, d for one of each."""
+    if gate is None:
+        return 0
+    if gate.dtype not in _BF16 or tuple(gate.shape) not in ((d,), (T, d)):
+        raise ValueError(f"gate must be a bf16 tensor of shape {(d,)} or {(T, d)}")
+    return 0 if gate.dim() == 1 else d
+
+
+def block_norms(y: Optional[torch.Tensor], residual: torch.Tensor, *, pre_weight: Optional[torch.Tensor] = None,
+                post_weight: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None, scale: float = 1.0,
+                eps: float = NORM_EPS, out: Optional[torch.Tensor] = None, normed: Optional[torch.Tensor] = None,
+                stream=None):
+    """What stands between two blocks of a residual stream (moe_block_norms):
+    out = bf16(residual + scale * gate * norm(y) * post_weight) and normed = bf16(norm(out) * pre_weight).
+    post_weight None: y is not normed; gate [d], [T, d] or None; pre_weight None: normed is None; y None:
+    the norm of the stream alone, out is residual.  out may be residual.  Returns (out, normed)."""
+    T, d = residual.shape
+    if y is None and (out is not None or post_weight is not None or gate is not None or pre_weight is None):
+        raise ValueError("without y there is the norm before the next block alone: pre_weight, and no post_weight, gate or out")
+    if pre_weight is None and normed is not None:
+        raise ValueError("normed needs pre_weight")
+    _bf16_shaped(y=(y, (T, d)), residual=(residual, (T, d)), pre_weight=(pre_weight, (d,)),
+                 post_weight=(post_weight, (d,)), out=(out, (T, d)), normed=(normed, (T, d)))
+    stride = _gate_stride(gate, T, d)
+    _same_device(residual, y, pre_weight, post_weight, gate, out, normed)
+    with _on(stream):
+        if out is None and y is not None:
+            out = torch.empty((T, d), dtype=residual.dtype, device=residual.device)
+        if normed is None and pre_weight is not None:
+            normed = torch.empty((T, d), dtype=residual.dtype, device=residual.device)
+    _check(lib().moe_block_norms(_p(y), _p(residual), _p(post_weight), _p(pre_weight), _p(gate), stride, T, d, scale, eps,
+                                 _p(out), _p(normed), _stream(stream)), "moe_block_norms")
+    return (residual if y is None else out), normed
+
+
+class BlockNormsGrads(NamedTuple):
+    """What block_norms_backward gives: dresidual and dy bf16 [T, d], dpost_weight and dpre_weight fp32 [d],
+    dgate fp32 [d] for a gate of all tokens or bf16 [T, d] for one of each; None where there is no such input."""
+    dresidual: torch.Tensor
+    dy: Optional[torch.Tensor]
+    dpost_weight: Optional[torch.Tensor]
+    dpre_weight: Optional[torch.Tensor]
+    dgate: Optional[torch.Tensor]
+
+
+def block_norms_backward_workspace_size(num_tokens: int, d_model: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_block_norms_backward_workspace_size(num_tokens, d_model, ctypes.byref(n)),
+           "moe_block_norms_backward_workspace_size")
+    return int(n.value)
+
+
+def block_norms_backward(dout: Optional[torch.Tensor], dnormed: Optional[torch.Tensor], y: Optional[torch.Tensor],
+                         out: Optional[torch.Tensor], *, pre_weight: Optional[torch.Tensor] = None,
+                         post_weight: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                         scale: float = 1.0, eps: float = NORM_EPS, grads: Optional[BlockNormsGrads] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None) -> BlockNormsGrads:
+    """The gradients of block_norms (moe_block_norms_backward): dout and dnormed are those of its two results
+    (either may be None: zero), out is the stream that it returned (None without pre_weight); grads holds
+    tensors to write to, among which dresidual may be dout."""
+    first = next((t for t in (dout, dnormed) if t is not None), None)
+    if first is None:
+        raise ValueError("dout or dnormed")
+    T, d = first.shape
+    if y is None and (post_weight is not None or gate is not None or pre_weight is None):
+        raise ValueError("without y there is the norm before the next block alone: pre_weight, and no post_weight or gate")
+    if (pre_weight is None) != (out is None) or (pre_weight is None and dnormed is not None):
+        raise ValueError("out and dnormed belong to pre_weight")
+    _bf16_shaped(dout=(dout, (T, d)), dnormed=(dnormed, (T, d)), y=(y, (T, d)), out=(out, (T, d)),
+                 pre_weight=(pre_weight, (d,)), post_weight=(post_weight, (d,)))
+    stride = _gate_stride(gate, T, d)
+    shapes = dict(dresidual=(T, d), dy=None if y is None else (T, d), dpost_weight=None if post_weight is None else (d,),
+                  dpre_weight=None if pre_weight is None else (d,),
+                  dgate=None if gate is None else (T, d) if stride else (d,))
+    given = BlockNormsGrads(None, None, None, None, None) if grads is None else grads
+    for name, t in given._asdict().items():
+        if t is None:
+            continue
+        types = _BF16 if shapes[name] == (T, d) and (name != "dgate" or stride) and not name.endswith("weight") \
+            else (torch.float32,)
+        if shapes[name] is None or tuple(t.shape) != shapes[name] or t.dtype not in types:
+            raise ValueError(f"{name} must be a {types[0]} tensor of shape {shapes[name]}")
+    _same_device(first, dout, dnormed, y, out, pre_weight, post_weight, gate, workspace, *given)
+    with _on(stream):
+        made = {}
+        for n, t in given._asdict().items():
+            if t is None and shapes[n] is not None:
+                f32 = n.endswith("weight") or (n == "dgate" and not stride)
+                t = torch.empty(shapes[n], dtype=torch.float32 if f32 else first.dtype, device=first.device)
+            made[n] = t
+        if workspace is None:
+            workspace = torch.empty(block_norms_backward_workspace_size(T, d), dtype=torch.uint8, device=first.device)
+    got = BlockNormsGrads(**made)
+    _check(lib().moe_block_norms_backward(_p(dout), _p(dnormed), _p(y), _p(out), _p(post_weight), _p(pre_weight), _p(gate),
+                                          stride, T, d, scale, eps, *map(_p, got), _p(workspace),
+                                          workspace.numel() * workspace.element_size(), _stream(stream)),
+           "moe_block_norms_backward")
+    return got
+
+
 def reap_saliency(y: torch.Tensor, topk_w: torch.Tensor, perm: torch.Tensor, expert_offsets: torch.Tensor,
                   num_experts: int, saliency: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Adds the REAP score sums of these routed rows to saliency (fp64 [E], zeros if None)."""
@@ -686,4 +795,5 @@ __all__ = ["lib", "MoEConfig", "RoutingOut", "MoEError", "make_config", "expert_
            "LIB_PATH", "expert_slots_bytes", "alloc_expert_slots", "layer_forward_streamed", "layer_forward_noalloc",
            "NOALLOC_SCRATCH_BYTES", "Lora", "linear_lora", "linear_lora_workspace_size", "layer_lora_workspace_size",
            "layer_decode", "layer_decode_workspace_size", "DECODE_MAX_TOKENS", "DECODE_MAX_ROWS",
-           "gated_ffn", "gated_ffn_backward", "gated_ffn_workspace_size", "GatedFfnGrads"]
+           "gated_ffn", "gated_ffn_backward", "gated_ffn_workspace_size", "GatedFfnGrads", "NORM_EPS",
+           "block_norms", "block_norms_backward", "block_norms_backward_workspace_size", "BlockNormsGrads"]

@@ -1,5 +1,7 @@
 // C ABI of the MXFP4 Stable-LatentMoE layer: argument checks, workspace layout and
 // the order of kernels on the caller's stream.  No device memory is allocated here.
+#include <float.h>
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -1211,6 +1213,100 @@ moe_status moe_gated_ffn_backward(const void* dout, const void* x, const void* w
   a.dw_up = static_cast<uint16_t*>(dw_up);
   a.dw_down = static_cast<uint16_t*>(dw_down);
   return dev(launch_ffn_backward(a, workspace, st));
+}
+
+// ---- between two blocks
+static moe_status check_norms(const void* y, const void* post, const void* pre, const void* gate, int64_t gate_stride,
+                              int64_t T, int32_t d, float scale, float eps) {
+  if (T < 0 || d <= 0 || d % 8 || !(eps >= 0.f) || !(fabsf(scale) <= FLT_MAX) || !(eps <= FLT_MAX))
+    return MOE_ERR_INVALID_ARG;
+  if (gate_stride != 0 && gate_stride != d) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && !y && (post || gate || !pre)) return MOE_ERR_INVALID_ARG;  // the pointers of no tokens are null
+  if (T > (int64_t)1 << 24 || d > MAX_DIM) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status moe_block_norms(const void* y, const void* residual, const void* post_weight, const void* pre_weight,
+                           const void* gate, int64_t gate_row_stride, int64_t num_tokens, int32_t d_model, float scale,
+                           float eps, void* out, void* normed, moe_stream_t stream) {
+  MOE_TRY(check_norms(y, post_weight, pre_weight, gate, gate_row_stride, num_tokens, d_model, scale, eps));
+  if (num_tokens == 0) return MOE_OK;
+  if (!residual || !y != !out || !pre_weight != !normed) return MOE_ERR_INVALID_ARG;
+  const size_t row = 2 * (size_t)d_model, all = row * (size_t)num_tokens;
+  const Span in[] = {{y, all}, {out == residual ? nullptr : residual, all}, {post_weight, row}, {pre_weight, row},
+                     {gate, gate_row_stride ? all : row}};
+  const Span to[] = {{out, all}, {normed, all}};
+  if (!spans_fit(in, to)) return MOE_ERR_INVALID_ARG;
+  NormArgs a;
+  a.y = static_cast<const uint16_t*>(y);
+  a.residual = static_cast<const uint16_t*>(residual);
+  a.post = static_cast<const uint16_t*>(post_weight);
+  a.pre = static_cast<const uint16_t*>(pre_weight);
+  a.gate = static_cast<const uint16_t*>(gate);
+  a.gate_stride = gate_row_stride;
+  a.T = num_tokens;
+  a.d = d_model;
+  a.scale = scale;
+  a.eps = eps;
+  a.out = static_cast<uint16_t*>(out);
+  a.normed = static_cast<uint16_t*>(normed);
+  return dev(launch_block_norms(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_block_norms_backward_workspace_size(int64_t num_tokens, int32_t d_model, size_t* bytes) {
+  if (!bytes || num_tokens < 0 || d_model <= 0 || d_model % 8) return MOE_ERR_INVALID_ARG;
+  if (num_tokens > (int64_t)1 << 24 || d_model > MAX_DIM) return MOE_ERR_UNSUPPORTED;
+  *bytes = num_tokens == 0 ? 0 : norms_backward_ws_bytes(num_tokens, d_model);
+  return MOE_OK;
+}
+
+moe_status moe_block_norms_backward(const void* dout, const void* dnormed, const void* y, const void* out,
+                                    const void* post_weight, const void* pre_weight, const void* gate,
+                                    int64_t gate_row_stride, int64_t num_tokens, int32_t d_model, float scale, float eps,
+                                    void* dresidual, void* dy, float* dpost_weight, float* dpre_weight, void* dgate,
+                                    void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  MOE_TRY(check_norms(y, post_weight, pre_weight, gate, gate_row_stride, num_tokens, d_model, scale, eps));
+  const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  const bool rows = gate_row_stride != 0;
+  if (num_tokens == 0) {
+    for (void* w : {(void*)dpost_weight, (void*)dpre_weight, rows ? nullptr : dgate}) {
+      if (!w) continue;
+      if (!aligned16(w)) return MOE_ERR_INVALID_ARG;
+      MOE_TRY(zero_i32(static_cast<int32_t*>(w), d_model, st));
+    }
+    return MOE_OK;
+  }
+  if ((!dout && !dnormed) || (dnormed && !pre_weight) || !pre_weight != !out || (dy && !y) ||
+      (dpost_weight && !post_weight) || (dpre_weight && !pre_weight) || (dgate && !gate))
+    return MOE_ERR_INVALID_ARG;
+  const size_t row = 2 * (size_t)d_model, all = row * (size_t)num_tokens;
+  const size_t need = norms_backward_ws_bytes(num_tokens, d_model);
+  const Span in[] = {{dresidual == dout ? nullptr : dout, all}, {dnormed, all}, {y, all}, {out, all}, {post_weight, row},
+                     {pre_weight, row}, {gate, rows ? all : row}};
+  const Span to[] = {{dresidual, all}, {dy, all}, {dpost_weight, 2 * row}, {dpre_weight, 2 * row},
+                     {dgate, rows ? all : 2 * row}, {workspace, need}};
+  if (!spans_fit(in, to)) return MOE_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < need) return MOE_ERR_WORKSPACE;
+  NormBackArgs a;
+  a.dout = static_cast<const uint16_t*>(dout);
+  a.dnormed = static_cast<const uint16_t*>(dnormed);
+  a.y = static_cast<const uint16_t*>(y);
+  a.out = static_cast<const uint16_t*>(out);
+  a.post = static_cast<const uint16_t*>(post_weight);
+  a.pre = static_cast<const uint16_t*>(pre_weight);
+  a.gate = static_cast<const uint16_t*>(gate);
+  a.gate_stride = gate_row_stride;
+  a.T = num_tokens;
+  a.d = d_model;
+  a.scale = scale;
+  a.eps = eps;
+  a.dresidual = static_cast<uint16_t*>(dresidual);
+  a.dy = static_cast<uint16_t*>(dy);
+  a.dgate_rows = rows ? static_cast<uint16_t*>(dgate) : nullptr;
+  a.dpre = dpre_weight;
+  a.dpost = dpost_weight;
+  a.dgate = rows ? nullptr : static_cast<float*>(dgate);
+  return dev(launch_block_norms_backward(a, workspace, st));
 }
 
 }  // extern "C"

@@ -274,4 +274,28 @@ FfnLayout ffn_backward_layout(int64_t T, int32_t d, int32_t F);
 hipError_t launch_ffn(const FfnArgs& p, void* ws, hipStream_t st);
 hipError_t launch_ffn_backward(const FfnBackArgs& p, void* ws, hipStream_t st);
 
+// ---- norms.hip: the norms, gate and sum between two blocks of a residual stream
+struct NormArgs {
+  const uint16_t *y, *residual, *post, *pre, *gate;  // y, post, pre, gate nullable
+  int64_t gate_stride;                               // 0: one row for all tokens, or d
+  int64_t T;
+  int32_t d;
+  float scale, eps;
+  uint16_t *out, *normed;  // with y; with pre
+};
+struct NormBackArgs {
+  const uint16_t *dout, *dnormed, *y, *out, *post, *pre, *gate;
+  int64_t gate_stride;
+  int64_t T;
+  int32_t d;
+  float scale, eps;
+  uint16_t *dresidual, *dy, *dgate_rows;  // nullable
+  float *dpre, *dpost, *dgate;            // nullable, [d]
+  float* part;                            // set by the launcher: [3][blocks][d]
+  int32_t sums;                           // set by the launcher: which of dpre, dpost, dgate
+};
+size_t norms_backward_ws_bytes(int64_t T, int32_t d);
+hipError_t launch_block_norms(const NormArgs& a, hipStream_t st);
+hipError_t launch_block_norms_backward(const NormBackArgs& a, void* ws, hipStream_t st);
+
 }  // namespace moe

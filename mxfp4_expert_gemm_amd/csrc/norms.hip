@@ -1,0 +1,442 @@
+// What stands between two blocks of a residual stream, in one pass over it: the norm after a
+// block, its gate and residual scale, the sum into the stream, and the norm before the next
+// block; and the gradients of all of that.
+//   forward:   v = y / rms(y) post (or v = y),  out = bf16(residual + scale gate v),
+//              normed = bf16(out / rms(out) pre),  rms(t) = sqrt(mean t^2 + eps)
+//   backward:  with r = out, rh = r / rms(r), e = dnormed pre:
+//              G = dout + (e - rh mean(e rh)) / rms(r)   (the gradient of out and of residual)
+//              dpre = sum_t dnormed rh,  dgate = scale G v (summed over t for one gate of all tokens)
+//              with yh = y / rms(y), b = scale gate G, f = b post:
+//              dpost = sum_t b yh,  dy = (f - yh mean(f yh)) / rms(y)   (dy = b without a norm)
+// Bound: HBM.  A row is held in registers from its first load on, so each tensor is read and
+// written once: 8 bytes an element forward, 12 backward, 2 and 4 more with a gate of each token.
+// A row belongs to one wave, or to four or eight where it is long.  Sums are fp32.
+#include "common.h"
+#include "kernels.h"
+
+namespace moe {
+
+namespace {
+
+__device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
+  const uint32_t d[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16lo(d[i]);
+    v[2 * i + 1] = bf16hi(d[i]);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  uint32_t d[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bf16x2_t p = {(__bf16)v[2 * i], (__bf16)v[2 * i + 1]};
+    d[i] = __builtin_bit_cast(uint32_t, p);
+  }
+  return make_uint4(d[0], d[1], d[2], d[3]);
+}
+__device__ __forceinline__ uint4 load16(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ void store16(uint16_t* p, const uint4& v) { *reinterpret_cast<uint4*>(p) = v; }
+
+// N sums over the WPR waves of a row, to all of them.  `turn` alternates between two places of
+// the LDS, so that one barrier is enough: a wave writes a place again only behind the next
+// barrier, which every wave reaches after it has read the place.
+template <int WPR, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float* lds, int turn) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_sum_dpp(v[i]);
+  if constexpr (WPR > 1) {
+    const int wave = threadIdx.x / WAVE, nw = blockDim.x / WAVE;
+    float* at = lds + turn * nw * 4;
+    if (lane_id() == 0)
+#pragma unroll
+      for (int i = 0; i < N; ++i) at[4 * wave + i] = v[i];
+    lds_barrier();
+    const int first = wave / WPR * WPR;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < WPR; ++w) s += at[4 * (first + w) + i];
+      v[i] = s;
+    }
+  }
+}
+
+__device__ __forceinline__ float inverse_rms(float squares, float inv_d, float eps) {
+  return 1.f / sqrtf(squares * inv_d + eps);
+}
+
+// WPR waves a row, C pieces of 8 columns a thread
+template <int WPR, int C>
+__global__ void __launch_bounds__(256) block_norms_kernel(NormArgs p) {
+  constexpr int GT = WPR * WAVE, ROWS = 256 / GT;
+  __shared__ float red[2 * 4 * 4];
+  const int at = threadIdx.x % GT;
+  int64_t t = (int64_t)blockIdx.x * ROWS + threadIdx.x / GT;
+  if constexpr (ROWS > 1) {
+    if (t >= p.T) return;  // a wave of its own: no barrier waits for it
+  }
+  const int64_t row = t * p.d;
+  uint4 y[C], r[C], g[C], pw[C], nw[C];
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int col = 8 * (at + GT * c);
+    const bool in = col < p.d;
+    y[c] = in && p.y ? load16(p.y + row + col) : zero;
+    r[c] = in ? load16(p.residual + row + col) : zero;
+    g[c] = in && p.gate ? load16(p.gate + t * p.gate_stride + col) : zero;
+    pw[c] = in && p.post ? load16(p.post + col) : zero;
+    nw[c] = in && p.pre ? load16(p.pre + col) : zero;
+  }
+  const float inv_d = 1.f / (float)p.d;
+  float m = p.scale;
+  if (p.post) {
+    float s[1] = {0.f};
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      float v[8];
+      unpack8(y[c], v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[0] += v[i] * v[i];
+    }
+    row_sums<WPR>(s, red, 0);
+    m = inverse_rms(s[0], inv_d, p.eps);
+  }
+  float s[1] = {0.f};
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    if (p.y) {
+      float v[8], o[8], w[8];
+      unpack8(y[c], v);
+      unpack8(r[c], o);
+      if (p.post) {
+        unpack8(pw[c], w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = v[i] * m * w[i] * p.scale;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= p.scale;
+      }
+      if (p.gate) {
+        unpack8(g[c], w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= w[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] += v[i];
+      r[c] = pack8(o);
+      const int col = 8 * (at + GT * c);
+      if (col < p.d) store16(p.out + row + col, r[c]);
+    }
+    float v[8];
+    unpack8(r[c], v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[0] += v[i] * v[i];
+  }
+  if (!p.pre) return;
+  row_sums<WPR>(s, red, 1);
+  const float k = inverse_rms(s[0], inv_d, p.eps);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int col = 8 * (at + GT * c);
+    float v[8], w[8];
+    unpack8(r[c], v);
+    unpack8(nw[c], w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = v[i] * k * w[i];
+    if (col < p.d) store16(p.normed + row + col, pack8(v));
+  }
+}
+
+// Sums over the tokens are kept by each thread for its columns over all rows of its group, joined
+// over the block's groups in LDS, and written as one row of partial sums per block (which = 0
+// dpre, 1 dpost, 2 dgate); join_norm_sums adds those in the blocks' order.  So the blocks are few
+// and go on from row to row, the next row's loads on their way while one is worked on.
+constexpr int NB_THREADS = 512;
+
+template <int WPR, int C>
+__global__ void __launch_bounds__(NB_THREADS) block_norms_backward_kernel(NormBackArgs p) {
+  constexpr int GT = WPR * WAVE, ROWS = NB_THREADS / GT;
+  extern __shared__ __align__(16) uint8_t lds[];
+  float* red = reinterpret_cast<float*>(lds);           // [2][8 waves][4]
+  float* sums = reinterpret_cast<float*>(lds) + 2 * 8 * 4;  // [ROWS - 1][columns], at the end
+  const int at = threadIdx.x % GT, group = threadIdx.x / GT;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  const float inv_d = 1.f / (float)p.d;
+  const int64_t turns = ceil_div(p.T, (int64_t)gridDim.x * ROWS);
+
+  uint4 nw[C], pw[C], gw[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int col = 8 * (at + GT * c);
+    const bool in = col < p.d;
+    nw[c] = in && p.pre ? load16(p.pre + col) : zero;
+    pw[c] = in && p.post ? load16(p.post + col) : zero;
+    gw[c] = in && p.gate && p.gate_stride == 0 ? load16(p.gate + col) : zero;
+  }
+  float apre[C][8], apost[C][8], agate[C][8];
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) apre[c][i] = apost[c][i] = agate[c][i] = 0.f;
+
+  uint4 dout[C], dn[C], y[C], r[C], g[C];
+  auto load = [&](int64_t turn) {
+    int64_t t = (turn * gridDim.x + blockIdx.x) * ROWS + group;
+    if (t >= p.T) t = p.T - 1;  // read, and not used
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int col = 8 * (at + GT * c);
+      const bool in = col < p.d;
+      const int64_t e = t * p.d + col;
+      dout[c] = in && p.dout ? load16(p.dout + e) : zero;
+      dn[c] = in && p.dnormed ? load16(p.dnormed + e) : zero;
+      r[c] = in && p.pre ? load16(p.out + e) : zero;
+      y[c] = in && p.y ? load16(p.y + e) : zero;
+      g[c] = in && p.gate && p.gate_stride ? load16(p.gate + e) : gw[c];
+    }
+  };
+  load(0);
+  for (int64_t turn = 0; turn < turns; ++turn) {
+    const int64_t t = (turn * gridDim.x + blockIdx.x) * ROWS + group;
+    const bool live = t < p.T;
+    const int64_t row = t * p.d;
+    uint4 cd[C], cn[C], cy[C], cr[C], cg[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      cd[c] = dout[c];
+      cn[c] = dn[c];
+      cy[c] = y[c];
+      cr[c] = r[c];
+      cg[c] = g[c];
+    }
+    if (turn + 1 < turns) load(turn + 1);
+    float s[3] = {0.f, 0.f, 0.f};  // r^2, e r, y^2
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      float a[8], b[8], w[8];
+      if (p.pre) {
+        unpack8(cr[c], a);
+        unpack8(cn[c], b);
+        unpack8(nw[c], w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          s[0] += a[i] * a[i];
+          s[1] += b[i] * w[i] * a[i];
+        }
+      }
+      if (p.post) {
+        unpack8(cy[c], a);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[2] += a[i] * a[i];
+      }
+    }
+    row_sums<WPR>(s, red, 0);
+    const float ir = inverse_rms(s[0], inv_d, p.eps), mean = s[1] * inv_d * ir * ir;  // mean(e rh) / rms(r)
+    const float iy = p.post ? inverse_rms(s[2], inv_d, p.eps) : 1.f;
+    float f[C][8], q[1] = {0.f};
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int col = 8 * (at + GT * c);
+      float G[8], a[8], b[8], w[8], gt[8];
+      unpack8(cd[c], G);
+      if (p.pre) {
+        unpack8(cr[c], a);
+        unpack8(cn[c], b);
+        unpack8(nw[c], w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float rh = a[i] * ir;
+          G[i] += ir * (b[i] * w[i]) - rh * mean;
+          if (live) apre[c][i] += b[i] * rh;
+        }
+      }
+      if (live && col < p.d && p.dresidual) store16(p.dresidual + row + col, pack8(G));
+      if (p.y) {
+        unpack8(cy[c], a);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) G[i] *= p.scale;
+        if (p.post) {
+          unpack8(pw[c], w);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = 1.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] *= iy;
+        if (p.gate) {
+          unpack8(cg[c], gt);
+          float dg[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            dg[i] = G[i] * (a[i] * w[i]);
+            if (live) agate[c][i] += dg[i];
+            G[i] *= gt[i];
+          }
+          if (p.gate_stride && p.dgate_rows && live && col < p.d) store16(p.dgate_rows + row + col, pack8(dg));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (live) apost[c][i] += G[i] * a[i];
+          f[c][i] = G[i] * w[i];
+          q[0] += f[c][i] * a[i];
+        }
+      }
+    }
+    if (p.y) {
+      if (p.post) {
+        row_sums<WPR>(q, red, 1);
+        q[0] *= inv_d;
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int col = 8 * (at + GT * c);
+        if (p.post) {
+          float a[8];
+          unpack8(cy[c], a);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[c][i] = iy * (f[c][i] - a[i] * iy * q[0]);
+        }
+        if (live && col < p.d && p.dy) store16(p.dy + row + col, pack8(f[c]));
+      }
+    }
+    if (WPR > 1 && !(p.y && p.post)) lds_barrier();  // one of the two places is read by all before it is written again
+  }
+
+  if (!p.part) return;
+  auto join = [&](float (&acc)[C][8], int which) {
+    if (!(p.sums >> which & 1)) return;
+    lds_barrier();
+    if (group > 0)
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<float4*>(sums + ((group - 1) * C * GT + c * GT + at) * 8 + 4 * h) =
+              make_float4(acc[c][4 * h], acc[c][4 * h + 1], acc[c][4 * h + 2], acc[c][4 * h + 3]);
+    lds_barrier();
+    if (group > 0) return;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int col = 8 * (at + GT * c);
+      if (col >= p.d) continue;
+      float* to = p.part + ((int64_t)which * gridDim.x + blockIdx.x) * p.d + col;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float4 v = make_float4(acc[c][4 * h], acc[c][4 * h + 1], acc[c][4 * h + 2], acc[c][4 * h + 3]);
+        for (int o = 1; o < ROWS; ++o) {
+          const float4 w = *reinterpret_cast<const float4*>(sums + ((o - 1) * C * GT + c * GT + at) * 8 + 4 * h);
+          v.x += w.x;
+          v.y += w.y;
+          v.z += w.z;
+          v.w += w.w;
+        }
+        *reinterpret_cast<float4*>(to + 4 * h) = v;
+      }
+    }
+  };
+  join(apre, 0);
+  join(apost, 1);
+  join(agate, 2);
+}
+
+// column sums of the blocks' rows: 16 slices of the rows a block, joined in their order
+__global__ void __launch_bounds__(256) join_norm_sums(const float* __restrict__ part, int rows, int32_t d,
+                                                      float* dpre, float* dpost, float* dgate) {
+  __shared__ float4 sh[16][16];
+  float* out = blockIdx.y == 0 ? dpre : blockIdx.y == 1 ? dpost : dgate;
+  if (!out) return;
+  const int x = threadIdx.x % 16, slice = threadIdx.x / 16;
+  const int col = (blockIdx.x * 16 + x) * 4;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (col < d) {
+    const float* p = part + (int64_t)blockIdx.y * rows * d + col;
+    for (int r = slice; r < rows; r += 16) {
+      const float4 w = *reinterpret_cast<const float4*>(p + (int64_t)r * d);
+      v.x += w.x;
+      v.y += w.y;
+      v.z += w.z;
+      v.w += w.w;
+    }
+  }
+  sh[slice][x] = v;
+  __syncthreads();
+  if (slice == 0 && col < d) {
+    for (int s = 1; s < 16; ++s) {
+      const float4 w = sh[s][x];
+      v.x += w.x;
+      v.y += w.y;
+      v.z += w.z;
+      v.w += w.w;
+    }
+    *reinterpret_cast<float4*>(out + col) = v;
+  }
+}
+
+// waves a row of the backward pass: two pieces of columns a thread, more do not fit its registers
+// beside the three sums of each and the next row
+int backward_waves(int32_t d) { return d <= 1024 ? 1 : d <= 4096 ? 4 : 8; }
+int64_t backward_blocks(int64_t T, int32_t d) {
+  const int64_t n = ceil_div(T, NB_THREADS / (backward_waves(d) * WAVE));
+  return n < 256 ? n : 256;
+}
+
+template <int WPR, int C>
+hipError_t launch_forward(const NormArgs& a, hipStream_t st) {
+  hipLaunchKernelGGL((block_norms_kernel<WPR, C>), dim3((unsigned)ceil_div(a.T, 4 / WPR)), dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+template <int WPR, int C>
+hipError_t launch_backward(const NormBackArgs& a, hipStream_t st) {
+  constexpr int LDS = 2 * 8 * 4 * 4 + (NB_THREADS / (WPR * WAVE) - 1) * C * WPR * WAVE * 8 * 4;
+  static_assert(LDS <= 65536, "no attribute needed");
+  hipLaunchKernelGGL((block_norms_backward_kernel<WPR, C>), dim3((unsigned)backward_blocks(a.T, a.d)),
+                     dim3(NB_THREADS), LDS, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t norms_backward_ws_bytes(int64_t T, int32_t d) { return (size_t)(3 * backward_blocks(T, d) * d) * 4; }
+
+hipError_t launch_block_norms(const NormArgs& a, hipStream_t st) {
+  const int c = (int)ceil_div(a.d, a.d <= 2048 ? 512 : 2048);
+  if (a.d <= 2048) {
+    switch (c) {
+      case 1: return launch_forward<1, 1>(a, st);
+      case 2: return launch_forward<1, 2>(a, st);
+      case 3: return launch_forward<1, 3>(a, st);
+      default: return launch_forward<1, 4>(a, st);
+    }
+  }
+  switch (c) {
+    case 2: return launch_forward<4, 2>(a, st);
+    case 3: return launch_forward<4, 3>(a, st);
+    default: return launch_forward<4, 4>(a, st);
+  }
+}
+
+hipError_t launch_block_norms_backward(const NormBackArgs& a0, void* ws, hipStream_t st) {
+  NormBackArgs a = a0;
+  a.sums = (a.dpre ? 1 : 0) | (a.dpost ? 2 : 0) | (a.dgate ? 4 : 0);
+  a.part = a.sums ? static_cast<float*>(ws) : nullptr;
+  hipError_t err;
+  if (a.d <= 512)
+    err = launch_backward<1, 1>(a, st);
+  else if (a.d <= 1024)
+    err = launch_backward<1, 2>(a, st);
+  else if (a.d <= 2048)
+    err = launch_backward<4, 1>(a, st);
+  else if (a.d <= 4096)
+    err = launch_backward<4, 2>(a, st);
+  else
+    err = launch_backward<8, 2>(a, st);
+  if (err != hipSuccess || !a.sums) return err;
+  hipLaunchKernelGGL(join_norm_sums, dim3((unsigned)ceil_div(a.d, 64), 3), dim3(256), 0, st, a.part,
+                     (int)backward_blocks(a.T, a.d), a.d, a.dpre, a.dpost, a.dgate);
+  return hipGetLastError();
+}
+
+}  // namespace moe
