@@ -523,6 +523,30 @@ moe_status moe_block_norms_backward(const void* dout, const void* dnormed, const
                                     void* dresidual, void* dy, float* dpost_weight, float* dpre_weight, void* dgate,
                                     void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
+/* ---- a projection in 8-bit integers ---- */
+
+/* The codes and scale of each row of x (bf16 [rows][n]): with top = max |x| over the row,
+ *   scale = top / 127 (fp32),  q = 127 x / top rounded to the nearest whole number, ties to even.
+ * A row of zeros has scale 0 and codes 0; a row with an infinity or NaN has scale NaN and codes 0,
+ * so that every product of it is NaN.  It serves tokens (a row a token) and, once, weights
+ * [n_out][n_in] (a row a channel).  n a multiple of 16, at most 65536; rows up to 2^24.  x, q and
+ * scale 16-byte aligned, no overlap. */
+moe_status moe_quantize_int8(const void* x, int64_t rows, int32_t n, void* q, float* scale, moe_stream_t stream);
+
+/* The projection of moe_linear_bf16 with codes for weights and tokens:
+ *   out[t][o] = bf16(x_scale[t] w_scale[o] sum_i x[t][i] W[o][i])
+ * W int8 [n_out][n_in] with w_scale fp32 [n_out].  x_scale not NULL: x int8 [T][n_in], one scale a
+ * token; x_scale NULL: x bf16 [T][n_in], quantised as by moe_quantize_int8 on the way in.  The sums
+ * are exact (codes from -128 to 127), then two fp32 products and one rounding; the product of sum and
+ * x_scale has to stay within fp32's range.  n_in a multiple of 16, at most 65536; any n_out; T up to 2^24.
+ * Every pointer 16-byte aligned.  out and workspace overlap nothing; workspace of moe_linear_int8_workspace_size bytes (quantize 1
+ * for x_scale NULL), needing no clearing; it may be NULL where that is 0. */
+moe_status moe_linear_int8_workspace_size(int64_t num_tokens, int32_t n_in, int32_t n_out, int32_t quantize,
+                                          size_t* bytes);
+moe_status moe_linear_int8(const void* x, const float* x_scale, const void* W, const float* w_scale, int64_t num_tokens,
+                           int32_t n_in, int32_t n_out, void* out, void* workspace, size_t workspace_bytes,
+                           moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -40,7 +40,8 @@ EXPORTS = ["moe_expert_bytes", "moe_packed_expert_bytes", "moe_pack_experts", "m
            "moe_layer_lora_workspace_size", "moe_layer_forward_lora", "moe_layer_decode_workspace_size",
            "moe_layer_decode", "moe_gated_ffn_workspace_size", "moe_gated_ffn",
            "moe_gated_ffn_backward_workspace_size", "moe_gated_ffn_backward", "moe_block_norms",
-           "moe_block_norms_backward_workspace_size", "moe_block_norms_backward"]
+           "moe_block_norms_backward_workspace_size", "moe_block_norms_backward", "moe_quantize_int8",
+           "moe_linear_int8_workspace_size", "moe_linear_int8"]
 
 
 class MoEError(RuntimeError):
@@ -147,6 +148,9 @@ def lib():
             "moe_block_norms": (ctypes.c_int, [vp] * 5 + [i64, i64, i32, f32, f32, vp, vp, vp]),
             "moe_block_norms_backward_workspace_size": (ctypes.c_int, [i64, i32, ctypes.POINTER(sz)]),
             "moe_block_norms_backward": (ctypes.c_int, [vp] * 7 + [i64, i64, i32, f32, f32] + [vp] * 6 + [sz, vp]),
+            "moe_quantize_int8": (ctypes.c_int, [vp, i64, i32, vp, vp, vp]),
+            "moe_linear_int8_workspace_size": (ctypes.c_int, [i64, i32, i32, i32, ctypes.POINTER(sz)]),
+            "moe_linear_int8": (ctypes.c_int, [vp, vp, vp, vp, i64, i32, i32, vp, vp, sz, vp]),
             "moe_layer_decode": (ctypes.c_int, [vp, vp, vp, vp, vp, i32, cfgp, vp, lp, lp, vp, rp, vp, sz, vp]),
         }
         for name, (res, args) in sig.items():
@@ -766,6 +770,60 @@ def block_norms_backward(dout: Optional[torch.Tensor], dnormed: Optional[torch.T
     return got
 
 
+def quantize_int8(x: torch.Tensor, *, q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                  stream=None):
+    """8-bit codes and a scale of each row of bf16 x [rows, n] (moe_quantize_int8): (q int8 [rows, n], scale fp32
+    [rows]), x about scale * q.  For tokens, and for the weights [n_out, n_in] of linear_int8."""
+    rows, n = x.shape
+    _bf16_shaped(x=(x, (rows, n)))
+    if q is not None and (tuple(q.shape) != (rows, n) or q.dtype != torch.int8):
+        raise ValueError(f"q must be an int8 tensor of shape {(rows, n)}")
+    if scale is not None and (tuple(scale.shape) != (rows,) or scale.dtype != torch.float32):
+        raise ValueError(f"scale must be an fp32 tensor of shape {(rows,)}")
+    _same_device(x, q, scale)
+    with _on(stream):
+        if q is None:
+            q = torch.empty((rows, n), dtype=torch.int8, device=x.device)
+        if scale is None:
+            scale = torch.empty((rows,), dtype=torch.float32, device=x.device)
+    _check(lib().moe_quantize_int8(_p(x), rows, n, _p(q), _p(scale), _stream(stream)), "moe_quantize_int8")
+    return q, scale
+
+
+def linear_int8_workspace_size(num_tokens: int, n_in: int, n_out: int, quantize: bool = True) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_linear_int8_workspace_size(num_tokens, n_in, n_out, int(quantize), ctypes.byref(n)),
+           "moe_linear_int8_workspace_size")
+    return int(n.value)
+
+
+def linear_int8(inp: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor, *, x_scale: Optional[torch.Tensor] = None,
+                out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """linear_bf16 with 8-bit codes (moe_linear_int8): W int8 [n_out, n_in] with w_scale fp32 [n_out]; inp bf16
+    [T, n_in], quantised token by token on the way in, or int8 with the tokens' x_scale fp32 [T].  out bf16 [T, n_out]."""
+    T, n_in = inp.shape
+    n_out = W.shape[0]
+    if tuple(W.shape) != (n_out, n_in) or W.dtype != torch.int8:
+        raise ValueError(f"W must be an int8 tensor of shape [n_out, {n_in}]")
+    if x_scale is None:
+        _bf16_shaped(inp=(inp, (T, n_in)))
+    elif inp.dtype != torch.int8 or tuple(x_scale.shape) != (T,) or x_scale.dtype != torch.float32:
+        raise ValueError(f"with x_scale, an fp32 tensor of shape {(T,)}, inp holds int8 codes")
+    if tuple(w_scale.shape) != (n_out,) or w_scale.dtype != torch.float32:
+        raise ValueError(f"w_scale must be an fp32 tensor of shape {(n_out,)}")
+    _bf16_shaped(out=(out, (T, n_out)))
+    _same_device(inp, W, w_scale, x_scale, out, workspace)
+    with _on(stream):
+        if out is None:
+            out = torch.empty((T, n_out), dtype=inp.dtype if x_scale is None else torch.bfloat16, device=inp.device)
+        if workspace is None:
+            workspace = torch.empty(linear_int8_workspace_size(T, n_in, n_out, x_scale is None), dtype=torch.uint8,
+                                    device=inp.device)
+    _check(lib().moe_linear_int8(_p(inp), _p(x_scale), _p(W), _p(w_scale), T, n_in, n_out, _p(out), _p(workspace),
+                                 workspace.numel() * workspace.element_size(), _stream(stream)), "moe_linear_int8")
+    return out
+
+
 def reap_saliency(y: torch.Tensor, topk_w: torch.Tensor, perm: torch.Tensor, expert_offsets: torch.Tensor,
                   num_experts: int, saliency: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Adds the REAP score sums of these routed rows to saliency (fp64 [E], zeros if None)."""
@@ -796,4 +854,5 @@ __all__ = ["lib", "MoEConfig", "RoutingOut", "MoEError", "make_config", "expert_
            "NOALLOC_SCRATCH_BYTES", "Lora", "linear_lora", "linear_lora_workspace_size", "layer_lora_workspace_size",
            "layer_decode", "layer_decode_workspace_size", "DECODE_MAX_TOKENS", "DECODE_MAX_ROWS",
            "gated_ffn", "gated_ffn_backward", "gated_ffn_workspace_size", "GatedFfnGrads", "NORM_EPS",
-           "block_norms", "block_norms_backward", "block_norms_backward_workspace_size", "BlockNormsGrads"]
+           "block_norms", "block_norms_backward", "block_norms_backward_workspace_size", "BlockNormsGrads",
+           "quantize_int8", "linear_int8", "linear_int8_workspace_size"]

@@ -20,6 +20,7 @@ constexpr int MAX_E = 1024;    // experts held in registers by the routing wave
 constexpr int MAX_DIM = 8192;  // columns a GEMV wave holds in registers
 constexpr int MAX_EXPERT_DIM = 7168;  // latent / FFN width whose staged activation rows fit LDS
 constexpr int MAX_SHARED = 8;
+constexpr int MAX_INT8_DIM = 65536;  // codes of -128: sums stay below 2^31
 constexpr int MAX_FFN_DIM = 32768;  // dense block: a tile's row offsets stay within 32 bits
 
 // Experts run as grouped GEMMs over 64-row tiles once they hold 8 routed rows on
@@ -1307,6 +1308,58 @@ moe_status moe_block_norms_backward(const void* dout, const void* dnormed, const
   a.dpost = dpost_weight;
   a.dgate = rows ? nullptr : static_cast<float*>(dgate);
   return dev(launch_block_norms_backward(a, workspace, st));
+}
+
+// ---- the 8-bit projection
+static moe_status check_int8(int64_t T, int32_t n_in, int32_t n_out) {
+  if (T < 0 || n_in <= 0 || n_out <= 0 || n_in % 16) return MOE_ERR_INVALID_ARG;
+  if (T > (int64_t)1 << 24 || n_in > MAX_INT8_DIM) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status moe_quantize_int8(const void* x, int64_t rows, int32_t n, void* q, float* scale, moe_stream_t stream) {
+  MOE_TRY(check_int8(rows, n, 1));
+  if (rows == 0) return MOE_OK;
+  if (!x || !q || !scale) return MOE_ERR_INVALID_ARG;
+  const size_t all = (size_t)rows * n;
+  const Span in[] = {{x, 2 * all}};
+  const Span to[] = {{q, all}, {scale, 4 * (size_t)rows}};
+  if (!spans_fit(in, to)) return MOE_ERR_INVALID_ARG;
+  return dev(launch_quantize_int8(static_cast<const uint16_t*>(x), rows, n, static_cast<int8_t*>(q), scale,
+                                  reinterpret_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_linear_int8_workspace_size(int64_t num_tokens, int32_t n_in, int32_t n_out, int32_t quantize,
+                                          size_t* bytes) {
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_int8(num_tokens, n_in, n_out));
+  *bytes = num_tokens == 0 ? 0 : int8_layout(num_tokens, n_in, n_out, quantize != 0).total;
+  return MOE_OK;
+}
+
+moe_status moe_linear_int8(const void* x, const float* x_scale, const void* W, const float* w_scale, int64_t num_tokens,
+                           int32_t n_in, int32_t n_out, void* out, void* workspace, size_t workspace_bytes,
+                           moe_stream_t stream) {
+  MOE_TRY(check_int8(num_tokens, n_in, n_out));
+  if (num_tokens == 0) return MOE_OK;
+  const bool quantize = !x_scale;
+  const Int8Layout l = int8_layout(num_tokens, n_in, n_out, quantize);
+  if (!x || !W || !w_scale || !out) return MOE_ERR_INVALID_ARG;
+  const size_t T = (size_t)num_tokens, K = (size_t)n_in, N = (size_t)n_out;
+  const Span in[] = {{x, T * K * (quantize ? 2 : 1)}, {x_scale, 4 * T}, {W, N * K}, {w_scale, 4 * N}};
+  const Span to[] = {{out, 2 * T * N}, {workspace, l.total}};
+  if (!spans_fit(in, to)) return MOE_ERR_INVALID_ARG;
+  if (l.total > 0 && (!workspace || workspace_bytes < l.total)) return MOE_ERR_WORKSPACE;
+  const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  const int8_t* q = static_cast<const int8_t*>(x);
+  if (quantize) {
+    int8_t* qw = at<int8_t>(workspace, l.q);
+    MOE_TRY(dev(launch_quantize_int8(static_cast<const uint16_t*>(x), num_tokens, n_in, qw, at<float>(workspace, l.scale), st)));
+    q = qw;
+    x_scale = at<float>(workspace, l.scale);
+  }
+  return dev(launch_linear_int8(q, x_scale, static_cast<const int8_t*>(W), w_scale, num_tokens, n_in, n_out,
+                                static_cast<uint16_t*>(out), at<int32_t>(workspace, l.part), st));
 }
 
 }  // extern "C"

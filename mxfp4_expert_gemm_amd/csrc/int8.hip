@@ -1,0 +1,175 @@
+// A projection in 8-bit integers: out[t][o] = bf16(x_scale[t] w_scale[o] sum_i q[t][i] W[o][i]), the
+// sums exact in 32 bits, on the tiles of tile_gemm.h (v_mfma_i32_16x16x64_i8: the same bytes a
+// step as the bf16 products, for twice the values); and the quantiser of its tokens,
+//   q = 127 x / max|x| rounded to the nearest whole number, ties to even, x_scale = max|x| / 127.
+#include "common.h"
+#include "kernels.h"
+#include "tile_gemm.h"
+
+namespace moe {
+
+namespace {
+
+struct EpiInt8 {
+  const float *xs, *ws;
+  uint16_t* out;
+  int32_t* part;  // split sums: [split][M][N]
+  int32_t M, N;
+  template <class C>
+  __device__ __forceinline__ void row(int m, int n, int rows, int split, const tg_i32x4 (&acc)[C::NJ]) const {
+    if (part) {
+      int32_t* p = part + ((int64_t)split * M + m) * N + n;
+#pragma unroll
+      for (int j = 0; j < C::NJ; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (n + 4 * j + r < rows) p[4 * j + r] = acc[j][r];
+      return;
+    }
+    const float s = xs[m];
+    uint16_t* o = out + (int64_t)m * N + n;
+#pragma unroll
+    for (int j = 0; j < C::NJ; ++j) {
+      if (n + 4 * j + 4 <= rows && N % 4 == 0) {
+        const float4 w = *reinterpret_cast<const float4*>(ws + n + 4 * j);
+        const bf16x2_t a = {(__bf16)((float)acc[j][0] * s * w.x), (__bf16)((float)acc[j][1] * s * w.y)};
+        const bf16x2_t b = {(__bf16)((float)acc[j][2] * s * w.z), (__bf16)((float)acc[j][3] * s * w.w)};
+        *reinterpret_cast<uint2*>(o + 4 * j) = make_uint2(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b));
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (n + 4 * j + r < rows) o[4 * j + r] = f32_to_bf16((float)acc[j][r] * s * ws[n + 4 * j + r]);
+      }
+    }
+  }
+};
+
+__global__ void __launch_bounds__(256) join_int8_kernel(const int32_t* __restrict__ part, int64_t n, int splits, int32_t N,
+                                                        const float* __restrict__ xs, const float* __restrict__ ws,
+                                                        uint16_t* __restrict__ out) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  int32_t v = 0;
+  for (int s = 0; s < splits; ++s) v += part[(int64_t)s * n + i];
+  const int64_t t = i / N;
+  out[i] = f32_to_bf16((float)v * xs[t] * ws[i - t * N]);
+}
+
+// One row a block.  Rows of up to 8192 values stay in registers between the search for the largest
+// and the codes; longer ones are read again.  The bits of |x| order like the values, with what is
+// not finite above them: such a row gets the scale NaN and codes 0, so that all of its results are
+// NaN.  127 x is exact in fp32 and the quotient's one Newton step makes every representable one
+// exact, so a tie (x = max / 2 is 63.5) is seen as one; other quotients lie further from a border
+// than their error.  Tiny and huge rows are scaled by a power of two first.
+__device__ __forceinline__ uint32_t pack_codes(float a, float b, float c, float d) {
+  return ((uint32_t)(int)a & 255u) | ((uint32_t)(int)b & 255u) << 8 | ((uint32_t)(int)c & 255u) << 16 | (uint32_t)(int)d << 24;
+}
+__global__ void __launch_bounds__(256) quantize_int8_kernel(const uint16_t* __restrict__ x, int32_t n, int8_t* __restrict__ q,
+                                                            float* __restrict__ scale) {
+  constexpr int C = 4;
+  __shared__ uint32_t tops[4];
+  const int64_t t = blockIdx.x;
+  const uint16_t* row = x + t * n;
+  uint4 v[C];
+  uint32_t top = 0;
+  auto look = [&](const uint4& w) {
+    const uint32_t d[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = d[i] & 0x7FFFu, hi = (d[i] >> 16) & 0x7FFFu;
+      top = max(top, max(lo, hi));
+    }
+  };
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int col = 8 * (threadIdx.x + 256 * c);
+    v[c] = col < n ? *reinterpret_cast<const uint4*>(row + col) : make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) look(v[c]);
+  for (int col = 8 * (threadIdx.x + 256 * C); col < n; col += 8 * 256) look(*reinterpret_cast<const uint4*>(row + col));
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
+  if (lane_id() == 0) tops[threadIdx.x / WAVE] = top;
+  __syncthreads();
+  top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+
+  const bool finite = top < 0x7F80u;
+  const float most = bf16f((uint16_t)top);
+  if (threadIdx.x == 0) scale[t] = finite ? most / 127.f : __builtin_nanf("");
+  const float f = most < 0x1p-60f ? 0x1p100f : most > 0x1p60f ? 0x1p-60f : 1.f;
+  const float a = most * f, m = 127.f * f;
+  const float inv = finite && top != 0 ? 1.f / a : 0.f;
+  auto code = [&](float xv) {
+    if (!finite) return 0.f;
+    const float p = xv * m, r = p * inv;
+    return rintf(fmaf(fmaf(-r, a, p), inv, r));
+  };
+  auto write = [&](const uint4& w, int col) {
+    const uint32_t d[4] = {w.x, w.y, w.z, w.w};
+    uint32_t o[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      o[h] = pack_codes(code(bf16lo(d[2 * h])), code(bf16hi(d[2 * h])), code(bf16lo(d[2 * h + 1])), code(bf16hi(d[2 * h + 1])));
+    *reinterpret_cast<uint2*>(q + t * n + col) = make_uint2(o[0], o[1]);
+  };
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int col = 8 * (threadIdx.x + 256 * c);
+    if (col < n) write(v[c], col);
+  }
+  for (int col = 8 * (threadIdx.x + 256 * C); col < n; col += 8 * 256) write(*reinterpret_cast<const uint4*>(row + col), col);
+}
+
+enum Int8Tile { I8_32, I8_64, I8_128, I8_256 };
+Int8Tile int8_tile(int64_t M, int64_t N) {
+  if (ceil_div(M, 256) * ceil_div(N, 256) >= 192) return I8_256;
+  return M > 64 ? I8_128 : M > 32 ? I8_64 : I8_32;
+}
+int int8_splits(int64_t M, int64_t N, int64_t K) {
+  const Int8Tile z = int8_tile(M, N);
+  const int64_t tiles = z == I8_256 ? 256 : z == I8_128 ? ceil_div(M, 128) * ceil_div(N, 128) : ceil_div(N, 32);
+  const int64_t most = K / 1024, want = 256 / tiles, s = want < most ? want : most;
+  return s < 1 ? 1 : s > 16 ? 16 : (int)s;
+}
+
+}  // namespace
+
+Int8Layout int8_layout(int64_t T, int32_t n_in, int32_t n_out, bool quantize) {
+  Int8Layout l;
+  l.scale = 0;
+  l.q = quantize ? align_up((size_t)T * 4, 256) : 0;
+  l.part = l.q + (quantize ? align_up((size_t)T * n_in, 256) : 0);
+  const int s = int8_splits(T, n_out, n_in);
+  l.total = l.part + (s > 1 ? align_up((size_t)s * T * n_out * 4, 256) : 0);
+  return l;
+}
+
+hipError_t launch_quantize_int8(const uint16_t* x, int64_t T, int32_t n, int8_t* q, float* scale, hipStream_t st) {
+  hipLaunchKernelGGL(quantize_int8_kernel, dim3((unsigned)T), dim3(256), 0, st, x, n, q, scale);
+  return hipGetLastError();
+}
+
+hipError_t launch_linear_int8(const int8_t* q, const float* xs, const int8_t* W, const float* ws, int64_t T, int32_t n_in,
+                              int32_t n_out, uint16_t* out, int32_t* part, hipStream_t st) {
+  TileArgs a{};
+  a.m = TileOperand{{q, q}, n_in, (int32_t)T};
+  a.n = TileOperand{{W, W}, n_in, n_out};
+  a.K = n_in;
+  a.splits = int8_splits(T, n_out, n_in);
+  const EpiInt8 e{xs, ws, out, a.splits > 1 ? part : nullptr, (int32_t)T, n_out};
+  hipError_t err;
+  switch (int8_tile(T, n_out)) {
+    case I8_256: err = launch_tile_gemm<TileCfg<8, 8, 2, 2, 1, 4, TILE_KMAJ, TILE_KMAJ, false, true>>(a, 1, e, st); break;
+    case I8_128: err = launch_tile_gemm<TileCfg<4, 4, 2, 2, 1, 4, TILE_KMAJ, TILE_KMAJ, false, true>>(a, 1, e, st); break;
+    case I8_64: err = launch_tile_gemm<TileCfg<2, 1, 2, 2, 2, 6, TILE_KMAJ, TILE_KMAJ, false, true>>(a, 1, e, st); break;
+    default: err = launch_tile_gemm<TileCfg<1, 1, 2, 2, 2, 6, TILE_KMAJ, TILE_KMAJ, false, true>>(a, 1, e, st); break;
+  }
+  if (err != hipSuccess || a.splits == 1) return err;
+  const int64_t n = T * n_out;
+  hipLaunchKernelGGL(join_int8_kernel, dim3((unsigned)ceil_div(n, 256)), dim3(256), 0, st, part, n, a.splits, n_out, xs, ws,
+                     out);
+  return hipGetLastError();
+}
+
+}  // namespace moe

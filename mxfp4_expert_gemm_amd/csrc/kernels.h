@@ -298,4 +298,13 @@ size_t norms_backward_ws_bytes(int64_t T, int32_t d);
 hipError_t launch_block_norms(const NormArgs& a, hipStream_t st);
 hipError_t launch_block_norms_backward(const NormBackArgs& a, void* ws, hipStream_t st);
 
+// ---- int8.hip: a projection in 8-bit integers and its quantiser
+struct Int8Layout {
+  size_t scale, q, part, total;  // workspace: the tokens' scales and codes, pieces of split sums
+};
+Int8Layout int8_layout(int64_t T, int32_t n_in, int32_t n_out, bool quantize);
+hipError_t launch_quantize_int8(const uint16_t* x, int64_t T, int32_t n, int8_t* q, float* scale, hipStream_t st);
+hipError_t launch_linear_int8(const int8_t* q, const float* xs, const int8_t* W, const float* ws, int64_t T, int32_t n_in,
+                              int32_t n_out, uint16_t* out, int32_t* part, hipStream_t st);
+
 }  // namespace moe
