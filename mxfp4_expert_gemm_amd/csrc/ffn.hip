@@ -177,12 +177,12 @@ size_t part_bytes(int64_t M, int64_t N, int64_t K, bool row_major) {
 
 template <int MO, int NO>
 hipError_t product_tiles(TileSize z, const TileArgs& a, int segs, const EpiRows& e, hipStream_t st) {
-  if (z == TILE_256) return launch_tile_gemm<TileCfg<8, 8, 2, 2, 1, 4, MO, NO, false>>(a, segs, e, st);
+  if (z == TILE_256) return launch_tile_gemm<TileCfg<8, 8, 2, 2, 5, MO, NO, false>>(a, segs, e, st);
   if constexpr (MO == TILE_KMAJ && NO == TILE_KMAJ) {
-    if (z == TILE_64) return launch_tile_gemm<TileCfg<2, 1, 2, 2, 2, 6, MO, NO, false>>(a, segs, e, st);
-    if (z == TILE_32) return launch_tile_gemm<TileCfg<1, 1, 2, 2, 2, 6, MO, NO, false>>(a, segs, e, st);
+    if (z == TILE_64) return launch_tile_gemm<TileCfg<2, 1, 2, 2, 13, MO, NO, false>>(a, segs, e, st);
+    if (z == TILE_32) return launch_tile_gemm<TileCfg<1, 1, 2, 2, 13, MO, NO, false>>(a, segs, e, st);
   }
-  return launch_tile_gemm<TileCfg<4, 4, 2, 2, 1, 4, MO, NO, false>>(a, segs, e, st);
+  return launch_tile_gemm<TileCfg<4, 4, 2, 2, 5, MO, NO, false>>(a, segs, e, st);
 }
 
 // out [M][N] (its rows from `cut` on at out1) = sum over `segs` segments of K; part: room for splits
@@ -237,10 +237,10 @@ hipError_t launch_ffn(const FfnArgs& p, void* ws, hipStream_t st) {
   const EpiGlu e{a, p.gate, p.up, p.F};
   hipError_t err;
   switch (tile_size(p.T, 2 * (int64_t)p.F, false)) {
-    case TILE_256: err = launch_tile_gemm<TileCfg<8, 8, 2, 2, 1, 4, TILE_KMAJ, TILE_KMAJ, true>>(t, 1, e, st); break;
-    case TILE_128: err = launch_tile_gemm<TileCfg<4, 4, 2, 2, 1, 4, TILE_KMAJ, TILE_KMAJ, true>>(t, 1, e, st); break;
-    case TILE_64: err = launch_tile_gemm<TileCfg<2, 2, 2, 2, 2, 6, TILE_KMAJ, TILE_KMAJ, true>>(t, 1, e, st); break;
-    default: err = launch_tile_gemm<TileCfg<1, 2, 2, 2, 2, 6, TILE_KMAJ, TILE_KMAJ, true>>(t, 1, e, st); break;
+    case TILE_256: err = launch_tile_gemm<TileCfg<8, 8, 2, 2, 5, TILE_KMAJ, TILE_KMAJ, true>>(t, 1, e, st); break;
+    case TILE_128: err = launch_tile_gemm<TileCfg<4, 4, 2, 2, 5, TILE_KMAJ, TILE_KMAJ, true>>(t, 1, e, st); break;
+    case TILE_64: err = launch_tile_gemm<TileCfg<2, 2, 2, 2, 13, TILE_KMAJ, TILE_KMAJ, true>>(t, 1, e, st); break;
+    default: err = launch_tile_gemm<TileCfg<1, 2, 2, 2, 13, TILE_KMAJ, TILE_KMAJ, true>>(t, 1, e, st); break;
   }
   if (err != hipSuccess) return err;
   t.m = operand(a, p.F, (int32_t)p.T);
@@ -263,8 +263,8 @@ hipError_t launch_ffn_backward(const FfnBackArgs& p, void* ws, hipStream_t st) {
   const EpiGluBack e{p.gate, p.up, a, dgu, p.F};
   hipError_t err =
       tile_size(T, p.F, true) == TILE_256
-          ? launch_tile_gemm<TileCfg<8, 8, 2, 2, 1, 4, TILE_KMAJ, TILE_RMAJ, false>>(t, 1, e, st)
-          : launch_tile_gemm<TileCfg<4, 4, 2, 2, 1, 4, TILE_KMAJ, TILE_RMAJ, false>>(t, 1, e, st);
+          ? launch_tile_gemm<TileCfg<8, 8, 2, 2, 5, TILE_KMAJ, TILE_RMAJ, false>>(t, 1, e, st)
+          : launch_tile_gemm<TileCfg<4, 4, 2, 2, 5, TILE_KMAJ, TILE_RMAJ, false>>(t, 1, e, st);
   if (err == hipSuccess && p.dx) {
     t.m = operand(dgu, 2 * (int64_t)p.F, T, dgu + p.F);
     t.n = operand(p.w_gate, p.d, p.d, p.w_up);

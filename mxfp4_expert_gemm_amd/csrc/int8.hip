@@ -160,10 +160,10 @@ hipError_t launch_linear_int8(const int8_t* q, const float* xs, const int8_t* W,
   const EpiInt8 e{xs, ws, out, a.splits > 1 ? part : nullptr, (int32_t)T, n_out};
   hipError_t err;
   switch (int8_tile(T, n_out)) {
-    case I8_256: err = launch_tile_gemm<TileCfg<8, 8, 2, 2, 1, 4, TILE_KMAJ, TILE_KMAJ, false, true>>(a, 1, e, st); break;
-    case I8_128: err = launch_tile_gemm<TileCfg<4, 4, 2, 2, 1, 4, TILE_KMAJ, TILE_KMAJ, false, true>>(a, 1, e, st); break;
-    case I8_64: err = launch_tile_gemm<TileCfg<2, 1, 2, 2, 2, 6, TILE_KMAJ, TILE_KMAJ, false, true>>(a, 1, e, st); break;
-    default: err = launch_tile_gemm<TileCfg<1, 1, 2, 2, 2, 6, TILE_KMAJ, TILE_KMAJ, false, true>>(a, 1, e, st); break;
+    case I8_256: err = launch_tile_gemm<TileCfg<8, 8, 2, 2, 5, TILE_KMAJ, TILE_KMAJ, false, true>>(a, 1, e, st); break;
+    case I8_128: err = launch_tile_gemm<TileCfg<4, 4, 2, 2, 5, TILE_KMAJ, TILE_KMAJ, false, true>>(a, 1, e, st); break;
+    case I8_64: err = launch_tile_gemm<TileCfg<2, 1, 2, 2, 13, TILE_KMAJ, TILE_KMAJ, false, true>>(a, 1, e, st); break;
+    default: err = launch_tile_gemm<TileCfg<1, 1, 2, 2, 13, TILE_KMAJ, TILE_KMAJ, false, true>>(a, 1, e, st); break;
   }
   if (err != hipSuccess || a.splits == 1) return err;
   const int64_t n = T * n_out;

@@ -7,12 +7,16 @@
 // the same matrices: dx = dg W reads W by its rows, dW = dg^T x reads both by their tokens.
 //
 // A block of WM x WN waves owns a tile of 16 MI WM x 16 NJ WN results, a wave 16 MI x 16 NJ of
-// them.  K moves in tiles of 32 KS values (64 KS bytes; 64 KS 8-bit values), loaded straight into
-// one of S stages of LDS S tiles ahead (lds loads of 16 bytes a lane), one barrier for a tile, and
-// the operands of the next step of 32 are read into registers while the current step's products
-// run.  What bounds it at large sizes is the LDS: a wave of 128 x 128 reads (128 + 128) x 64 bytes
-// for 64 products of 16 cycles, four waves half of the LDS's 128 bytes a cycle, the loads into LDS
-// a quarter.
+// them.  K moves in tiles of 128 bytes of it (64 bf16 or 128 8-bit values: whole lines of a K-major
+// operand, half lines cost each line two trips from the L2), two steps of 64 bytes a tile.
+// Operand tiles are loaded straight into LDS (16 bytes a lane) into a ring of R slots, M and N of
+// a tile one after another: while tile t is worked on, M of tile t + (R - 1) / 2 is loaded during
+// its first step, into the slot that N of tile t - 1 left, and N during its second, into the slot of
+// M of tile t, one barrier for a tile.  R is odd, so the ring holds one operand more than whole
+// tiles: five slots of 32 KB are all of the LDS.  The operands of the next step are read into
+// registers while the current step's products run.  What bounds it at large sizes is the LDS: a
+// wave of 128 x 128 reads (128 + 128) x 64 bytes for 64 products of 16 cycles, four waves half of
+// the LDS's 128 bytes a cycle, the loads into LDS a quarter.
 //
 // The operand that the matrix instruction calls A (its rows go to a lane's four result registers)
 // is N, so that a lane holds consecutive n; and the n of a wave are dealt to instructions so that
@@ -21,9 +25,8 @@
 // second the same rows of another; a lane holds both for the same f.
 //
 // LDS layouts, in pieces of 16 bytes, free of bank conflicts for the reads below:
-//  K-major: a row is 4 KS pieces, piece c stored at c ^ key(row) (KS = 2), or c ^ key(row) / 2
-//    (KS = 1, where two rows share 128 bytes), key = the row's bits 0, 1 and SB, the bit in which
-//    the rows read together by lanes 0-3 and 4-7 differ.
+//  K-major: a row is 8 pieces, piece c stored at c ^ key(row), key = the row's bits 0, 1 and SB, the
+//    bit in which the rows read together by lanes 0-3 and 4-7 differ.
 //  row-major: a k is R/8 pieces, piece p stored at p ^ f(k), read by the transposing LDS read: 16
 //    lanes hand in 4 k x 16 rows, and lane i receives row i's four k.
 #pragma once
@@ -66,15 +69,16 @@ __device__ __forceinline__ void tile_dma(const uint8_t* base, uint32_t off, uint
 __device__ __forceinline__ void tile_dma(const uint8_t* at, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(at), "s"(lds) : "memory");
 }
+// waits for all of the wave's loads into LDS but the last VM, and for its LDS reads, then for the block
 template <int VM>
 __device__ __forceinline__ void tile_wait_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(VM) : "memory");
 }
 
 // One operand's tile of R rows.  SB, J: see above; SPLIT: the second half of the rows comes from p[1].
-template <int ORDER, int R, int KS, int NW, int SB, int J, bool SPLIT>
+template <int ORDER, int R, int NW, int SB, int J, bool SPLIT>
 struct TileLoader {
-  static constexpr int BYTES = R * 64 * KS;
+  static constexpr int BYTES = R * 128;
   static constexpr int NU = BYTES / (1024 * NW);  // loads of a wave for one tile
   static_assert(NU * 1024 * NW == BYTES, "whole loads");
   static_assert(ORDER == TILE_KMAJ || R >= 128, "row-major tiles permute within 16 pieces");
@@ -95,18 +99,17 @@ struct TileLoader {
     for (int s = 0; s < 2; ++s)
       base[s] = static_cast<const uint8_t*>(o.p[s]) + (ORDER == TILE_KMAJ ? (int64_t)r0 * o.ld : (int64_t)r0 * 2);
     if constexpr (ORDER == TILE_KMAJ) {
-      step = 64 * KS;
+      step = 128;
       K16 = K * es;
     } else {
-      step = (int64_t)(32 * KS) * o.ld;
+      step = 64 * o.ld;
       K16 = K;
     }
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
       const int p = NW * u + wave;
       if constexpr (ORDER == TILE_KMAJ) {
-        const int row = p * (16 / KS) + lane / (4 * KS), pos = lane % (4 * KS);
-        const int c = pos ^ (KS == 1 ? key(row) >> 1 : key(row));
+        const int row = 8 * p + lane / 8, c = (lane % 8) ^ key(row);
         const int in = row % half;
         off[u] = (uint32_t)((in < left ? in : left - 1) * o.ld + 16 * c);
       } else {
@@ -131,11 +134,10 @@ struct TileLoader {
       const int p = NW * u + wave;
       bool in;
       if constexpr (ORDER == TILE_KMAJ) {
-        const int row = p * (16 / KS) + lane / (4 * KS), pos = lane % (4 * KS);
-        const int c = pos ^ (KS == 1 ? key(row) >> 1 : key(row));
-        in = (int64_t)kt * (64 * KS) + 16 * c < K16;
+        const int row = 8 * p + lane / 8, c = (lane % 8) ^ key(row);
+        in = (int64_t)kt * 128 + 16 * c < K16;
       } else {
-        in = (int64_t)kt * (32 * KS) + p * (512 / R) + lane / (R / 8) < K16;
+        in = (int64_t)kt * 64 + p * (512 / R) + lane / (R / 8) < K16;
       }
       const uint8_t* a = at(kt, u, seg1) + off[u];
       tile_dma(in ? a : reinterpret_cast<const uint8_t*>(tile_zero), lds + p * 1024);
@@ -143,27 +145,62 @@ struct TileLoader {
   }
 };
 
-// MI x NJ results of 16 x 16 a wave, WM x WN waves, K tiles of KS steps, S stages
-template <int MI_, int NJ_, int WM_, int WN_, int KS_, int S_, int MORD_, int NORD_, bool GLU_, bool I8_ = false>
+// MI x NJ results of 16 x 16 a wave, WM x WN waves, R slots
+template <int MI_, int NJ_, int WM_, int WN_, int R_, int MORD_, int NORD_, bool GLU_, bool I8_ = false>
 struct TileCfg {
-  static constexpr int MI = MI_, NJ = NJ_, WM = WM_, WN = WN_, KS = KS_, S = S_, MORD = MORD_, NORD = NORD_;
+  static constexpr int MI = MI_, NJ = NJ_, WM = WM_, WN = WN_, R = R_, MORD = MORD_, NORD = NORD_;
   static constexpr bool GLU = GLU_, I8 = I8_;
   static constexpr int NW = WM * WN, BM = 16 * MI * WM, BN = 16 * NJ * WN;
-  static constexpr int ES = I8 ? 1 : 2, BK = 64 * KS / ES;
+  static constexpr int ES = I8 ? 1 : 2, BK = 128 / ES;
   static constexpr int J = GLU ? NJ / 2 : NJ;  // a lane's consecutive n: 4 J
   static constexpr int SB = J == 8 ? 5 : J == 4 ? 4 : J == 2 ? 3 : 2;
-  static constexpr int STAGE = (BM + BN) * 64 * KS, LDS = S * STAGE;
+  static constexpr int SLOT = (BM > BN ? BM : BN) * 128, LDS = R * SLOT;
   // one wave a SIMD where the accumulators need it
   static constexpr int WAVES = MI * NJ > 32 ? 1 : 2;
+  static_assert(R % 2 == 1 && R >= 5, "two whole tiles (the first may be cut short) and one operand");
 };
+
+// acc += n m for one step.  Where the accumulators take half of the registers they are held in the
+// accumulation registers by hand: left to itself the compiler moves them back and forth (280 moves
+// for the 128 products of a K tile).  It does not know these instructions, so what it must not do
+// next to them is kept away: between two that share an accumulator lie 63 others, operands come
+// from LDS reads, which it waits for, and tile_settle stands before and after the loop.
+template <class C, class Acc>
+__device__ __forceinline__ void tile_mfma(Acc& acc, const u32x4_t& n, const u32x4_t& m) {
+  if constexpr (C::WAVES == 1) {
+    if constexpr (C::I8)
+      asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(n), "v"(m));
+    else
+      asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(n), "v"(m));
+  } else if constexpr (C::I8) {
+    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(tg_i32x4, n), __builtin_bit_cast(tg_i32x4, m), acc, 0, 0, 0);
+  } else {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(tg_bf16x8, n), __builtin_bit_cast(tg_bf16x8, m), acc, 0, 0, 0);
+  }
+}
+// 32 wait states between what writes the accumulators before it and what reads them behind it (a
+// product's result needs 18 at most)
+template <class C, class Acc>
+__device__ __forceinline__ void tile_settle(Acc (&acc)[C::MI][C::NJ]) {
+  if constexpr (C::WAVES == 1) {
+#pragma unroll
+    for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+      for (int j = 0; j < C::NJ; ++j) asm volatile("" : "+a"(acc[i][j]));
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+      for (int j = 0; j < C::NJ; ++j) asm volatile("" : "+a"(acc[i][j]));
+  }
+}
 
 template <class C, class Epi>
 __global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArgs p, Epi epi) {
-  constexpr int MI = C::MI, NJ = C::NJ, KS = C::KS, S = C::S, NW = C::NW, BM = C::BM, BN = C::BN, J = C::J;
-  using ML = TileLoader<C::MORD, BM, KS, NW, 2, 1, false>;
-  using NL = TileLoader<C::NORD, BN, KS, NW, C::SB, J, C::GLU>;
-  constexpr int NU = ML::NU + NL::NU;
-  constexpr int M_BYTES = BM * 64 * KS;
+  constexpr int MI = C::MI, NJ = C::NJ, R = C::R, H = (R - 1) / 2, NW = C::NW, BM = C::BM, BN = C::BN, J = C::J;
+  using ML = TileLoader<C::MORD, BM, NW, 2, 1, false>;
+  using NL = TileLoader<C::NORD, BN, NW, C::SB, J, C::GLU>;
+  constexpr int MU = ML::NU, NU = NL::NU;
   using Acc = std::conditional_t<C::I8, tg_i32x4, tg_f32x4>;
   extern __shared__ __align__(16) uint8_t lds[];
 
@@ -188,30 +225,22 @@ __global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArg
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
   const int full = (int)(p.K / C::BK), part = (p.nkt - full * (p.nkt / p.nk)) != 0 ? p.nkt / p.nk : 0;
 
-  // Tile t of this block's K range, to stage t % S.  Tiles that reach past K (one a segment) come
-  // first, so that only the first S loads have to look for them.
-  auto load_one = [&](int t, uint32_t at, auto uc) {
-    constexpr int U = decltype(uc)::value;
+  // Tile t of this block's K range.  Tiles that reach past K (one a segment) come first, so that
+  // only the loads ahead of the loop have to look for them.
+  auto place = [&](int t, bool& seg1) {
     int kt = k0 + t - part;
-    const bool seg1 = kt >= full;
-    if (seg1) kt -= full;
-    if constexpr (U < ML::NU)
-      ml.load(kt, seg1, U, at, wave);
-    else
-      nl.load(kt, seg1, U - ML::NU, at + M_BYTES, wave);
+    seg1 = kt >= full;
+    return seg1 ? kt - full : kt;
   };
-  auto load_first = [&](int t, uint32_t at) {
-    int kt = k0 + t;
-    bool seg1 = kt == 1;
-    if (kt < part) {
-      kt = full;
-    } else {
-      kt -= part;
-      seg1 = kt >= full;
-      if (seg1) kt -= full;
-    }
+  auto first_m = [&](int t, uint32_t at) {
+    bool seg1 = k0 + t == 1;
+    const int kt = k0 + t < part ? full : place(t, seg1);
     ml.load_tail(kt, seg1, at, wave, lane);
-    nl.load_tail(kt, seg1, at + M_BYTES, wave, lane);
+  };
+  auto first_n = [&](int t, uint32_t at) {
+    bool seg1 = k0 + t == 1;
+    const int kt = k0 + t < part ? full : place(t, seg1);
+    nl.load_tail(kt, seg1, at, wave, lane);
   };
 
   // the operands of one step in registers
@@ -226,26 +255,25 @@ __global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArg
     r.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(at + 4 * row_bytes));
     return r.v;
   };
-  auto read_m = [&](const uint8_t* stage, int ks, int i) -> u32x4_t {
+  auto read_m = [&](const uint8_t* slot, int ks, int i) -> u32x4_t {
     if constexpr (C::MORD == TILE_KMAJ) {
-      const int row = 16 * MI * wm + 16 * i + rho, c = 4 * ks + g, k = ML::key(rho);
-      return *reinterpret_cast<const u32x4_t*>(stage + row * (64 * KS) + 16 * (KS == 1 ? c ^ (k >> 1) : c ^ k));
+      const int row = 16 * MI * wm + 16 * i + rho;
+      return *reinterpret_cast<const u32x4_t*>(slot + row * 128 + 16 * ((4 * ks + g) ^ ML::key(rho)));
     } else {
       const int k = 32 * ks + 8 * g + (rho >> 2), q = rho & 3;
       const int piece = 2 * MI * wm + 2 * i + (q >> 1);
-      return tr_read(stage + k * (2 * BM) + 16 * (piece ^ ML::fold(rho >> 2)) + 8 * (q & 1), 2 * BM);
+      return tr_read(slot + k * (2 * BM) + 16 * (piece ^ ML::fold(rho >> 2)) + 8 * (q & 1), 2 * BM);
     }
   };
-  auto read_n = [&](const uint8_t* stage, int ks, int j) -> u32x4_t {
+  auto read_n = [&](const uint8_t* slot, int ks, int j) -> u32x4_t {
     const int h = C::GLU ? j / J : 0, jj = C::GLU ? j % J : j;
     const int at = h * (BN / 2) + 16 * J * wn + 4 * jj;
     if constexpr (C::NORD == TILE_KMAJ) {
-      const int row = at + 4 * J * (rho >> 2) + (rho & 3), c = 4 * ks + g;
-      const int k = (rho & 3) | ((rho >> 2) & 1) << 2;
-      return *reinterpret_cast<const u32x4_t*>(stage + M_BYTES + row * (64 * KS) + 16 * (KS == 1 ? c ^ (k >> 1) : c ^ k));
+      const int row = at + 4 * J * (rho >> 2) + (rho & 3), key = (rho & 3) | ((rho >> 2) & 1) << 2;
+      return *reinterpret_cast<const u32x4_t*>(slot + row * 128 + 16 * ((4 * ks + g) ^ key));
     } else {
       const int k = 32 * ks + 8 * g + (rho >> 2), col = at + 4 * J * (rho & 3);
-      return tr_read(stage + M_BYTES + k * (2 * BN) + 16 * ((col >> 3) ^ NL::fold(rho >> 2)) + 2 * (col & 7), 2 * BN);
+      return tr_read(slot + k * (2 * BN) + 16 * ((col >> 3) ^ NL::fold(rho >> 2)) + 2 * (col & 7), 2 * BN);
     }
   };
   Acc acc[MI][NJ];
@@ -254,89 +282,78 @@ __global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArg
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = Acc{0, 0, 0, 0};
 
-  // the products of one step from registers CUR, while the next step's operands are read into the
-  // others and, with FETCH (or FETCH 2 and `fetch`), tile td is loaded to sd
-  auto step = [&](auto curc, auto fetchc, bool fetch, const uint8_t* next, int ks_next, int td, uint32_t sd) {
-    constexpr int CUR = decltype(curc)::value, FETCH = decltype(fetchc)::value;
+  // the products of step KS, while the next step's operands are read into the other registers and,
+  // with FETCH, the step's operand of tile td (M in the first step, N in the second) is loaded to `to`
+  auto step = [&](auto ksc, auto fetchc, const uint8_t* next_m, const uint8_t* next_n, int td, uint32_t to) {
+    constexpr int KS = decltype(ksc)::value;
+    constexpr bool FETCH = decltype(fetchc)::value;
+    constexpr int U = KS == 0 ? MU : NU;
     unroll_n<MI>([&](auto qc) {
       constexpr int Q = decltype(qc)::value;
-      constexpr int U0 = Q * NU / MI, U1 = (Q + 1) * NU / MI;
-      if constexpr (FETCH != 0 && U1 > U0) {
-        if (FETCH == 1 || fetch)
-          unroll_n<U1 - U0>([&](auto uc) { load_one(td, sd, std::integral_constant<int, U0 + decltype(uc)::value>{}); });
+      if constexpr (FETCH) {
+        bool seg1;
+        const int kt = place(td, seg1);
+        unroll_n<(Q + 1) * U / MI - Q * U / MI>([&](auto uc) {
+          constexpr int X = Q * U / MI + decltype(uc)::value;
+          if constexpr (KS == 0)
+            ml.load(kt, seg1, X, to, wave);
+          else
+            nl.load(kt, seg1, X, to, wave);
+        });
       }
       constexpr int A = MI + NJ, R0 = Q * A / MI, R1 = (Q + 1) * A / MI;
       unroll_n<R1 - R0>([&](auto rc) {
-        constexpr int R = R0 + decltype(rc)::value;
-        if constexpr (R < NJ)
-          fn[CUR ^ 1][R] = read_n(next, ks_next, R);
+        constexpr int X = R0 + decltype(rc)::value;
+        if constexpr (X < NJ)
+          fn[KS ^ 1][X] = read_n(next_n, KS ^ 1, X);
         else
-          fm[CUR ^ 1][R - NJ] = read_m(next, ks_next, R - NJ);
+          fm[KS ^ 1][X - NJ] = read_m(next_m, KS ^ 1, X - NJ);
       });
       unroll_n<NJ>([&](auto jc) {
-        constexpr int JJ = decltype(jc)::value;
-        if constexpr (C::I8)
-          acc[Q][JJ] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(tg_i32x4, fn[CUR][JJ]),
-                                                             __builtin_bit_cast(tg_i32x4, fm[CUR][Q]), acc[Q][JJ], 0, 0, 0);
-        else
-          acc[Q][JJ] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(tg_bf16x8, fn[CUR][JJ]),
-                                                               __builtin_bit_cast(tg_bf16x8, fm[CUR][Q]), acc[Q][JJ], 0, 0, 0);
+        constexpr int X = decltype(jc)::value;
+        tile_mfma<C>(acc[Q][X], fn[KS][X], fm[KS][Q]);
       });
       __builtin_amdgcn_sched_barrier(0);
     });
   };
 
-  // Tile t.  At its last step every wave has its operands of tile t in registers, so that the
-  // barrier frees t's stage, and tile t + 1 has landed; the tiles behind that one (S - 2 of them,
-  // NU loads a wave each) may still be on their way.
-  auto run_tile = [&](auto parc, auto fetchc, int t, int stage) {
-    constexpr int P = decltype(parc)::value;  // the registers that hold the tile's first step
-    const uint8_t* here = lds + stage * C::STAGE;
-    const int sn = stage + 1 == S ? 0 : stage + 1;
-    unroll_n<KS - 1>([&](auto kc) {
-      constexpr int X = decltype(kc)::value;
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      step(std::integral_constant<int, (P + X) & 1>{}, std::integral_constant<int, 0>{}, false, here, X + 1, 0, 0);
-    });
-    if (decltype(fetchc)::value == 1 || t + S - 1 < nkt)
-      tile_wait_barrier<(S - 2) * NU>();
+  // Tile t, its M in slot sm.  At the barrier every wave has the operands of its second step in
+  // registers, which frees both slots, and tile t + 1 has landed; what was loaded behind that one (M
+  // and N of tiles t + 2 .. t + H - 1, and M of tile t + H) may still be on its way.
+  auto after = [](int slot, int by) { return slot + by >= R ? slot + by - R : slot + by; };
+  auto run_tile = [&](auto fetchc, int t, int sm) {
+    const int sn = after(sm, 1), next = after(sm, 2);
+    const uint8_t *m = lds + sm * C::SLOT, *n = lds + sn * C::SLOT;
+    step(std::integral_constant<int, 0>{}, fetchc, m, n, t + H, lds0 + after(sm, R - 1) * C::SLOT);
+    if constexpr (decltype(fetchc)::value)
+      tile_wait_barrier<(H - 1) * MU + (H - 2) * NU>();
     else
       tile_wait_barrier<0>();
-    step(std::integral_constant<int, (P + KS - 1) & 1>{}, fetchc, t + S < nkt, lds + sn * C::STAGE, 0, t + S,
-         lds0 + stage * C::STAGE);
+    step(std::integral_constant<int, 1>{}, fetchc, lds + next * C::SLOT, lds + after(next, 1) * C::SLOT, t + H,
+         lds0 + sm * C::SLOT);
+    return next;
   };
 
-  const int pre = nkt < S ? nkt : S;
-  for (int t = 0; t < pre; ++t) load_first(t, lds0 + t * C::STAGE);
-  if (nkt >= S)
-    tile_wait_barrier<(S - 1) * NU>();
+  const int pre = nkt < H ? nkt : H;
+  for (int t = 0; t < pre; ++t) {
+    first_m(t, lds0 + 2 * t * C::SLOT);
+    first_n(t, lds0 + (2 * t + 1) * C::SLOT);
+  }
+  if (nkt >= H)
+    tile_wait_barrier<(H - 1) * (MU + NU)>();
   else
     tile_wait_barrier<0>();
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) fn[0][j] = read_n(lds, 0, j);
+  for (int j = 0; j < NJ; ++j) fn[0][j] = read_n(lds + C::SLOT, 0, j);
 #pragma unroll
   for (int i = 0; i < MI; ++i) fm[0][i] = read_m(lds, 0, i);
-  // two tiles a turn (with an odd KS the registers swap from tile to tile), the last S or S + 1
-  // tiles, which load nothing, or little, in a loop of their own: a branch in the first one costs
-  // the accumulators their registers
-  auto after = [](int stage) { return stage + 1 == S ? 0 : stage + 1; };
-  int stage = 0, t = 0;
-  for (; t + 1 + S < nkt; t += 2) {
-    run_tile(std::integral_constant<int, 0>{}, std::integral_constant<int, 1>{}, t, stage);
-    stage = after(stage);
-    run_tile(std::integral_constant<int, KS & 1>{}, std::integral_constant<int, 1>{}, t + 1, stage);
-    stage = after(stage);
-  }
-  for (; t < nkt; t += 2) {
-    run_tile(std::integral_constant<int, 0>{}, std::integral_constant<int, 2>{}, t, stage);
-    stage = after(stage);
-    if (t + 1 < nkt) {
-      run_tile(std::integral_constant<int, KS & 1>{}, std::integral_constant<int, 2>{}, t + 1, stage);
-      stage = after(stage);
-    }
-  }
+  tile_settle<C>(acc);
+  int slot = 0, t = 0;
+  for (; t + H < nkt; ++t) slot = run_tile(std::true_type{}, t, slot);
+  for (; t < nkt; ++t) slot = run_tile(std::false_type{}, t, slot);  // nothing left to load
   // the reads of the step past the end are still on their way
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  tile_settle<C>(acc);
 
   // lane: results m = 16 i + rho, n = 4 J g .. 4 J g + 4 J - 1 (of each half)
 #pragma unroll
