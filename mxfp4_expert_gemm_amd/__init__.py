@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from typing import NamedTuple, Optional
 
@@ -588,18 +589,56 @@ def linear_bf16(inp: torch.Tensor, W: torch.Tensor) -> torch.Tensor:
     return out
 
 
-def _bf16_shaped(**tensors):
-    """Each value is (tensor or None, shape): a bf16 tensor of that shape."""
-    for name, (t, shape) in tensors.items():
-        if t is not None and (tuple(t.shape) != shape or t.dtype not in _BF16):
-            raise ValueError(f"{name} must be a bf16 tensor of shape {shape}")
+def _shaped(name: str, t: Optional[torch.Tensor], shape: tuple, dtypes=_BF16):
+    """t is None, or a tensor of that shape and of one of the types."""
+    if t is not None and (t.shape != shape or t.dtype not in dtypes):
+        raise ValueError(f"{name} must be a {dtypes[0]} tensor of shape {shape}")
 
 
-def gated_ffn_workspace_size(num_tokens: int, d_model: int, d_ffn: int, backward: bool = False) -> int:
+_F32, _I8 = (torch.float32,), (torch.int8,)
+
+
+def _pointers(*tensors):
+    """The device pointers (None: none) of contiguous tensors, all of which live on the current device."""
+    at = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (t.get_device() != at or not t.is_contiguous()):
+            if t.get_device() != at:
+                raise ValueError("the tensors must live on the current CUDA device")
+            raise ValueError("tensors passed to the HIP library must be contiguous")
+    return [None if t is None else t.data_ptr() for t in tensors]
+
+
+def _raw_stream(stream):
+    """The stream's handle.  The current one is asked for by the device's number: making the object that
+    torch.cuda.current_stream() returns takes as long as a launch."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
+
+
+_NOTHING = contextlib.nullcontext()
+
+
+def _at(stream):
+    """_on(stream), without a new object for the current stream."""
+    return _NOTHING if stream is None else _on(stream)
+
+
+def _bytes(workspace: torch.Tensor) -> int:
+    return workspace.numel() * workspace.element_size()
+
+
+def _host_size(name: str, *args) -> int:
     n = ctypes.c_size_t(0)
-    name = "moe_gated_ffn_backward_workspace_size" if backward else "moe_gated_ffn_workspace_size"
-    _check(getattr(lib(), name)(num_tokens, d_model, d_ffn, ctypes.byref(n)), name)
+    _check(getattr(lib(), name)(*args, ctypes.byref(n)), name)
     return int(n.value)
+
+
+@functools.lru_cache(maxsize=1024)
+def gated_ffn_workspace_size(num_tokens: int, d_model: int, d_ffn: int, backward: bool = False) -> int:
+    return _host_size("moe_gated_ffn_backward_workspace_size" if backward else "moe_gated_ffn_workspace_size",
+                      num_tokens, d_model, d_ffn)
 
 
 def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor, *,
@@ -610,18 +649,18 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down:
     projections for gated_ffn_backward."""
     T, d = x.shape
     F = w_gate.shape[0]
-    _bf16_shaped(x=(x, (T, d)), w_gate=(w_gate, (F, d)), w_up=(w_up, (F, d)), w_down=(w_down, (d, F)), out=(out, (T, d)),
-                 gate=(gate, (T, F)), up=(up, (T, F)))
+    for name, t, shape in (("x", x, (T, d)), ("w_gate", w_gate, (F, d)), ("w_up", w_up, (F, d)),
+                           ("w_down", w_down, (d, F)), ("out", out, (T, d)), ("gate", gate, (T, F)), ("up", up, (T, F))):
+        _shaped(name, t, shape)
     if (gate is None) != (up is None):
         raise ValueError("gate and up are kept together")
-    _same_device(x, w_gate, w_up, w_down, out, gate, up, workspace)
-    with _on(stream):
+    with _at(stream):
         if out is None:
-            out = torch.empty((T, d), dtype=x.dtype, device=x.device)
+            out = torch.empty_like(x)
         if workspace is None:
             workspace = torch.empty(gated_ffn_workspace_size(T, d, F), dtype=torch.uint8, device=x.device)
-    _check(lib().moe_gated_ffn(_p(x), _p(w_gate), _p(w_up), _p(w_down), T, d, F, _p(out), _p(gate), _p(up),
-                               _p(workspace), workspace.numel() * workspace.element_size(), _stream(stream)),
+    xp, wgp, wup, wdp, op, gp, up_, ws = _pointers(x, w_gate, w_up, w_down, out, gate, up, workspace)
+    _check(lib().moe_gated_ffn(xp, wgp, wup, wdp, T, d, F, op, gp, up_, ws, _bytes(workspace), _raw_stream(stream)),
            "moe_gated_ffn")
     return out
 
@@ -644,26 +683,27 @@ def gated_ffn_backward(dout: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor
     F = w_gate.shape[0]
     if not (want_dx or want_dw):
         raise ValueError("want_dx or want_dw")
-    _bf16_shaped(dout=(dout, (T, d)), x=(x, (T, d)), w_gate=(w_gate, (F, d)), w_up=(w_up, (F, d)),
-                 w_down=(w_down, (d, F)), gate=(gate, (T, F)), up=(up, (T, F)))
-    shapes = dict(dx=(T, d) if want_dx else None, dw_gate=(F, d) if want_dw else None,
-                  dw_up=(F, d) if want_dw else None, dw_down=(d, F) if want_dw else None)
-    given = GatedFfnGrads(None, None, None, None) if out is None else out
-    for name, t in given._asdict().items():
-        if t is not None and shapes[name] is None:
-            raise ValueError(f"{name} is given and not wanted")
-        _bf16_shaped(**{name: (t, shapes[name])})
-    _same_device(x, dout, w_gate, w_up, w_down, gate, up, workspace, *given)
-    with _on(stream):
-        made = {n: t if t is not None or shapes[n] is None else torch.empty(shapes[n], dtype=x.dtype, device=x.device)
-                for n, t in given._asdict().items()}
+    for name, t, shape in (("dout", dout, (T, d)), ("x", x, (T, d)), ("w_gate", w_gate, (F, d)), ("w_up", w_up, (F, d)),
+                           ("w_down", w_down, (d, F)), ("gate", gate, (T, F)), ("up", up, (T, F))):
+        _shaped(name, t, shape)
+    dx, dwg, dwu, dwd = (None, None, None, None) if out is None else out
+    if (dx is not None and not want_dx) or ((dwg is not None or dwu is not None or dwd is not None) and not want_dw):
+        raise ValueError("out holds a tensor that is not wanted")
+    for name, t, shape in (("dx", dx, (T, d)), ("dw_gate", dwg, (F, d)), ("dw_up", dwu, (F, d)), ("dw_down", dwd, (d, F))):
+        _shaped(name, t, shape)
+    with _at(stream):
+        if want_dx and dx is None:
+            dx = torch.empty_like(x)
+        if want_dw:
+            dwg = torch.empty_like(w_gate) if dwg is None else dwg
+            dwu = torch.empty_like(w_up) if dwu is None else dwu
+            dwd = torch.empty_like(w_down) if dwd is None else dwd
         if workspace is None:
-            workspace = torch.empty(gated_ffn_workspace_size(T, d, F, backward=True), dtype=torch.uint8, device=x.device)
-    got = GatedFfnGrads(**made)
-    _check(lib().moe_gated_ffn_backward(_p(dout), _p(x), _p(w_gate), _p(w_up), _p(w_down), _p(gate), _p(up), T, d, F,
-                                        *map(_p, got), _p(workspace), workspace.numel() * workspace.element_size(),
-                                        _stream(stream)), "moe_gated_ffn_backward")
-    return got
+            workspace = torch.empty(gated_ffn_workspace_size(T, d, F, True), dtype=torch.uint8, device=x.device)
+    p = _pointers(dout, x, w_gate, w_up, w_down, gate, up, dx, dwg, dwu, dwd, workspace)
+    _check(lib().moe_gated_ffn_backward(*p[:7], T, d, F, *p[7:], _bytes(workspace), _raw_stream(stream)),
+           "moe_gated_ffn_backward")
+    return GatedFfnGrads(dx, dwg, dwu, dwd)
 
 
 NORM_EPS = 2.0 ** -23  # fp32's, as the K3 port takes it
@@ -673,7 +713,7 @@ def _gate_stride(gate, T: int, d: int) -> int:
     """0 for one gate row of all tokens, d for one of each."""
     if gate is None:
         return 0
-    if gate.dtype not in _BF16 or tuple(gate.shape) not in ((d,), (T, d)):
+    if gate.dtype not in _BF16 or (gate.shape != (d,) and gate.shape != (T, d)):
         raise ValueError(f"gate must be a bf16 tensor of shape {(d,)} or {(T, d)}")
     return 0 if gate.dim() == 1 else d
 
@@ -691,17 +731,18 @@ def block_norms(y: Optional[torch.Tensor], residual: torch.Tensor, *, pre_weight
         raise ValueError("without y there is the norm before the next block alone: pre_weight, and no post_weight, gate or out")
     if pre_weight is None and normed is not None:
         raise ValueError("normed needs pre_weight")
-    _bf16_shaped(y=(y, (T, d)), residual=(residual, (T, d)), pre_weight=(pre_weight, (d,)),
-                 post_weight=(post_weight, (d,)), out=(out, (T, d)), normed=(normed, (T, d)))
+    for name, t, shape in (("y", y, (T, d)), ("residual", residual, (T, d)), ("pre_weight", pre_weight, (d,)),
+                           ("post_weight", post_weight, (d,)), ("out", out, (T, d)), ("normed", normed, (T, d))):
+        _shaped(name, t, shape)
     stride = _gate_stride(gate, T, d)
-    _same_device(residual, y, pre_weight, post_weight, gate, out, normed)
-    with _on(stream):
+    with _at(stream):
         if out is None and y is not None:
-            out = torch.empty((T, d), dtype=residual.dtype, device=residual.device)
+            out = torch.empty_like(residual)
         if normed is None and pre_weight is not None:
-            normed = torch.empty((T, d), dtype=residual.dtype, device=residual.device)
-    _check(lib().moe_block_norms(_p(y), _p(residual), _p(post_weight), _p(pre_weight), _p(gate), stride, T, d, scale, eps,
-                                 _p(out), _p(normed), _stream(stream)), "moe_block_norms")
+            normed = torch.empty_like(residual)
+    yp, rp, post, pre, gp, op, np_ = _pointers(y, residual, post_weight, pre_weight, gate, out, normed)
+    _check(lib().moe_block_norms(yp, rp, post, pre, gp, stride, T, d, scale, eps, op, np_, _raw_stream(stream)),
+           "moe_block_norms")
     return (residual if y is None else out), normed
 
 
@@ -715,11 +756,9 @@ class BlockNormsGrads(NamedTuple):
     dgate: Optional[torch.Tensor]
 
 
+@functools.lru_cache(maxsize=1024)
 def block_norms_backward_workspace_size(num_tokens: int, d_model: int) -> int:
-    n = ctypes.c_size_t(0)
-    _check(lib().moe_block_norms_backward_workspace_size(num_tokens, d_model, ctypes.byref(n)),
-           "moe_block_norms_backward_workspace_size")
-    return int(n.value)
+    return _host_size("moe_block_norms_backward_workspace_size", num_tokens, d_model)
 
 
 def block_norms_backward(dout: Optional[torch.Tensor], dnormed: Optional[torch.Tensor], y: Optional[torch.Tensor],
@@ -738,36 +777,34 @@ def block_norms_backward(dout: Optional[torch.Tensor], dnormed: Optional[torch.T
         raise ValueError("without y there is the norm before the next block alone: pre_weight, and no post_weight or gate")
     if (pre_weight is None) != (out is None) or (pre_weight is None and dnormed is not None):
         raise ValueError("out and dnormed belong to pre_weight")
-    _bf16_shaped(dout=(dout, (T, d)), dnormed=(dnormed, (T, d)), y=(y, (T, d)), out=(out, (T, d)),
-                 pre_weight=(pre_weight, (d,)), post_weight=(post_weight, (d,)))
+    for name, t, shape in (("dout", dout, (T, d)), ("dnormed", dnormed, (T, d)), ("y", y, (T, d)), ("out", out, (T, d)),
+                           ("pre_weight", pre_weight, (d,)), ("post_weight", post_weight, (d,))):
+        _shaped(name, t, shape)
     stride = _gate_stride(gate, T, d)
-    shapes = dict(dresidual=(T, d), dy=None if y is None else (T, d), dpost_weight=None if post_weight is None else (d,),
-                  dpre_weight=None if pre_weight is None else (d,),
-                  dgate=None if gate is None else (T, d) if stride else (d,))
-    given = BlockNormsGrads(None, None, None, None, None) if grads is None else grads
-    for name, t in given._asdict().items():
-        if t is None:
-            continue
-        types = _BF16 if shapes[name] == (T, d) and (name != "dgate" or stride) and not name.endswith("weight") \
-            else (torch.float32,)
-        if shapes[name] is None or tuple(t.shape) != shapes[name] or t.dtype not in types:
-            raise ValueError(f"{name} must be a {types[0]} tensor of shape {shapes[name]}")
-    _same_device(first, dout, dnormed, y, out, pre_weight, post_weight, gate, workspace, *given)
-    with _on(stream):
-        made = {}
-        for n, t in given._asdict().items():
-            if t is None and shapes[n] is not None:
-                f32 = n.endswith("weight") or (n == "dgate" and not stride)
-                t = torch.empty(shapes[n], dtype=torch.float32 if f32 else first.dtype, device=first.device)
-            made[n] = t
+    dr, dy, dpost, dpre, dgate = (None,) * 5 if grads is None else grads
+    if ((dy is not None and y is None) or (dpost is not None and post_weight is None)
+            or (dpre is not None and pre_weight is None) or (dgate is not None and gate is None)):
+        raise ValueError("grads holds the gradient of an input that is not given")
+    for name, t, shape, types in (("dresidual", dr, (T, d), _BF16), ("dy", dy, (T, d), _BF16), ("dpost_weight", dpost, (d,), _F32),
+                                  ("dpre_weight", dpre, (d,), _F32),
+                                  ("dgate", dgate, (T, d) if stride else (d,), _BF16 if stride else _F32)):
+        _shaped(name, t, shape, types)
+    with _at(stream):
+        if dr is None:
+            dr = torch.empty_like(first)
+        if dy is None and y is not None:
+            dy = torch.empty_like(first)
+        if dgate is None and stride:
+            dgate = torch.empty_like(first)
+        f32 = [torch.empty(d, dtype=torch.float32, device=first.device) if t is None and w is not None else t
+               for t, w in ((dpost, post_weight), (dpre, pre_weight), (dgate, None if stride else gate))]
+        dpost, dpre, dgate = f32
         if workspace is None:
             workspace = torch.empty(block_norms_backward_workspace_size(T, d), dtype=torch.uint8, device=first.device)
-    got = BlockNormsGrads(**made)
-    _check(lib().moe_block_norms_backward(_p(dout), _p(dnormed), _p(y), _p(out), _p(post_weight), _p(pre_weight), _p(gate),
-                                          stride, T, d, scale, eps, *map(_p, got), _p(workspace),
-                                          workspace.numel() * workspace.element_size(), _stream(stream)),
+    p = _pointers(dout, dnormed, y, out, post_weight, pre_weight, gate, dr, dy, dpost, dpre, dgate, workspace)
+    _check(lib().moe_block_norms_backward(*p[:7], stride, T, d, scale, eps, *p[7:], _bytes(workspace), _raw_stream(stream)),
            "moe_block_norms_backward")
-    return got
+    return BlockNormsGrads(dr, dy, dpost, dpre, dgate)
 
 
 def quantize_int8(x: torch.Tensor, *, q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
@@ -775,26 +812,22 @@ def quantize_int8(x: torch.Tensor, *, q: Optional[torch.Tensor] = None, scale: O
     """8-bit codes and a scale of each row of bf16 x [rows, n] (moe_quantize_int8): (q int8 [rows, n], scale fp32
     [rows]), x about scale * q.  For tokens, and for the weights [n_out, n_in] of linear_int8."""
     rows, n = x.shape
-    _bf16_shaped(x=(x, (rows, n)))
-    if q is not None and (tuple(q.shape) != (rows, n) or q.dtype != torch.int8):
-        raise ValueError(f"q must be an int8 tensor of shape {(rows, n)}")
-    if scale is not None and (tuple(scale.shape) != (rows,) or scale.dtype != torch.float32):
-        raise ValueError(f"scale must be an fp32 tensor of shape {(rows,)}")
-    _same_device(x, q, scale)
-    with _on(stream):
+    _shaped("x", x, (rows, n))
+    _shaped("q", q, (rows, n), _I8)
+    _shaped("scale", scale, (rows,), _F32)
+    with _at(stream):
         if q is None:
-            q = torch.empty((rows, n), dtype=torch.int8, device=x.device)
+            q = torch.empty_like(x, dtype=torch.int8)
         if scale is None:
-            scale = torch.empty((rows,), dtype=torch.float32, device=x.device)
-    _check(lib().moe_quantize_int8(_p(x), rows, n, _p(q), _p(scale), _stream(stream)), "moe_quantize_int8")
+            scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+    xp, qp, sp = _pointers(x, q, scale)
+    _check(lib().moe_quantize_int8(xp, rows, n, qp, sp, _raw_stream(stream)), "moe_quantize_int8")
     return q, scale
 
 
+@functools.lru_cache(maxsize=1024)
 def linear_int8_workspace_size(num_tokens: int, n_in: int, n_out: int, quantize: bool = True) -> int:
-    n = ctypes.c_size_t(0)
-    _check(lib().moe_linear_int8_workspace_size(num_tokens, n_in, n_out, int(quantize), ctypes.byref(n)),
-           "moe_linear_int8_workspace_size")
-    return int(n.value)
+    return _host_size("moe_linear_int8_workspace_size", num_tokens, n_in, n_out, int(quantize))
 
 
 def linear_int8(inp: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor, *, x_scale: Optional[torch.Tensor] = None,
@@ -803,24 +836,20 @@ def linear_int8(inp: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor, *, x_
     [T, n_in], quantised token by token on the way in, or int8 with the tokens' x_scale fp32 [T].  out bf16 [T, n_out]."""
     T, n_in = inp.shape
     n_out = W.shape[0]
-    if tuple(W.shape) != (n_out, n_in) or W.dtype != torch.int8:
-        raise ValueError(f"W must be an int8 tensor of shape [n_out, {n_in}]")
-    if x_scale is None:
-        _bf16_shaped(inp=(inp, (T, n_in)))
-    elif inp.dtype != torch.int8 or tuple(x_scale.shape) != (T,) or x_scale.dtype != torch.float32:
-        raise ValueError(f"with x_scale, an fp32 tensor of shape {(T,)}, inp holds int8 codes")
-    if tuple(w_scale.shape) != (n_out,) or w_scale.dtype != torch.float32:
-        raise ValueError(f"w_scale must be an fp32 tensor of shape {(n_out,)}")
-    _bf16_shaped(out=(out, (T, n_out)))
-    _same_device(inp, W, w_scale, x_scale, out, workspace)
-    with _on(stream):
+    _shaped("W", W, (n_out, n_in), _I8)
+    _shaped("inp", inp, (T, n_in), _BF16 if x_scale is None else _I8)
+    _shaped("x_scale", x_scale, (T,), _F32)
+    _shaped("w_scale", w_scale, (n_out,), _F32)
+    _shaped("out", out, (T, n_out))
+    with _at(stream):
         if out is None:
             out = torch.empty((T, n_out), dtype=inp.dtype if x_scale is None else torch.bfloat16, device=inp.device)
         if workspace is None:
             workspace = torch.empty(linear_int8_workspace_size(T, n_in, n_out, x_scale is None), dtype=torch.uint8,
                                     device=inp.device)
-    _check(lib().moe_linear_int8(_p(inp), _p(x_scale), _p(W), _p(w_scale), T, n_in, n_out, _p(out), _p(workspace),
-                                 workspace.numel() * workspace.element_size(), _stream(stream)), "moe_linear_int8")
+    xp, xs, wp, ws, op, work = _pointers(inp, x_scale, W, w_scale, out, workspace)
+    _check(lib().moe_linear_int8(xp, xs, wp, ws, T, n_in, n_out, op, work, _bytes(workspace), _raw_stream(stream)),
+           "moe_linear_int8")
     return out
 
 
