@@ -20,42 +20,20 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
-// N consecutive values at p, 16 (or 8) bytes a store; those from `left` on are not there
-template <int N>
-__device__ __forceinline__ void store_bf16(uint16_t* p, int left, const float (&v)[N]) {
-  if constexpr (N == 4) {
-    if (left > 0) *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-  } else {
+__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+}
+__device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
+  const uint32_t d[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int c = 0; c < N; c += 8)
-      if (c < left)
-        *reinterpret_cast<uint4*>(p + c) = make_uint4(pack_bf16(v[c], v[c + 1]), pack_bf16(v[c + 2], v[c + 3]),
-                                                      pack_bf16(v[c + 4], v[c + 5]), pack_bf16(v[c + 6], v[c + 7]));
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16lo(d[i]);
+    v[2 * i + 1] = bf16hi(d[i]);
   }
 }
-template <int N>
-__device__ __forceinline__ void load_bf16(const uint16_t* p, int left, float (&v)[N]) {
-  static_assert(N % 8 == 0, "pieces of 16 bytes");
-#pragma unroll
-  for (int c = 0; c < N; c += 8) {
-    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    if (c < left) w = *reinterpret_cast<const uint4*>(p + c);
-    const uint32_t d[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[c + 2 * i] = bf16lo(d[i]);
-      v[c + 2 * i + 1] = bf16hi(d[i]);
-    }
-  }
-}
-// results 4 J0 .. of a lane's row, in order
-template <int J0, int J1, class Acc, int NJ>
-__device__ __forceinline__ void lane_values(const Acc (&acc)[NJ], float (&v)[4 * (J1 - J0)]) {
-#pragma unroll
-  for (int j = J0; j < J1; ++j)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) v[4 * (j - J0) + r] = acc[j][r];
-}
+
+// The epilogues' results come in whole pieces of eight: every width is a multiple of 8.
+struct NoHeld {};
 
 // rows of bf16, the first `cut` of them at out[0], the others at out[1]; or, of split sums, fp32
 // pieces [split][M][N]
@@ -64,19 +42,16 @@ struct EpiRows {
   int32_t cut;
   float* part;
   int32_t M, N;
-  template <class C>
-  __device__ __forceinline__ void row(int m, int n, int rows, int split, const tg_f32x4 (&acc)[C::NJ]) const {
+  using Held = NoHeld;
+  __device__ __forceinline__ Held hold(int, int, int) const { return {}; }
+  __device__ __forceinline__ void put(int m, int n, int, int split, const Held&, const float (&v)[8]) const {
     if (part) {
       float* p = part + ((int64_t)split * M + m) * N + n;
-#pragma unroll
-      for (int j = 0; j < C::NJ; ++j)
-        if (n + 4 * j < rows) *reinterpret_cast<tg_f32x4*>(p + 4 * j) = acc[j];
-      return;
+      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      store8((m < cut ? out[0] + (int64_t)m * N : out[1] + (int64_t)(m - cut) * N) + n, v);
     }
-    float v[4 * C::NJ];
-    lane_values<0, C::NJ>(acc, v);
-    uint16_t* o = m < cut ? out[0] + (int64_t)m * N : out[1] + (int64_t)(m - cut) * N;
-    store_bf16(o + n, rows - n, v);
   }
 };
 
@@ -84,20 +59,18 @@ struct EpiRows {
 struct EpiGlu {
   uint16_t *a, *gate, *up;
   int32_t F;
-  template <class C>
-  __device__ __forceinline__ void row(int m, int n, int rows, int, const tg_f32x4 (&acc)[C::NJ]) const {
-    constexpr int N = 4 * C::J;
-    float gv[N], uv[N], av[N];
-    lane_values<0, C::J>(acc, gv);
-    lane_values<C::J, 2 * C::J>(acc, uv);
+  using Held = NoHeld;
+  __device__ __forceinline__ Held hold(int, int, int) const { return {}; }
+  __device__ __forceinline__ void put(int m, int n, int, int, const Held&, const float (&g)[8], const float (&u)[8]) const {
     const int64_t at = (int64_t)m * F + n;
     if (gate) {
-      store_bf16(gate + at, rows - n, gv);
-      store_bf16(up + at, rows - n, uv);
+      store8(gate + at, g);
+      store8(up + at, u);
     }
+    float v[8];
 #pragma unroll
-    for (int i = 0; i < N; ++i) av[i] = silu_f32(gv[i]) * uv[i];
-    store_bf16(a + at, rows - n, av);
+    for (int i = 0; i < 8; ++i) v[i] = silu_f32(g[i]) * u[i];
+    store8(a + at, v);
   }
 };
 
@@ -106,25 +79,28 @@ struct EpiGluBack {
   const uint16_t *gate, *up;
   uint16_t *a, *dgu;
   int32_t F;
-  template <class C>
-  __device__ __forceinline__ void row(int m, int n, int rows, int, const tg_f32x4 (&acc)[C::NJ]) const {
-    constexpr int N = 4 * C::NJ;
+  struct Held {
+    uint4 g, u;
+  };
+  __device__ __forceinline__ Held hold(int m, int n, int) const {
     const int64_t at = (int64_t)m * F + n;
-    float gv[N], uv[N], av[N], dg[N], du[N];
-    load_bf16(gate + at, rows - n, gv);
-    load_bf16(up + at, rows - n, uv);
+    return {*reinterpret_cast<const uint4*>(gate + at), *reinterpret_cast<const uint4*>(up + at)};
+  }
+  __device__ __forceinline__ void put(int m, int n, int, int, const Held& h, const float (&d)[8]) const {
+    float g[8], u[8], av[8], dg[8], du[8];
+    unpack8(h.g, g);
+    unpack8(h.u, u);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float d = acc[i / 4][i % 4], g = gv[i], s = 1.f / (1.f + __expf(-g));
-      const float gs = g * s;
-      av[i] = gs * uv[i];
-      du[i] = d * gs;
-      dg[i] = d * uv[i] * (s + gs * (1.f - s));
+    for (int i = 0; i < 8; ++i) {
+      const float s = 1.f / (1.f + __expf(-g[i])), gs = g[i] * s;
+      av[i] = gs * u[i];
+      du[i] = d[i] * gs;
+      dg[i] = d[i] * u[i] * (s + gs * (1.f - s));
     }
-    store_bf16(a + at, rows - n, av);
+    store8(a + (int64_t)m * F + n, av);
     uint16_t* o = dgu + (int64_t)m * 2 * F + n;
-    store_bf16(o, rows - n, dg);
-    store_bf16(o + F, rows - n, du);
+    store8(o, dg);
+    store8(o + F, du);
   }
 };
 
@@ -141,7 +117,7 @@ __global__ void __launch_bounds__(256) join_splits_kernel(const float* __restric
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] += w[j];
   }
-  store_bf16(out + 8 * i, 8, v);
+  store8(out + 8 * i, v);
 }
 
 // which tiles a product takes

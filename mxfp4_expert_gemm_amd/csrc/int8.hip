@@ -15,31 +15,32 @@ struct EpiInt8 {
   uint16_t* out;
   int32_t* part;  // split sums: [split][M][N]
   int32_t M, N;
-  template <class C>
-  __device__ __forceinline__ void row(int m, int n, int rows, int split, const tg_i32x4 (&acc)[C::NJ]) const {
+  struct Held {};
+  __device__ __forceinline__ Held hold(int, int, int) const { return {}; }
+  __device__ __forceinline__ void put(int m, int n, int left, int split, const Held&, const int32_t (&v)[8]) const {
     if (part) {
       int32_t* p = part + ((int64_t)split * M + m) * N + n;
 #pragma unroll
-      for (int j = 0; j < C::NJ; ++j)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (n + 4 * j + r < rows) p[4 * j + r] = acc[j][r];
+      for (int r = 0; r < 8; ++r)
+        if (r < left) p[r] = v[r];
       return;
     }
     const float s = xs[m];
     uint16_t* o = out + (int64_t)m * N + n;
+    if (left >= 8 && N % 8 == 0) {
+      const float4 a = *reinterpret_cast<const float4*>(ws + n), b = *reinterpret_cast<const float4*>(ws + n + 4);
+      const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      uint32_t d[4];
 #pragma unroll
-    for (int j = 0; j < C::NJ; ++j) {
-      if (n + 4 * j + 4 <= rows && N % 4 == 0) {
-        const float4 w = *reinterpret_cast<const float4*>(ws + n + 4 * j);
-        const bf16x2_t a = {(__bf16)((float)acc[j][0] * s * w.x), (__bf16)((float)acc[j][1] * s * w.y)};
-        const bf16x2_t b = {(__bf16)((float)acc[j][2] * s * w.z), (__bf16)((float)acc[j][3] * s * w.w)};
-        *reinterpret_cast<uint2*>(o + 4 * j) = make_uint2(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b));
-      } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (n + 4 * j + r < rows) o[4 * j + r] = f32_to_bf16((float)acc[j][r] * s * ws[n + 4 * j + r]);
+      for (int r = 0; r < 4; ++r) {
+        const bf16x2_t c = {(__bf16)((float)v[2 * r] * s * w[2 * r]), (__bf16)((float)v[2 * r + 1] * s * w[2 * r + 1])};
+        d[r] = __builtin_bit_cast(uint32_t, c);
       }
+      *reinterpret_cast<uint4*>(o) = make_uint4(d[0], d[1], d[2], d[3]);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < left) o[r] = f32_to_bf16((float)v[r] * s * ws[n + r]);
     }
   }
 };

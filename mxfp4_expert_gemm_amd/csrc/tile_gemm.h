@@ -1,6 +1,6 @@
 // Tiles of a matrix product on the matrix cores, for the dense block (ffn.hip) and the 8-bit
 // projection (int8.hip):
-//   C[m][n] = sum_k M(m, k) N(n, k),   the results handed to an epilogue.
+//   C[m][n] = sum_k M(m, k) N(n, k),   the results handed to an epilogue, eight n at a time.
 //
 // Either operand is K-major (rows of consecutive k, as activations and weights lie in a forward
 // product) or row-major in the other index (k is the slow one), which a backward pass needs for
@@ -14,21 +14,24 @@
 // its first step, into the slot that N of tile t - 1 left, and N during its second, into the slot of
 // M of tile t, one barrier for a tile.  R is odd, so the ring holds one operand more than whole
 // tiles: five slots of 32 KB are all of the LDS.  The operands of the next step are read into
-// registers while the current step's products run.  What bounds it at large sizes is the LDS: a
-// wave of 128 x 128 reads (128 + 128) x 64 bytes for 64 products of 16 cycles, four waves half of
-// the LDS's 128 bytes a cycle, the loads into LDS a quarter.
+// registers while the current step's products run.
+//
+// A block goes on from tile to tile of its share, the first K tiles of the next one loading under
+// the epilogue of the last.  Each XCD (blocks b with the same b mod 8) has a contiguous range of an
+// order that goes through groups of 8 tiles in m, so that what is resident shares operands.
 //
 // The operand that the matrix instruction calls A (its rows go to a lane's four result registers)
-// is N, so that a lane holds consecutive n; and the n of a wave are dealt to instructions so that
-// a lane's NJ x 4 results are consecutive: row rho of instruction j is
-// n = 4 NJ (rho / 4) + 4 j + rho % 4.  GLU: the tile's first half are rows of one matrix, its
-// second the same rows of another; a lane holds both for the same f.
+// is N: lane l holds n = 4 (l / 16) + 0..3 of m = l % 16.  GLU: N has the rows of two matrices; an
+// instruction's first eight are rows f .. f + 7 of the first and its other eight the same of the
+// second.
 //
-// LDS layouts, in pieces of 16 bytes, free of bank conflicts for the reads below:
-//  K-major: a row is 8 pieces, piece c stored at c ^ key(row), key = the row's bits 0, 1 and SB, the
-//    bit in which the rows read together by lanes 0-3 and 4-7 differ.
-//  row-major: a k is R/8 pieces, piece p stored at p ^ f(k), read by the transposing LDS read: 16
-//    lanes hand in 4 k x 16 rows, and lane i receives row i's four k.
+// LDS layouts, in pieces of 16 bytes, free of bank conflicts for the reads:
+//  K-major: a row is 8 pieces, piece c stored at c ^ (row % 8);
+//  row-major: a k is RP/8 pieces, piece p stored at p ^ 2 (k % 4), read by the transposing LDS
+//    read: 16 lanes hand in 4 k x 16 rows, and lane i receives row i's four k.
+// What bounds it at large sizes: a wave of 128 x 128 reads (128 + 128) x 64 bytes from LDS for 64
+// products of 16 cycles, four waves half of the LDS's 128 bytes a cycle, the loads into LDS a
+// quarter; the products themselves run at what the card's power allows.
 #pragma once
 
 #include "common.h"
@@ -43,18 +46,19 @@ typedef short tg_s16x4 __attribute__((ext_vector_type(4)));
 enum TileOrder { TILE_KMAJ = 0, TILE_RMAJ = 1 };
 
 struct TileOperand {
-  const void* p[2];  // second: the other K segment, or the rows of a tile's second half (GLU)
+  const void* p[2];  // second: the other K segment, or the second matrix (GLU)
   int64_t ld;        // bytes from a row (K-major) or a k (row-major) to the next
   int32_t rows;
 };
 struct TileArgs {
   TileOperand m, n;
-  int64_t K;       // values of one K segment; K-major: a multiple of 16 bytes of them
-  int32_t nk;      // K tiles of a segment
-  int32_t nkt;     // K tiles in all (nk, or 2 nk)
-  int32_t splits;  // the K tiles are dealt to so many blocks, each with an output of its own
+  int64_t K;       // values of one K segment; K-major: whole pieces of 16 bytes
+  int32_t splits;  // the K tiles are dealt to so many blocks, each with results of its own
+  // set by the launcher
+  int32_t nk;        // K tiles of a segment
+  int32_t nkt;       // K tiles in all (nk, or 2 nk)
   int32_t ntm, ntn;
-  int32_t nblocks;  // ntm * ntn * splits
+  int32_t nblocks;   // ntm * ntn * splits
 };
 
 // what a lane reads where a tile's k lie past K
@@ -75,57 +79,47 @@ __device__ __forceinline__ void tile_wait_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(VM) : "memory");
 }
 
-// One operand's tile of R rows.  SB, J: see above; SPLIT: the second half of the rows comes from p[1].
-template <int ORDER, int R, int NW, int SB, int J, bool SPLIT>
+// One operand's tile of ROWS rows.  SPLIT: its second half are rows of p[1].
+template <int ORDER, int ROWS, int NW, bool SPLIT>
 struct TileLoader {
-  static constexpr int BYTES = R * 128;
+  // a row-major tile is as wide as the next power of two: what it permutes stays inside
+  static constexpr int RP = ORDER == TILE_KMAJ ? ROWS : ROWS <= 64 ? 64 : ROWS <= 128 ? 128 : 256;
+  static constexpr int BYTES = RP * 128;
   static constexpr int NU = BYTES / (1024 * NW);  // loads of a wave for one tile
   static_assert(NU * 1024 * NW == BYTES, "whole loads");
-  static_assert(ORDER == TILE_KMAJ || R >= 128, "row-major tiles permute within 16 pieces");
+  static_assert(!SPLIT || ORDER == TILE_KMAJ, "two matrices by their rows");
   uint32_t off[NU];
   const uint8_t* base[2];
   int64_t step, K16;  // bytes (K-major) or k (row-major) of a segment
-  int nk;
 
-  static __device__ __forceinline__ int key(int row) { return (row & 3) | ((row >> SB) & 1) << 2; }
-  static __device__ __forceinline__ int fold(int k) {  // row-major: what a k's pieces are stored at
-    return J == 8 ? (k & 3) : J == 4 ? (k & 1) | ((k >> 1) & 1) << 3 : (k & 3) << 1;
-  }
-  __device__ __forceinline__ void init(const TileOperand& o, int r0, int64_t K, int nk_, int es, int wave, int lane) {
-    nk = nk_;
-    const int half = SPLIT ? R / 2 : R;
+  __device__ __forceinline__ void init(const TileOperand& o, int r0, int64_t K, int es, int wave, int lane) {
+    constexpr int HALF = SPLIT ? ROWS / 2 : ROWS;
     const int left = o.rows - r0;
 #pragma unroll
     for (int s = 0; s < 2; ++s)
       base[s] = static_cast<const uint8_t*>(o.p[s]) + (ORDER == TILE_KMAJ ? (int64_t)r0 * o.ld : (int64_t)r0 * 2);
-    if constexpr (ORDER == TILE_KMAJ) {
-      step = 128;
-      K16 = K * es;
-    } else {
-      step = 64 * o.ld;
-      K16 = K;
-    }
+    step = ORDER == TILE_KMAJ ? 128 : 64 * o.ld;
+    K16 = ORDER == TILE_KMAJ ? K * es : K;
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
       const int p = NW * u + wave;
-      if constexpr (ORDER == TILE_KMAJ) {
-        const int row = 8 * p + lane / 8, c = (lane % 8) ^ key(row);
-        const int in = row % half;
+      if constexpr (ORDER == TILE_KMAJ) {  // rows past the last one are read as that one, and not used
+        const int row = 8 * p + lane / 8, c = (lane % 8) ^ (row % 8), in = row % HALF;
         off[u] = (uint32_t)((in < left ? in : left - 1) * o.ld + 16 * c);
       } else {
-        const int k = p * (512 / R) + lane / (R / 8), pos = lane % (R / 8);
-        const int piece = pos ^ fold(k), last = (left - 1) / 8;
+        const int k = p * (512 / RP) + lane / (RP / 8), pos = lane % (RP / 8);
+        const int piece = pos ^ (2 * (k % 4)), last = (left - 1) / 8;
         off[u] = (uint32_t)(k * o.ld + 16 * (piece < last ? piece : last));
       }
     }
   }
-  __device__ __forceinline__ const uint8_t* at(int kt, int u, bool seg1) const {
-    if constexpr (SPLIT) return base[(u >= NU / 2) ? 1 : 0] + kt * step;
+  __device__ __forceinline__ const uint8_t* at(int kt, int p, bool seg1) const {
+    if constexpr (SPLIT) return base[p >= ROWS / 16 ? 1 : 0] + kt * step;  // 8 rows a load, half the rows
     return (seg1 ? base[1] : base[0]) + kt * step;
   }
   // load u of K tile kt (of its segment), all of whose k exist
   __device__ __forceinline__ void load(int kt, bool seg1, int u, uint32_t lds, int wave) const {
-    tile_dma(at(kt, u, seg1), off[u], lds + (NW * u + wave) * 1024);
+    tile_dma(at(kt, NW * u + wave, seg1), off[u], lds + (NW * u + wave) * 1024);
   }
   // all loads of a tile, some of whose k may lie past K: zeros
   __device__ __forceinline__ void load_tail(int kt, bool seg1, uint32_t lds, int wave, int lane) const {
@@ -133,13 +127,11 @@ struct TileLoader {
     for (int u = 0; u < NU; ++u) {
       const int p = NW * u + wave;
       bool in;
-      if constexpr (ORDER == TILE_KMAJ) {
-        const int row = 8 * p + lane / 8, c = (lane % 8) ^ key(row);
-        in = (int64_t)kt * 128 + 16 * c < K16;
-      } else {
-        in = (int64_t)kt * 64 + p * (512 / R) + lane / (R / 8) < K16;
-      }
-      const uint8_t* a = at(kt, u, seg1) + off[u];
+      if constexpr (ORDER == TILE_KMAJ)
+        in = (int64_t)kt * 128 + 16 * ((lane % 8) ^ (lane / 8)) < K16;  // row 8 p + lane / 8
+      else
+        in = (int64_t)kt * 64 + p * (512 / RP) + lane / (RP / 8) < K16;
+      const uint8_t* a = at(kt, p, seg1) + off[u];
       tile_dma(in ? a : reinterpret_cast<const uint8_t*>(tile_zero), lds + p * 1024);
     }
   }
@@ -151,19 +143,22 @@ struct TileCfg {
   static constexpr int MI = MI_, NJ = NJ_, WM = WM_, WN = WN_, R = R_, MORD = MORD_, NORD = NORD_;
   static constexpr bool GLU = GLU_, I8 = I8_;
   static constexpr int NW = WM * WN, BM = 16 * MI * WM, BN = 16 * NJ * WN;
+  static constexpr int OUT_N = GLU ? BN / 2 : BN;  // columns of the result
   static constexpr int ES = I8 ? 1 : 2, BK = 128 / ES;
-  static constexpr int J = GLU ? NJ / 2 : NJ;  // a lane's consecutive n: 4 J
-  static constexpr int SB = J == 8 ? 5 : J == 4 ? 4 : J == 2 ? 3 : 2;
-  static constexpr int SLOT = (BM > BN ? BM : BN) * 128, LDS = R * SLOT;
+  using ML = TileLoader<MORD, BM, NW, false>;
+  using NL = TileLoader<NORD, BN, NW, GLU>;
+  static constexpr int SLOT = ML::BYTES > NL::BYTES ? ML::BYTES : NL::BYTES, LDS = R * SLOT;
   // one wave a SIMD where the accumulators need it
   static constexpr int WAVES = MI * NJ > 32 ? 1 : 2;
+  static constexpr int BLOCKS = 256 * (LDS > 81920 ? 1 : 2);  // resident at once on 256 CUs
   static_assert(R % 2 == 1 && R >= 5, "two whole tiles (the first may be cut short) and one operand");
+  static_assert(NW * 16 * 16 * NJ * 4 <= SLOT, "the epilogue passes 16 rows a wave through one slot");
 };
 
 // acc += n m for one step.  Where the accumulators take half of the registers they are held in the
 // accumulation registers by hand: left to itself the compiler moves them back and forth (280 moves
 // for the 128 products of a K tile).  It does not know these instructions, so what it must not do
-// next to them is kept away: between two that share an accumulator lie 63 others, operands come
+// next to them is kept away: between two that share an accumulator lie 50 others, operands come
 // from LDS reads, which it waits for, and tile_settle stands before and after the loop.
 template <class C, class Acc>
 __device__ __forceinline__ void tile_mfma(Acc& acc, const u32x4_t& n, const u32x4_t& m) {
@@ -195,52 +190,61 @@ __device__ __forceinline__ void tile_settle(Acc (&acc)[C::MI][C::NJ]) {
   }
 }
 
+// The epilogue's type Epi has
+//   struct Held             what it reads from memory for eight results
+//   Held hold(m, n, left)   reads that, ahead of the results (left: columns from n on that exist)
+//   void put(m, n, left, split, held, v)            eight results, or with GLU
+//   void put(m, n, left, split, held, v, w)         eight of each matrix
 template <class C, class Epi>
 __global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArgs p, Epi epi) {
-  constexpr int MI = C::MI, NJ = C::NJ, R = C::R, H = (R - 1) / 2, NW = C::NW, BM = C::BM, BN = C::BN, J = C::J;
-  using ML = TileLoader<C::MORD, BM, NW, 2, 1, false>;
-  using NL = TileLoader<C::NORD, BN, NW, C::SB, J, C::GLU>;
+  constexpr int MI = C::MI, NJ = C::NJ, R = C::R, H = (R - 1) / 2, BM = C::BM, BN = C::BN;
+  using ML = typename C::ML;
+  using NL = typename C::NL;
   constexpr int MU = ML::NU, NU = NL::NU;
   using Acc = std::conditional_t<C::I8, tg_i32x4, tg_f32x4>;
+  using Value = std::conditional_t<C::I8, int32_t, float>;
   extern __shared__ __align__(16) uint8_t lds[];
-
-  const int nbp = gridDim.x;
-  const int lb = (blockIdx.x & 7) * (nbp >> 3) + (blockIdx.x >> 3);
-  if (lb >= p.nblocks) return;
-  constexpr int GROUP = 8;
-  const int per = p.ntm * p.ntn, split = lb / per, tile = lb - split * per;
-  const int span = GROUP * p.ntn, grp = tile / span, first = grp * GROUP;
-  const int gs = p.ntm - first < GROUP ? p.ntm - first : GROUP;
-  const int within = tile - grp * span;
-  const int m0 = (first + within % gs) * BM, n0 = (within / gs) * (C::GLU ? BN / 2 : BN);
-  const int k0 = (int)((int64_t)p.nkt * split / p.splits), k1 = (int)((int64_t)p.nkt * (split + 1) / p.splits);
-  const int nkt = k1 - k0;
 
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / WAVE));
   const int wm = wave / C::WN, wn = wave % C::WN, rho = lane & 15, g = lane >> 4;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
+  const int full = (int)(p.K / C::BK), part = full == p.nk ? 0 : p.nkt / p.nk;
+  // this block's share: every gridDim / 8-th tile of its XCD's range
+  const int range = (p.nblocks + 7) / 8, first = (int)(blockIdx.x & 7) * range + (int)(blockIdx.x >> 3);
+  const int end = min((int)(blockIdx.x & 7) * range + range, p.nblocks), stride = gridDim.x >> 3;
+
   ML ml;
   NL nl;
-  ml.init(p.m, m0, p.K, p.nk, C::ES, wave, lane);
-  nl.init(p.n, n0, p.K, p.nk, C::ES, wave, lane);
-  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
-  const int full = (int)(p.K / C::BK), part = (p.nkt - full * (p.nkt / p.nk)) != 0 ? p.nkt / p.nk : 0;
-
-  // Tile t of this block's K range.  Tiles that reach past K (one a segment) come first, so that
-  // only the loads ahead of the loop have to look for them.
+  int m0, n0, split, k0, nkt;
+  auto start = [&](int lb) {
+    constexpr int GROUP = 8;
+    const int per = p.ntm * p.ntn;
+    split = lb / per;
+    const int tile = lb - split * per;
+    const int span = GROUP * p.ntn, grp = tile / span, from = grp * GROUP;
+    const int gs = p.ntm - from < GROUP ? p.ntm - from : GROUP;
+    const int within = tile - grp * span;
+    m0 = (from + within % gs) * BM;
+    n0 = (within / gs) * C::OUT_N;
+    k0 = (int)((int64_t)p.nkt * split / p.splits);
+    nkt = (int)((int64_t)p.nkt * (split + 1) / p.splits) - k0;
+    ml.init(p.m, m0, p.K, C::ES, wave, lane);
+    nl.init(p.n, n0, p.K, C::ES, wave, lane);
+  };
+  // K tile t of the share's tile.  Tiles that reach past K (one a segment) come first, so that only
+  // the loads ahead of the loop have to look for them.
   auto place = [&](int t, bool& seg1) {
     int kt = k0 + t - part;
     seg1 = kt >= full;
     return seg1 ? kt - full : kt;
   };
-  auto first_m = [&](int t, uint32_t at) {
-    bool seg1 = k0 + t == 1;
-    const int kt = k0 + t < part ? full : place(t, seg1);
-    ml.load_tail(kt, seg1, at, wave, lane);
-  };
-  auto first_n = [&](int t, uint32_t at) {
-    bool seg1 = k0 + t == 1;
-    const int kt = k0 + t < part ? full : place(t, seg1);
-    nl.load_tail(kt, seg1, at, wave, lane);
+  auto load_first = [&]() {
+    for (int t = 0; t < (nkt < H ? nkt : H); ++t) {
+      bool seg1 = k0 + t == 1;
+      const int kt = k0 + t < part ? full : place(t, seg1);
+      ml.load_tail(kt, seg1, lds0 + 2 * t * C::SLOT, wave, lane);
+      nl.load_tail(kt, seg1, lds0 + (2 * t + 1) * C::SLOT, wave, lane);
+    }
   };
 
   // the operands of one step in registers
@@ -255,32 +259,25 @@ __global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArg
     r.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(at + 4 * row_bytes));
     return r.v;
   };
-  auto read_m = [&](const uint8_t* slot, int ks, int i) -> u32x4_t {
-    if constexpr (C::MORD == TILE_KMAJ) {
-      const int row = 16 * MI * wm + 16 * i + rho;
-      return *reinterpret_cast<const u32x4_t*>(slot + row * 128 + 16 * ((4 * ks + g) ^ ML::key(rho)));
-    } else {
+  auto read_tile = [&](const uint8_t* slot, auto orderc, auto widthc, int ks, int row, int col0) -> u32x4_t {
+    if constexpr (decltype(orderc)::value == TILE_KMAJ) {
+      return *reinterpret_cast<const u32x4_t*>(slot + row * 128 + 16 * ((4 * ks + g) ^ (rho & 7)));
+    } else {  // lane: k = 32 ks + 8 g + rho / 4 (and + 4), four rows from 4 (rho % 4)
+      constexpr int W = 2 * decltype(widthc)::value;
       const int k = 32 * ks + 8 * g + (rho >> 2), q = rho & 3;
-      const int piece = 2 * MI * wm + 2 * i + (q >> 1);
-      return tr_read(slot + k * (2 * BM) + 16 * (piece ^ ML::fold(rho >> 2)) + 8 * (q & 1), 2 * BM);
+      return tr_read(slot + k * W + 16 * ((col0 / 8 + (q >> 1)) ^ (2 * (rho >> 2))) + 8 * (q & 1), W);
     }
   };
-  auto read_n = [&](const uint8_t* slot, int ks, int j) -> u32x4_t {
-    const int h = C::GLU ? j / J : 0, jj = C::GLU ? j % J : j;
-    const int at = h * (BN / 2) + 16 * J * wn + 4 * jj;
-    if constexpr (C::NORD == TILE_KMAJ) {
-      const int row = at + 4 * J * (rho >> 2) + (rho & 3), key = (rho & 3) | ((rho >> 2) & 1) << 2;
-      return *reinterpret_cast<const u32x4_t*>(slot + row * 128 + 16 * ((4 * ks + g) ^ key));
-    } else {
-      const int k = 32 * ks + 8 * g + (rho >> 2), col = at + 4 * J * (rho & 3);
-      return tr_read(slot + k * (2 * BN) + 16 * ((col >> 3) ^ NL::fold(rho >> 2)) + 2 * (col & 7), 2 * BN);
-    }
+  auto read_m = [&](const uint8_t* slot, int ks, int i) {
+    const int at = 16 * MI * wm + 16 * i;
+    return read_tile(slot, std::integral_constant<int, C::MORD>{}, std::integral_constant<int, ML::RP>{}, ks, at + rho, at);
+  };
+  auto read_n = [&](const uint8_t* slot, int ks, int j) {
+    const int at = 16 * NJ * wn + 16 * j;
+    const int row = C::GLU ? (rho >> 3) * (BN / 2) + at / 2 + (rho & 7) : at + rho;
+    return read_tile(slot, std::integral_constant<int, C::NORD>{}, std::integral_constant<int, NL::RP>{}, ks, row, at);
   };
   Acc acc[MI][NJ];
-#pragma unroll
-  for (int i = 0; i < MI; ++i)
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) acc[i][j] = Acc{0, 0, 0, 0};
 
   // the products of step KS, while the next step's operands are read into the other registers and,
   // with FETCH, the step's operand of tile td (M in the first step, N in the second) is loaded to `to`
@@ -334,46 +331,111 @@ __global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArg
     return next;
   };
 
-  const int pre = nkt < H ? nkt : H;
-  for (int t = 0; t < pre; ++t) {
-    first_m(t, lds0 + 2 * t * C::SLOT);
-    first_n(t, lds0 + (2 * t + 1) * C::SLOT);
-  }
-  if (nkt >= H)
-    tile_wait_barrier<(H - 1) * (MU + NU)>();
-  else
-    tile_wait_barrier<0>();
+  // Sixteen rows of the wave's results at a time through its part of the last slot (which the first
+  // loads of the next tile leave alone), so that memory is met in runs of whole rows: row rho is
+  // 16 NJ words, four of them at a time stored at their place ^ rho % 8 (of an odd NJ, whose rows
+  // alternate between the halves of 128 bytes, ^ rho / 2 % 4).
+  auto epilogue = [&](int em, int en, int es) {
+    constexpr int PR = (C::GLU ? 8 : 16) * NJ / 8;        // pieces of eight results of a row (of one matrix)
+    constexpr int P = 16 * PR, PL = (P + 63) / 64;        // of 16 rows, and of a lane
+    uint8_t* mine = lds + (R - 1) * C::SLOT + wave * (16 * 64 * NJ);
+    const int wcols = (C::GLU ? 8 : 16) * NJ * wn;
+    auto where = [&](int s, int i, int& m, int& n) {
+      const int x = lane + 64 * s, row = x / PR, piece = x - row * PR;
+      m = em + 16 * MI * wm + 16 * i + row;
+      n = en + wcols + 8 * piece;
+      return x < P && m < p.m.rows && n < p.n.rows;
+    };
+    typename Epi::Held held[2][PL];
+    auto hold = [&](int i) {
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) fn[0][j] = read_n(lds + C::SLOT, 0, j);
+      for (int s = 0; s < PL; ++s) {
+        int m, n;
+        if (where(s, i, m, n)) held[i & 1][s] = epi.hold(m, n, p.n.rows - n);
+      }
+    };
+    hold(0);
 #pragma unroll
-  for (int i = 0; i < MI; ++i) fm[0][i] = read_m(lds, 0, i);
-  tile_settle<C>(acc);
-  int slot = 0, t = 0;
-  for (; t + H < nkt; ++t) slot = run_tile(std::true_type{}, t, slot);
-  for (; t < nkt; ++t) slot = run_tile(std::false_type{}, t, slot);  // nothing left to load
-  // the reads of the step past the end are still on their way
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-  tile_settle<C>(acc);
+    for (int i = 0; i < MI; ++i) {
+      if (i + 1 < MI) hold(i + 1);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const int word = C::GLU ? (g >> 1) * (8 * NJ) + 8 * j + 4 * (g & 1) : 16 * j + 4 * g;
+        *reinterpret_cast<Acc*>(mine + rho * (64 * NJ) + 16 * ((word / 4) ^ (NJ % 2 ? (rho >> 1) & 3 : rho & 7))) = acc[i][j];
+      }
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int s = 0; s < PL; ++s) {
+        int m, n;
+        const bool in = where(s, i, m, n);
+        const int x = lane + 64 * s, row = x / PR, piece = x - row * PR;
+        auto eight = [&](int word, Value (&v)[8]) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const Acc a = *reinterpret_cast<const Acc*>(mine + (row & 15) * (64 * NJ) +
+                                                        16 * ((word / 4 + h) ^ (NJ % 2 ? (row >> 1) & 3 : row & 7)));
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[4 * h + r] = a[r];
+          }
+        };
+        Value v[8], w[8];
+        eight(8 * piece, v);
+        if constexpr (C::GLU) eight(8 * NJ + 8 * piece, w);
+        if (in) {
+          if constexpr (C::GLU)
+            epi.put(m, n, p.n.rows - n, es, held[i & 1][s], v, w);
+          else
+            epi.put(m, n, p.n.rows - n, es, held[i & 1][s], v);
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+  };
 
-  // lane: results m = 16 i + rho, n = 4 J g .. 4 J g + 4 J - 1 (of each half)
+  if (first >= end) return;
+  start(first);
+  load_first();
+  for (int lb = first;;) {
 #pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    const int m = m0 + 16 * MI * wm + 16 * i + rho;
-    const int n = n0 + 16 * J * wn + 4 * J * g;
-    if (m < p.m.rows) epi.template row<C>(m, n, p.n.rows, split, acc[i]);
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[i][j] = Acc{0, 0, 0, 0};
+    if (lb == first && nkt >= H)
+      tile_wait_barrier<(H - 1) * (MU + NU)>();  // the first K tile has landed
+    else
+      tile_wait_barrier<0>();  // the stores of the last epilogue are among what is waited for
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) fn[0][j] = read_n(lds + C::SLOT, 0, j);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) fm[0][i] = read_m(lds, 0, i);
+    tile_settle<C>(acc);
+    int slot = 0, t = 0;
+    for (; t + H < nkt; ++t) slot = run_tile(std::true_type{}, t, slot);
+    for (; t < nkt; ++t) slot = run_tile(std::false_type{}, t, slot);  // nothing left to load
+    tile_settle<C>(acc);
+    tile_wait_barrier<0>();  // the reads past the last step are done everywhere: the LDS is free
+    const int em = m0, en = n0, es = split;
+    lb += stride;
+    const bool more = lb < end;
+    if (more) {
+      start(lb);
+      load_first();
+    }
+    epilogue(em, en, es);
+    if (!more) break;
   }
 }
 
 template <class C, class Epi>
 hipError_t launch_tile_gemm(TileArgs a, int segs, const Epi& epi, hipStream_t st) {
   a.ntm = (int32_t)ceil_div(a.m.rows, C::BM);
-  a.ntn = (int32_t)ceil_div(a.n.rows, C::GLU ? C::BN / 2 : C::BN);
+  a.ntn = (int32_t)ceil_div(a.n.rows, C::OUT_N);
   a.nk = (int32_t)ceil_div(a.K, C::BK);
   a.nkt = a.nk * segs;
   const int64_t nb = (int64_t)a.ntm * a.ntn * a.splits;
   if (a.splits < 1 || a.splits > a.nkt || nb > 0x7FFFFFF0) return hipErrorInvalidValue;
   a.nblocks = (int32_t)nb;
-  const unsigned grid = (unsigned)((nb + 7) / 8 * 8);
+  const unsigned grid = (unsigned)(nb < C::BLOCKS ? (nb + 7) / 8 * 8 : C::BLOCKS);
   if constexpr (C::LDS > 65536) {
     static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&tile_gemm_kernel<C, Epi>),
                                                     hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
