@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(256) join_splits_kernel(const float* __restric
 }
 
 // which tiles a product takes
-enum TileSize { TILE_32, TILE_64, TILE_128, TILE_256 };
+enum TileSize { TILE_32, TILE_64, TILE_128, TILE_224, TILE_256 };
 
 // The K tiles are split where the tiles of the output alone leave compute units idle: no more
 // pieces than bring the grid to one block a unit, of 16 steps of 32 at least.
@@ -131,13 +131,13 @@ int split_count(int64_t tiles, int64_t K) {
   return s < 1 ? 1 : s > 16 ? 16 : (int)s;
 }
 TileSize tile_size(int64_t M, int64_t N, bool row_major) {
-  if (ceil_div(M, 256) * ceil_div(N, 256) >= 192) return TILE_256;
+  if (ceil_div(M, 256) * ceil_div(N, 256) >= 192) return tiles_of_224(M, N) ? TILE_224 : TILE_256;
   if (M > 64 || row_major) return TILE_128;
   return M > 32 ? TILE_64 : TILE_32;
 }
 int64_t tile_count(TileSize z, int64_t M, int64_t N) {
   switch (z) {
-    case TILE_256: return ceil_div(M, 256) * ceil_div(N, 256);
+    case TILE_256: case TILE_224: return 256;  // not split
     case TILE_128: return ceil_div(M, 128) * ceil_div(N, 128);
     case TILE_64: return ceil_div(N, 32);
     default: return ceil_div(N, 32);
@@ -154,6 +154,7 @@ size_t part_bytes(int64_t M, int64_t N, int64_t K, bool row_major) {
 template <int MO, int NO>
 hipError_t product_tiles(TileSize z, const TileArgs& a, int segs, const EpiRows& e, hipStream_t st) {
   if (z == TILE_256) return launch_tile_gemm<TileCfg<8, 8, 2, 2, 5, MO, NO, false>>(a, segs, e, st);
+  if (z == TILE_224) return launch_tile_gemm<TileCfg<8, 7, 2, 2, 5, MO, NO, false>>(a, segs, e, st);
   if constexpr (MO == TILE_KMAJ && NO == TILE_KMAJ) {
     if (z == TILE_64) return launch_tile_gemm<TileCfg<2, 1, 2, 2, 13, MO, NO, false>>(a, segs, e, st);
     if (z == TILE_32) return launch_tile_gemm<TileCfg<1, 1, 2, 2, 13, MO, NO, false>>(a, segs, e, st);
@@ -214,6 +215,7 @@ hipError_t launch_ffn(const FfnArgs& p, void* ws, hipStream_t st) {
   hipError_t err;
   switch (tile_size(p.T, 2 * (int64_t)p.F, false)) {
     case TILE_256: err = launch_tile_gemm<TileCfg<8, 8, 2, 2, 5, TILE_KMAJ, TILE_KMAJ, true>>(t, 1, e, st); break;
+    case TILE_224: err = launch_tile_gemm<TileCfg<8, 7, 2, 2, 5, TILE_KMAJ, TILE_KMAJ, true>>(t, 1, e, st); break;
     case TILE_128: err = launch_tile_gemm<TileCfg<4, 4, 2, 2, 5, TILE_KMAJ, TILE_KMAJ, true>>(t, 1, e, st); break;
     case TILE_64: err = launch_tile_gemm<TileCfg<2, 2, 2, 2, 13, TILE_KMAJ, TILE_KMAJ, true>>(t, 1, e, st); break;
     default: err = launch_tile_gemm<TileCfg<1, 2, 2, 2, 13, TILE_KMAJ, TILE_KMAJ, true>>(t, 1, e, st); break;
@@ -237,10 +239,12 @@ hipError_t launch_ffn_backward(const FfnBackArgs& p, void* ws, hipStream_t st) {
   t.K = p.d;
   t.splits = 1;
   const EpiGluBack e{p.gate, p.up, a, dgu, p.F};
-  hipError_t err =
-      tile_size(T, p.F, true) == TILE_256
-          ? launch_tile_gemm<TileCfg<8, 8, 2, 2, 5, TILE_KMAJ, TILE_RMAJ, false>>(t, 1, e, st)
-          : launch_tile_gemm<TileCfg<4, 4, 2, 2, 5, TILE_KMAJ, TILE_RMAJ, false>>(t, 1, e, st);
+  hipError_t err;
+  switch (tile_size(T, p.F, true)) {
+    case TILE_256: err = launch_tile_gemm<TileCfg<8, 8, 2, 2, 5, TILE_KMAJ, TILE_RMAJ, false>>(t, 1, e, st); break;
+    case TILE_224: err = launch_tile_gemm<TileCfg<8, 7, 2, 2, 5, TILE_KMAJ, TILE_RMAJ, false>>(t, 1, e, st); break;
+    default: err = launch_tile_gemm<TileCfg<4, 4, 2, 2, 5, TILE_KMAJ, TILE_RMAJ, false>>(t, 1, e, st); break;
+  }
   if (err == hipSuccess && p.dx) {
     t.m = operand(dgu, 2 * (int64_t)p.F, T, dgu + p.F);
     t.n = operand(p.w_gate, p.d, p.d, p.w_up);

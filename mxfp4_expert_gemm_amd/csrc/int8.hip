@@ -122,14 +122,14 @@ __global__ void __launch_bounds__(256) quantize_int8_kernel(const uint16_t* __re
   for (int col = 8 * (threadIdx.x + 256 * C); col < n; col += 8 * 256) write(*reinterpret_cast<const uint4*>(row + col), col);
 }
 
-enum Int8Tile { I8_32, I8_64, I8_128, I8_256 };
+enum Int8Tile { I8_32, I8_64, I8_128, I8_224, I8_256 };
 Int8Tile int8_tile(int64_t M, int64_t N) {
-  if (ceil_div(M, 256) * ceil_div(N, 256) >= 192) return I8_256;
+  if (ceil_div(M, 256) * ceil_div(N, 256) >= 192) return tiles_of_224(M, N) ? I8_224 : I8_256;
   return M > 64 ? I8_128 : M > 32 ? I8_64 : I8_32;
 }
 int int8_splits(int64_t M, int64_t N, int64_t K) {
   const Int8Tile z = int8_tile(M, N);
-  const int64_t tiles = z == I8_256 ? 256 : z == I8_128 ? ceil_div(M, 128) * ceil_div(N, 128) : ceil_div(N, 32);
+  const int64_t tiles = z >= I8_224 ? 256 : z == I8_128 ? ceil_div(M, 128) * ceil_div(N, 128) : ceil_div(N, 32);
   const int64_t most = K / 1024, want = 256 / tiles, s = want < most ? want : most;
   return s < 1 ? 1 : s > 16 ? 16 : (int)s;
 }
@@ -162,6 +162,7 @@ hipError_t launch_linear_int8(const int8_t* q, const float* xs, const int8_t* W,
   hipError_t err;
   switch (int8_tile(T, n_out)) {
     case I8_256: err = launch_tile_gemm<TileCfg<8, 8, 2, 2, 5, TILE_KMAJ, TILE_KMAJ, false, true>>(a, 1, e, st); break;
+    case I8_224: err = launch_tile_gemm<TileCfg<8, 7, 2, 2, 5, TILE_KMAJ, TILE_KMAJ, false, true>>(a, 1, e, st); break;
     case I8_128: err = launch_tile_gemm<TileCfg<4, 4, 2, 2, 5, TILE_KMAJ, TILE_KMAJ, false, true>>(a, 1, e, st); break;
     case I8_64: err = launch_tile_gemm<TileCfg<2, 1, 2, 2, 13, TILE_KMAJ, TILE_KMAJ, false, true>>(a, 1, e, st); break;
     default: err = launch_tile_gemm<TileCfg<1, 1, 2, 2, 13, TILE_KMAJ, TILE_KMAJ, false, true>>(a, 1, e, st); break;
