@@ -67,8 +67,9 @@ static __device__ __align__(16) const uint32_t tile_zero[4] = {0u, 0u, 0u, 0u};
 // 16 bytes a lane from scalar base + lane offset, or from a lane's own address, to LDS at lds + 16
 // lane.  m0 is left changed: the compiler keeps nothing there on this target, it writes m0 right
 // before its own uses.
-__device__ __forceinline__ void tile_dma(const uint8_t* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory");
+__device__ __forceinline__ void tile_dma_to(uint32_t lds) { asm volatile("s_mov_b32 m0, %0" ::"s"(lds)); }
+__device__ __forceinline__ void tile_dma_go(const uint8_t* base, uint32_t off) {  // one instruction or more behind tile_dma_to
+  asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base) : "memory");
 }
 __device__ __forceinline__ void tile_dma(const uint8_t* at, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(at), "s"(lds) : "memory");
@@ -117,9 +118,10 @@ struct TileLoader {
     if constexpr (SPLIT) return base[p >= ROWS / 16 ? 1 : 0] + kt * step;  // 8 rows a load, half the rows
     return (seg1 ? base[1] : base[0]) + kt * step;
   }
-  // load u of K tile kt (of its segment), all of whose k exist
-  __device__ __forceinline__ void load(int kt, bool seg1, int u, uint32_t lds, int wave) const {
-    tile_dma(at(kt, NW * u + wave, seg1), off[u], lds + (NW * u + wave) * 1024);
+  // load u of K tile kt (of its segment), all of whose k exist: first where to, then the load
+  __device__ __forceinline__ void load_to(int u, uint32_t lds, int wave) const { tile_dma_to(lds + (NW * u + wave) * 1024); }
+  __device__ __forceinline__ void load_go(int kt, bool seg1, int u, int wave) const {
+    tile_dma_go(at(kt, NW * u + wave, seg1), off[u]);
   }
   // all loads of a tile, some of whose k may lie past K: zeros
   __device__ __forceinline__ void load_tail(int kt, bool seg1, uint32_t lds, int wave, int lane) const {
@@ -279,36 +281,53 @@ __global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArg
   };
   Acc acc[MI][NJ];
 
-  // the products of step KS, while the next step's operands are read into the other registers and,
-  // with FETCH, the step's operand of tile td (M in the first step, N in the second) is loaded to `to`
+  // The products of step KS, while the next step's operands are read into the other registers and,
+  // with FETCH, the step's operand of tile td (M in the first step, N in the second) is loaded to `to`.
+  // A product occupies the matrix cores for 16 cycles and its wave for 4, so what else there is to
+  // issue is dealt out one by one between the products; a few instructions in a row leave them idle
+  // (a read, its address and a load at every eighth product: 63% busy at 4096 tokens 7168 -> 3584).  The
+  // reads end before three quarters of the products: the barrier that follows waits for the last.
   auto step = [&](auto ksc, auto fetchc, const uint8_t* next_m, const uint8_t* next_n, int td, uint32_t to) {
     constexpr int KS = decltype(ksc)::value;
     constexpr bool FETCH = decltype(fetchc)::value;
-    constexpr int U = KS == 0 ? MU : NU;
-    unroll_n<MI>([&](auto qc) {
-      constexpr int Q = decltype(qc)::value;
+    constexpr int U = KS == 0 ? MU : NU, A = MI + NJ, S = MI * NJ;
+    bool seg1 = false;
+    const int kt = FETCH ? place(td, seg1) : 0;
+    unroll_n<S>([&](auto sc) {
+      constexpr int X = decltype(sc)::value, Q = X / NJ, JJ = X % NJ;
+      // loads u at products floor(u S / U); reads r at floor(3 r S / 4 A)
+      constexpr int U0 = (X * U + S - 1) / S, U1 = ((X + 1) * U + S - 1) / S;
+      if constexpr (FETCH && U1 > U0) {
+        if constexpr (KS == 0)
+          ml.load_to(U0, to, wave);
+        else
+          nl.load_to(U0, to, wave);
+      }
+      tile_mfma<C>(acc[Q][JJ], fn[KS][JJ], fm[KS][Q]);
       if constexpr (FETCH) {
-        bool seg1;
-        const int kt = place(td, seg1);
-        unroll_n<(Q + 1) * U / MI - Q * U / MI>([&](auto uc) {
-          constexpr int X = Q * U / MI + decltype(uc)::value;
+        unroll_n<U1 - U0>([&](auto uc) {
+          constexpr int V = U0 + decltype(uc)::value;
+          if constexpr (V > U0) {
+            if constexpr (KS == 0)
+              ml.load_to(V, to, wave);
+            else
+              nl.load_to(V, to, wave);
+            asm volatile("s_nop 0");
+          }
           if constexpr (KS == 0)
-            ml.load(kt, seg1, X, to, wave);
+            ml.load_go(kt, seg1, V, wave);
           else
-            nl.load(kt, seg1, X, to, wave);
+            nl.load_go(kt, seg1, V, wave);
         });
       }
-      constexpr int A = MI + NJ, R0 = Q * A / MI, R1 = (Q + 1) * A / MI;
-      unroll_n<R1 - R0>([&](auto rc) {
-        constexpr int X = R0 + decltype(rc)::value;
-        if constexpr (X < NJ)
-          fn[KS ^ 1][X] = read_n(next_n, KS ^ 1, X);
+      constexpr int R0 = (4 * A * X + 3 * S - 1) / (3 * S), R1 = (4 * A * (X + 1) + 3 * S - 1) / (3 * S);
+      constexpr int E0 = R0 < A ? R0 : A, E1 = X == S - 1 ? A : R1 < A ? R1 : A;
+      unroll_n<E1 - E0>([&](auto rc) {
+        constexpr int V = E0 + decltype(rc)::value;
+        if constexpr (V < NJ)
+          fn[KS ^ 1][V] = read_n(next_n, KS ^ 1, V);
         else
-          fm[KS ^ 1][X - NJ] = read_m(next_m, KS ^ 1, X - NJ);
-      });
-      unroll_n<NJ>([&](auto jc) {
-        constexpr int X = decltype(jc)::value;
-        tile_mfma<C>(acc[Q][X], fn[KS][X], fm[KS][Q]);
+          fm[KS ^ 1][V - NJ] = read_m(next_m, KS ^ 1, V - NJ);
       });
       __builtin_amdgcn_sched_barrier(0);
     });
