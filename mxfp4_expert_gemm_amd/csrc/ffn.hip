@@ -35,23 +35,18 @@ __device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
 // The epilogues' results come in whole pieces of eight: every width is a multiple of 8.
 struct NoHeld {};
 
-// rows of bf16, the first `cut` of them at out[0], the others at out[1]; or, of split sums, fp32
-// pieces [split][M][N]
+// rows of bf16: product 0's at out[0], from row `cut` on at out[1], product 1's at out[2]
 struct EpiRows {
-  uint16_t* out[2];
+  uint16_t* out[3];
   int32_t cut;
+  int32_t N[2];
   float* part;
-  int32_t M, N;
   using Held = NoHeld;
-  __device__ __forceinline__ Held hold(int, int, int) const { return {}; }
-  __device__ __forceinline__ void put(int m, int n, int, int split, const Held&, const float (&v)[8]) const {
-    if (part) {
-      float* p = part + ((int64_t)split * M + m) * N + n;
-      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-      *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-      store8((m < cut ? out[0] + (int64_t)m * N : out[1] + (int64_t)(m - cut) * N) + n, v);
-    }
+  static constexpr bool JOINS = true;
+  __device__ __forceinline__ Held hold(int, int) const { return {}; }
+  __device__ __forceinline__ void put(int which, int m, int n, int, const Held&, const float (&v)[8]) const {
+    uint16_t* o = which ? out[2] + (int64_t)m * N[1] : m < cut ? out[0] + (int64_t)m * N[0] : out[1] + (int64_t)(m - cut) * N[0];
+    store8(o + n, v);
   }
 };
 
@@ -60,8 +55,9 @@ struct EpiGlu {
   uint16_t *a, *gate, *up;
   int32_t F;
   using Held = NoHeld;
-  __device__ __forceinline__ Held hold(int, int, int) const { return {}; }
-  __device__ __forceinline__ void put(int m, int n, int, int, const Held&, const float (&g)[8], const float (&u)[8]) const {
+  static constexpr bool JOINS = false;
+  __device__ __forceinline__ Held hold(int, int) const { return {}; }
+  __device__ __forceinline__ void put(int, int m, int n, int, const Held&, const float (&g)[8], const float (&u)[8]) const {
     const int64_t at = (int64_t)m * F + n;
     if (gate) {
       store8(gate + at, g);
@@ -82,17 +78,19 @@ struct EpiGluBack {
   struct Held {
     uint4 g, u;
   };
-  __device__ __forceinline__ Held hold(int m, int n, int) const {
+  static constexpr bool JOINS = false;
+  __device__ __forceinline__ Held hold(int m, int n) const {
     const int64_t at = (int64_t)m * F + n;
     return {*reinterpret_cast<const uint4*>(gate + at), *reinterpret_cast<const uint4*>(up + at)};
   }
-  __device__ __forceinline__ void put(int m, int n, int, int, const Held& h, const float (&d)[8]) const {
+  __device__ __forceinline__ void put(int, int m, int n, int, const Held& h, const float (&d)[8]) const {
     float g[8], u[8], av[8], dg[8], du[8];
     unpack8(h.g, g);
     unpack8(h.u, u);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float s = 1.f / (1.f + __expf(-g[i])), gs = g[i] * s;
+      // the hardware's 2^x and reciprocal, a few ulps each (a division in full: 1.5 us a turn of tiles more)
+      const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896341f * g[i])), gs = g[i] * s;
       av[i] = gs * u[i];
       du[i] = d[i] * gs;
       dg[i] = d[i] * u[i] * (s + gs * (1.f - s));
@@ -104,91 +102,168 @@ struct EpiGluBack {
   }
 };
 
-// out = bf16(sum over the splits), eight values a thread, in the splits' order
-__global__ void __launch_bounds__(256) join_splits_kernel(const float* __restrict__ part, int64_t n8, int splits,
-                                                          uint16_t* __restrict__ out) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n8) return;
-  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < splits; ++s) {
-    const float* p = part + (int64_t)s * n8 * 8 + 8 * i;
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+// Up to eight tokens on the vector units: one wave a row of the weights (GLU: the same row of both
+// matrices), 16 bytes a lane and load, eight loads (of each) on their way, the block's tokens in LDS.
+// out[t][row] = sum_k w[row][k] in[t][k]; GLU: bf16(silu(g) u), and g and u where they are kept.
+// Bound: HBM.  A lane's sum is at most K / 128 pairs of products one after another, in fp32, then a
+// tree over the lanes.
+struct GemvArgs {
+  const uint16_t *w, *w1;  // [rows][K]
+  const uint16_t* in;      // [T][K]
+  uint16_t *out, *gate, *up;  // [T][rows]; the last two nullable
+  int32_t T, K, rows;
+};
+constexpr int GEMV_TOKENS = 8;
+template <int G, bool GLU>
+__global__ void __launch_bounds__(256) ffn_gemv_kernel(GemvArgs p) {
+  constexpr int U = 8, M = GLU ? 2 : 1;
+  extern __shared__ __align__(16) uint8_t lds[];
+  uint4* xs = reinterpret_cast<uint4*>(lds);  // [G][K / 8]
+  const int lane = lane_id(), wave = threadIdx.x / WAVE;
+  const int row = min((int)blockIdx.x * 4 + wave, p.rows - 1);
+  const bool mine = blockIdx.x * 4 + wave < p.rows;
+  const int pieces = p.K / 8;
+  const uint4* w[2];
+  w[0] = reinterpret_cast<const uint4*>(p.w + (int64_t)row * p.K);
+  w[1] = GLU ? reinterpret_cast<const uint4*>(p.w1 + (int64_t)row * p.K) : w[0];
+  uint4 held[M][U];
+  auto load = [&](int base) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += w[j];
+    for (int u = 0; u < U; ++u) {
+      const int at = base + 64 * u + lane;
+#pragma unroll
+      for (int m = 0; m < M; ++m) held[m][u] = at < pieces ? load_nt16(w[m] + at) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  load(0);
+#pragma unroll
+  for (int t = 0; t < G; ++t) {
+    const uint4* x = reinterpret_cast<const uint4*>(p.in + (int64_t)min(t, p.T - 1) * p.K);
+    for (int i = threadIdx.x; i < pieces; i += 256) xs[t * pieces + i] = x[i];
   }
-  store8(out + 8 * i, v);
+  lds_barrier();
+  float acc[M][G];
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int t = 0; t < G; ++t) acc[m][t] = 0.f;
+  for (int base = 0; base < pieces; base += 64 * U) {
+    uint4 cur[M][U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int m = 0; m < M; ++m) cur[m][u] = held[m][u];
+    if (base + 64 * U < pieces) load(base + 64 * U);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = base + 64 * u + lane;
+      if (base + 64 * u >= pieces) break;
+#pragma unroll
+      for (int t = 0; t < G; ++t) {
+        const uint4 x = xs[t * pieces + min(at, pieces - 1)];
+        const bool in = at < pieces;
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+          float s = acc[m][t];
+          s = dot2(x.x, cur[m][u].x, s);
+          s = dot2(x.y, cur[m][u].y, s);
+          s = dot2(x.z, cur[m][u].z, s);
+          s = dot2(x.w, cur[m][u].w, s);
+          acc[m][t] = in ? s : acc[m][t];
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < G; ++t) {
+    float v[M];
+#pragma unroll
+    for (int m = 0; m < M; ++m) v[m] = wave_sum_dpp(acc[m][t]);
+    if (lane == 0 && mine && t < p.T) {
+      const int64_t at = (int64_t)t * p.rows + row;
+      if constexpr (GLU) {
+        p.out[at] = glu_bf16(v[0], v[1]);
+        if (p.gate) {
+          p.gate[at] = f32_to_bf16(v[0]);
+          p.up[at] = f32_to_bf16(v[1]);
+        }
+      } else {
+        p.out[at] = f32_to_bf16(v[0]);
+      }
+    }
+  }
+}
+template <int G, bool GLU>
+hipError_t launch_gemv(const GemvArgs& a, hipStream_t st) {
+  const size_t lds = (size_t)G * a.K * 2;
+  if (lds > 65536) {
+    static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&ffn_gemv_kernel<G, GLU>),
+                                                    hipFuncAttributeMaxDynamicSharedMemorySize, 163840);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((ffn_gemv_kernel<G, GLU>), dim3((unsigned)ceil_div(a.rows, 4)), dim3(256), lds, st, a);
+  return hipGetLastError();
+}
+template <bool GLU>
+hipError_t gemv(const GemvArgs& a, hipStream_t st) {
+  if (a.T == 1) return launch_gemv<1, GLU>(a, st);
+  if (a.T == 2) return launch_gemv<2, GLU>(a, st);
+  return a.T <= 4 ? launch_gemv<4, GLU>(a, st) : launch_gemv<8, GLU>(a, st);
+}
+// the tokens' rows have to fit the LDS
+bool gemv_takes(int64_t T, int32_t K) {
+  return T <= GEMV_TOKENS && (int64_t)(T <= 2 ? T : T <= 4 ? 4 : 8) * K * 2 <= 163840;
 }
 
-// which tiles a product takes
-enum TileSize { TILE_32, TILE_64, TILE_128, TILE_224, TILE_256 };
-
-// The K tiles are split where the tiles of the output alone leave compute units idle: no more
-// pieces than bring the grid to one block a unit, of 16 steps of 32 at least.
-int split_count(int64_t tiles, int64_t K) {
-  const int64_t most = K / 512, want = 256 / tiles;
-  const int64_t s = want < most ? want : most;
-  return s < 1 ? 1 : s > 16 ? 16 : (int)s;
-}
+// Tiles by the rows of M: few tokens take 16, 32, 48 or 64 rows by 64 columns in blocks of two
+// waves, two blocks a unit, with a deep ring; then 128 x 128, two blocks a unit; and 256 x 256 (or
+// 224) where those fill three quarters of the units.
+enum TileSize { TILE_16, TILE_32, TILE_48, TILE_64, TILE_128, TILE_224, TILE_256 };
 TileSize tile_size(int64_t M, int64_t N, bool row_major) {
   if (ceil_div(M, 256) * ceil_div(N, 256) >= 192) return tiles_of_224(M, N) ? TILE_224 : TILE_256;
   if (M > 64 || row_major) return TILE_128;
-  return M > 32 ? TILE_64 : TILE_32;
+  return (TileSize)((M - 1) / 16);
 }
-int64_t tile_count(TileSize z, int64_t M, int64_t N) {
-  switch (z) {
-    case TILE_256: case TILE_224: return 256;  // not split
-    case TILE_128: return ceil_div(M, 128) * ceil_div(N, 128);
-    case TILE_64: return ceil_div(N, 32);
-    default: return ceil_div(N, 32);
-  }
-}
+// K is split where the tiles of the output alone leave units idle: no more pieces than bring the
+// grid to a block a unit, of 8 K tiles at least, 16 at most (33 tokens, 7168 -> 3584, 56 tiles:
+// 23 us whole, 12.1 in two, 10.1 in four, 10.6 in eight).
 int splits_of(int64_t M, int64_t N, int64_t K, bool row_major) {
-  return split_count(tile_count(tile_size(M, N, row_major), M, N), K);
+  const TileSize z = tile_size(M, N, row_major);
+  if (z >= TILE_224) return 1;
+  const int64_t tiles = z == TILE_128 ? ceil_div(M, 128) * ceil_div(N, 128) : ceil_div(N, 64);
+  const int64_t most = K / 512, want = 256 / tiles, s = want < most ? want : most;
+  return s < 1 ? 1 : s > 16 ? 16 : (int)s;
 }
 size_t part_bytes(int64_t M, int64_t N, int64_t K, bool row_major) {
   const int s = splits_of(M, N, K, row_major);
   return s > 1 ? (size_t)s * M * N * 4 : 0;
 }
-
-template <int MO, int NO>
-hipError_t product_tiles(TileSize z, const TileArgs& a, int segs, const EpiRows& e, hipStream_t st) {
-  if (z == TILE_256) return launch_tile_gemm<TileCfg<8, 8, 2, 2, 5, MO, NO, false>>(a, segs, e, st);
-  if (z == TILE_224) return launch_tile_gemm<TileCfg<8, 7, 2, 2, 5, MO, NO, false>>(a, segs, e, st);
+template <int MO, int NO, bool GLU, class Epi>
+hipError_t run_tiles(TileSize z, const TileArgs& a, int segs, const Epi& e, hipStream_t st, const TileArgs* b = nullptr) {
+  if (z == TILE_256) return launch_tile_gemm<TileCfg<8, 8, 2, 2, 5, MO, NO, GLU>>(a, segs, e, st, b);
+  if (z == TILE_224) return launch_tile_gemm<TileCfg<8, 7, 2, 2, 5, MO, NO, GLU>>(a, segs, e, st, b);
   if constexpr (MO == TILE_KMAJ && NO == TILE_KMAJ) {
-    if (z == TILE_64) return launch_tile_gemm<TileCfg<2, 1, 2, 2, 13, MO, NO, false>>(a, segs, e, st);
-    if (z == TILE_32) return launch_tile_gemm<TileCfg<1, 1, 2, 2, 13, MO, NO, false>>(a, segs, e, st);
+    switch (z) {
+      case TILE_16: return launch_tile_gemm<TileCfg<1, 2, 1, 2, 9, MO, NO, GLU>>(a, segs, e, st, b);
+      case TILE_32: return launch_tile_gemm<TileCfg<2, 2, 1, 2, 9, MO, NO, GLU>>(a, segs, e, st, b);
+      case TILE_48: return launch_tile_gemm<TileCfg<3, 2, 1, 2, 9, MO, NO, GLU>>(a, segs, e, st, b);
+      case TILE_64: return launch_tile_gemm<TileCfg<4, 2, 1, 2, 9, MO, NO, GLU>>(a, segs, e, st, b);
+      default: break;
+    }
   }
-  return launch_tile_gemm<TileCfg<4, 4, 2, 2, 5, MO, NO, false>>(a, segs, e, st);
-}
-
-// out [M][N] (its rows from `cut` on at out1) = sum over `segs` segments of K; part: room for splits
-template <int MO, int NO>
-hipError_t product(TileArgs a, int segs, uint16_t* out, uint16_t* out1, int32_t cut, float* part, hipStream_t st) {
-  const int64_t M = a.m.rows, N = a.n.rows;
-  const bool rmaj = MO == TILE_RMAJ || NO == TILE_RMAJ;
-  const TileSize z = tile_size(M, N, rmaj);
-  a.splits = out1 ? 1 : splits_of(M, N, a.K * segs, rmaj);
-  EpiRows e{{out, out1}, cut, a.splits > 1 ? part : nullptr, (int32_t)M, (int32_t)N};
-  const hipError_t err = product_tiles<MO, NO>(z, a, segs, e, st);
-  if (err != hipSuccess || a.splits == 1) return err;
-  const int64_t n8 = M * N / 8;
-  hipLaunchKernelGGL(join_splits_kernel, dim3((unsigned)ceil_div(n8, 256)), dim3(256), 0, st, part, n8, a.splits, out);
-  return hipGetLastError();
+  return launch_tile_gemm<TileCfg<4, 4, 2, 2, 5, MO, NO, GLU>>(a, segs, e, st, b);
 }
 
 TileOperand operand(const void* p, int64_t ld_values, int32_t rows, const void* p1 = nullptr) {
   return TileOperand{{p, p1 ? p1 : p}, ld_values * 2, rows};
 }
 
-size_t max2(size_t a, size_t b) { return a > b ? a : b; }
-
 }  // namespace
 
 FfnLayout ffn_layout(int64_t T, int32_t d, int32_t F) {
   FfnLayout l;
   l.a = 0;
-  l.part = align_up((size_t)T * F * 2, 256);
+  l.part = l.a + align_up((size_t)T * F * 2, 256);
   l.dgu = 0;
   l.total = l.part + align_up(part_bytes(T, d, F, false), 256);
   return l;
@@ -196,72 +271,73 @@ FfnLayout ffn_layout(int64_t T, int32_t d, int32_t F) {
 FfnLayout ffn_backward_layout(int64_t T, int32_t d, int32_t F) {
   FfnLayout l;
   l.a = 0;
-  l.dgu = align_up((size_t)T * F * 2, 256);
+  l.dgu = l.a + align_up((size_t)T * F * 2, 256);
   l.part = l.dgu + align_up((size_t)T * F * 4, 256);
-  l.total = l.part + align_up(max2(part_bytes(T, d, 2 * (int64_t)F, true), part_bytes(d, F, T, true)), 256);
+  l.total = l.part + align_up(part_bytes(T, d, 2 * (int64_t)F, true), 256);
   return l;
 }
 
 hipError_t launch_ffn(const FfnArgs& p, void* ws, hipStream_t st) {
   const FfnLayout l = ffn_layout(p.T, p.d, p.F);
-  uint16_t* a = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + l.a);
-  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + l.part);
-  TileArgs t{};
-  t.m = operand(p.x, p.d, (int32_t)p.T);
-  t.n = operand(p.w_gate, p.d, p.F, p.w_up);
-  t.K = p.d;
-  t.splits = 1;
-  const EpiGlu e{a, p.gate, p.up, p.F};
+  char* w = static_cast<char*>(ws);
+  uint16_t* a = reinterpret_cast<uint16_t*>(w + l.a);
+  const int32_t T = (int32_t)p.T;
   hipError_t err;
-  switch (tile_size(p.T, 2 * (int64_t)p.F, false)) {
-    case TILE_256: err = launch_tile_gemm<TileCfg<8, 8, 2, 2, 5, TILE_KMAJ, TILE_KMAJ, true>>(t, 1, e, st); break;
-    case TILE_224: err = launch_tile_gemm<TileCfg<8, 7, 2, 2, 5, TILE_KMAJ, TILE_KMAJ, true>>(t, 1, e, st); break;
-    case TILE_128: err = launch_tile_gemm<TileCfg<4, 4, 2, 2, 5, TILE_KMAJ, TILE_KMAJ, true>>(t, 1, e, st); break;
-    case TILE_64: err = launch_tile_gemm<TileCfg<2, 2, 2, 2, 13, TILE_KMAJ, TILE_KMAJ, true>>(t, 1, e, st); break;
-    default: err = launch_tile_gemm<TileCfg<1, 2, 2, 2, 13, TILE_KMAJ, TILE_KMAJ, true>>(t, 1, e, st); break;
+  TileArgs t{};
+  if (gemv_takes(T, p.d)) {
+    err = gemv<true>(GemvArgs{p.w_gate, p.w_up, p.x, a, p.gate, p.up, T, p.d, p.F}, st);
+  } else {
+    t.m = operand(p.x, p.d, T);
+    t.n = operand(p.w_gate, p.d, p.F, p.w_up);
+    t.K = p.d;
+    t.splits = 1;
+    err = run_tiles<TILE_KMAJ, TILE_KMAJ, true>(tile_size(T, 2 * (int64_t)p.F, false), t, 1, EpiGlu{a, p.gate, p.up, p.F}, st);
   }
   if (err != hipSuccess) return err;
-  t.m = operand(a, p.F, (int32_t)p.T);
+  if (gemv_takes(T, p.F)) return gemv<false>(GemvArgs{p.w_down, nullptr, a, p.out, nullptr, nullptr, T, p.F, p.d}, st);
+  t.m = operand(a, p.F, T);
   t.n = operand(p.w_down, p.F, p.d);
   t.K = p.F;
-  return product<TILE_KMAJ, TILE_KMAJ>(t, 1, p.out, nullptr, (int32_t)p.T, part, st);
+  t.splits = splits_of(T, p.d, p.F, false);
+  const EpiRows e{{p.out, nullptr, nullptr}, T, {p.d, 0}, reinterpret_cast<float*>(w + l.part)};
+  return run_tiles<TILE_KMAJ, TILE_KMAJ, false>(tile_size(T, p.d, false), t, 1, e, st);
 }
 
+// Three launches, and a join where dx's K is split: dA with a, dG and dU; dx, whose K is dG's and then dU's; and the weights' gradients,
+// two products of the same K in one launch.
 hipError_t launch_ffn_backward(const FfnBackArgs& p, void* ws, hipStream_t st) {
   const FfnLayout l = ffn_backward_layout(p.T, p.d, p.F);
-  uint16_t* a = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + l.a);
-  uint16_t* dgu = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + l.dgu);
-  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + l.part);
+  char* w = static_cast<char*>(ws);
+  uint16_t* a = reinterpret_cast<uint16_t*>(w + l.a);
+  uint16_t* dgu = reinterpret_cast<uint16_t*>(w + l.dgu);
   const int32_t T = (int32_t)p.T;
   TileArgs t{};
   t.m = operand(p.dout, p.d, T);
   t.n = operand(p.w_down, p.F, p.F);
   t.K = p.d;
   t.splits = 1;
-  const EpiGluBack e{p.gate, p.up, a, dgu, p.F};
-  hipError_t err;
-  switch (tile_size(T, p.F, true)) {
-    case TILE_256: err = launch_tile_gemm<TileCfg<8, 8, 2, 2, 5, TILE_KMAJ, TILE_RMAJ, false>>(t, 1, e, st); break;
-    case TILE_224: err = launch_tile_gemm<TileCfg<8, 7, 2, 2, 5, TILE_KMAJ, TILE_RMAJ, false>>(t, 1, e, st); break;
-    default: err = launch_tile_gemm<TileCfg<4, 4, 2, 2, 5, TILE_KMAJ, TILE_RMAJ, false>>(t, 1, e, st); break;
-  }
+  hipError_t err = run_tiles<TILE_KMAJ, TILE_RMAJ, false>(tile_size(T, p.F, true), t, 1,
+                                                          EpiGluBack{p.gate, p.up, a, dgu, p.F}, st);
   if (err == hipSuccess && p.dx) {
     t.m = operand(dgu, 2 * (int64_t)p.F, T, dgu + p.F);
     t.n = operand(p.w_gate, p.d, p.d, p.w_up);
     t.K = p.F;
-    err = product<TILE_KMAJ, TILE_RMAJ>(t, 2, p.dx, nullptr, T, part, st);
+    t.splits = splits_of(T, p.d, 2 * (int64_t)p.F, true);
+    const EpiRows e{{p.dx, nullptr, nullptr}, T, {p.d, 0}, reinterpret_cast<float*>(w + l.part)};
+    err = run_tiles<TILE_KMAJ, TILE_RMAJ, false>(tile_size(T, p.d, true), t, 2, e, st);
   }
   if (err == hipSuccess && p.dw_gate) {
+    TileArgs u{};
     t.m = operand(dgu, 2 * (int64_t)p.F, 2 * p.F);
     t.n = operand(p.x, p.d, p.d);
-    t.K = T;
-    err = product<TILE_RMAJ, TILE_RMAJ>(t, 1, p.dw_gate, p.dw_up, p.F, part, st);
-  }
-  if (err == hipSuccess && p.dw_down) {
-    t.m = operand(p.dout, p.d, p.d);
-    t.n = operand(a, p.F, p.F);
-    t.K = T;
-    err = product<TILE_RMAJ, TILE_RMAJ>(t, 1, p.dw_down, nullptr, p.d, part, st);
+    u.m = operand(p.dout, p.d, p.d);
+    u.n = operand(a, p.F, p.F);
+    t.K = u.K = T;
+    t.splits = u.splits = 1;
+    u.which = 1;
+    const EpiRows e{{p.dw_gate, p.dw_up, p.dw_down}, p.F, {p.d, p.F}, nullptr};
+    // one tile for both: by the three matrices' area in rows of d
+    err = run_tiles<TILE_RMAJ, TILE_RMAJ, false>(tile_size(3 * (int64_t)p.F, p.d, true), t, 1, e, st, &u);
   }
   return err;
 }

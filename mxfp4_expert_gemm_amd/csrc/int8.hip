@@ -13,18 +13,12 @@ namespace {
 struct EpiInt8 {
   const float *xs, *ws;
   uint16_t* out;
-  int32_t* part;  // split sums: [split][M][N]
-  int32_t M, N;
+  int32_t N;
+  int32_t* part;
   struct Held {};
-  __device__ __forceinline__ Held hold(int, int, int) const { return {}; }
-  __device__ __forceinline__ void put(int m, int n, int left, int split, const Held&, const int32_t (&v)[8]) const {
-    if (part) {
-      int32_t* p = part + ((int64_t)split * M + m) * N + n;
-#pragma unroll
-      for (int r = 0; r < 8; ++r)
-        if (r < left) p[r] = v[r];
-      return;
-    }
+  static constexpr bool JOINS = true;
+  __device__ __forceinline__ Held hold(int, int) const { return {}; }
+  __device__ __forceinline__ void put(int, int m, int n, int left, const Held&, const int32_t (&v)[8]) const {
     const float s = xs[m];
     uint16_t* o = out + (int64_t)m * N + n;
     if (left >= 8 && N % 8 == 0) {
@@ -44,17 +38,6 @@ struct EpiInt8 {
     }
   }
 };
-
-__global__ void __launch_bounds__(256) join_int8_kernel(const int32_t* __restrict__ part, int64_t n, int splits, int32_t N,
-                                                        const float* __restrict__ xs, const float* __restrict__ ws,
-                                                        uint16_t* __restrict__ out) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
-  int32_t v = 0;
-  for (int s = 0; s < splits; ++s) v += part[(int64_t)s * n + i];
-  const int64_t t = i / N;
-  out[i] = f32_to_bf16((float)v * xs[t] * ws[i - t * N]);
-}
 
 // One row a block.  Rows of up to 8192 values stay in registers between the search for the largest
 // and the codes; longer ones are read again.  The bits of |x| order like the values, with what is
@@ -122,14 +105,16 @@ __global__ void __launch_bounds__(256) quantize_int8_kernel(const uint16_t* __re
   for (int col = 8 * (threadIdx.x + 256 * C); col < n; col += 8 * 256) write(*reinterpret_cast<const uint4*>(row + col), col);
 }
 
-enum Int8Tile { I8_32, I8_64, I8_128, I8_224, I8_256 };
+// the tiles of ffn.hip, by the same rules
+enum Int8Tile { I8_16, I8_32, I8_48, I8_64, I8_128, I8_224, I8_256 };
 Int8Tile int8_tile(int64_t M, int64_t N) {
   if (ceil_div(M, 256) * ceil_div(N, 256) >= 192) return tiles_of_224(M, N) ? I8_224 : I8_256;
-  return M > 64 ? I8_128 : M > 32 ? I8_64 : I8_32;
+  return M > 64 ? I8_128 : (Int8Tile)((M - 1) / 16);
 }
 int int8_splits(int64_t M, int64_t N, int64_t K) {
   const Int8Tile z = int8_tile(M, N);
-  const int64_t tiles = z >= I8_224 ? 256 : z == I8_128 ? ceil_div(M, 128) * ceil_div(N, 128) : ceil_div(N, 32);
+  if (z >= I8_224) return 1;
+  const int64_t tiles = z == I8_128 ? ceil_div(M, 128) * ceil_div(N, 128) : ceil_div(N, 64);
   const int64_t most = K / 1024, want = 256 / tiles, s = want < most ? want : most;
   return s < 1 ? 1 : s > 16 ? 16 : (int)s;
 }
@@ -138,14 +123,13 @@ int int8_splits(int64_t M, int64_t N, int64_t K) {
 
 Int8Layout int8_layout(int64_t T, int32_t n_in, int32_t n_out, bool quantize) {
   Int8Layout l;
-  l.scale = 0;
-  l.q = quantize ? align_up((size_t)T * 4, 256) : 0;
-  l.part = l.q + (quantize ? align_up((size_t)T * n_in, 256) : 0);
   const int s = int8_splits(T, n_out, n_in);
-  l.total = l.part + (s > 1 ? align_up((size_t)s * T * n_out * 4, 256) : 0);
+  l.scale = 0;
+  l.q = (quantize ? align_up((size_t)T * 4, 256) : 0);
+  l.part = l.q + (quantize ? align_up((size_t)T * n_in, 256) : 0);
+  l.total = l.part + (s > 1 ? align_up((size_t)s * T * align_up(n_out, 8) * 4, 256) : 0);
   return l;
 }
-
 hipError_t launch_quantize_int8(const uint16_t* x, int64_t T, int32_t n, int8_t* q, float* scale, hipStream_t st) {
   hipLaunchKernelGGL(quantize_int8_kernel, dim3((unsigned)T), dim3(256), 0, st, x, n, q, scale);
   return hipGetLastError();
@@ -158,20 +142,17 @@ hipError_t launch_linear_int8(const int8_t* q, const float* xs, const int8_t* W,
   a.n = TileOperand{{W, W}, n_in, n_out};
   a.K = n_in;
   a.splits = int8_splits(T, n_out, n_in);
-  const EpiInt8 e{xs, ws, out, a.splits > 1 ? part : nullptr, (int32_t)T, n_out};
-  hipError_t err;
+  const EpiInt8 e{xs, ws, out, n_out, part};
+  constexpr int KM = TILE_KMAJ;
   switch (int8_tile(T, n_out)) {
-    case I8_256: err = launch_tile_gemm<TileCfg<8, 8, 2, 2, 5, TILE_KMAJ, TILE_KMAJ, false, true>>(a, 1, e, st); break;
-    case I8_224: err = launch_tile_gemm<TileCfg<8, 7, 2, 2, 5, TILE_KMAJ, TILE_KMAJ, false, true>>(a, 1, e, st); break;
-    case I8_128: err = launch_tile_gemm<TileCfg<4, 4, 2, 2, 5, TILE_KMAJ, TILE_KMAJ, false, true>>(a, 1, e, st); break;
-    case I8_64: err = launch_tile_gemm<TileCfg<2, 1, 2, 2, 13, TILE_KMAJ, TILE_KMAJ, false, true>>(a, 1, e, st); break;
-    default: err = launch_tile_gemm<TileCfg<1, 1, 2, 2, 13, TILE_KMAJ, TILE_KMAJ, false, true>>(a, 1, e, st); break;
+    case I8_256: return launch_tile_gemm<TileCfg<8, 8, 2, 2, 5, KM, KM, false, true>>(a, 1, e, st);
+    case I8_224: return launch_tile_gemm<TileCfg<8, 7, 2, 2, 5, KM, KM, false, true>>(a, 1, e, st);
+    case I8_128: return launch_tile_gemm<TileCfg<4, 4, 2, 2, 5, KM, KM, false, true>>(a, 1, e, st);
+    case I8_64: return launch_tile_gemm<TileCfg<4, 2, 1, 2, 9, KM, KM, false, true>>(a, 1, e, st);
+    case I8_48: return launch_tile_gemm<TileCfg<3, 2, 1, 2, 9, KM, KM, false, true>>(a, 1, e, st);
+    case I8_32: return launch_tile_gemm<TileCfg<2, 2, 1, 2, 9, KM, KM, false, true>>(a, 1, e, st);
+    default: return launch_tile_gemm<TileCfg<1, 2, 1, 2, 9, KM, KM, false, true>>(a, 1, e, st);
   }
-  if (err != hipSuccess || a.splits == 1) return err;
-  const int64_t n = T * n_out;
-  hipLaunchKernelGGL(join_int8_kernel, dim3((unsigned)ceil_div(n, 256)), dim3(256), 0, st, part, n, a.splits, n_out, xs, ws,
-                     out);
-  return hipGetLastError();
 }
 
 }  // namespace moe

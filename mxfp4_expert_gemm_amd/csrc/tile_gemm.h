@@ -53,7 +53,8 @@ struct TileOperand {
 struct TileArgs {
   TileOperand m, n;
   int64_t K;       // values of one K segment; K-major: whole pieces of 16 bytes
-  int32_t splits;  // the K tiles are dealt to so many blocks, each with results of its own
+  int32_t splits;  // the K tiles are dealt to so many blocks; tile_join adds their results
+  int32_t which;   // told to the epilogue: of two products in one launch, whose results these are
   // set by the launcher
   int32_t nk;        // K tiles of a segment
   int32_t nkt;       // K tiles in all (nk, or 2 nk)
@@ -152,7 +153,11 @@ struct TileCfg {
   static constexpr int SLOT = ML::BYTES > NL::BYTES ? ML::BYTES : NL::BYTES, LDS = R * SLOT;
   // one wave a SIMD where the accumulators need it
   static constexpr int WAVES = MI * NJ > 32 ? 1 : 2;
-  static constexpr int BLOCKS = 256 * (LDS > 81920 ? 1 : 2);  // resident at once on 256 CUs
+  // Few-token tiles stream their weights, all blocks at one pace: where rows are multiples of 4 KB
+  // apart they would all ask the same memory channels at once, so there each block begins elsewhere
+  // in K (one token, 8192 -> 7168: 22.5 us from 26; 7168 -> 8192, rows of 14 KB: 42.5 from 40.8).
+  static constexpr bool TURN = R > 5;
+  static constexpr int BLOCKS = 256 * (163840 / LDS);  // resident at once on 256 CUs
   static_assert(R % 2 == 1 && R >= 5, "two whole tiles (the first may be cut short) and one operand");
   static_assert(NW * 16 * 16 * NJ * 4 <= SLOT, "the epilogue passes 16 rows a wave through one slot");
 };
@@ -193,12 +198,14 @@ __device__ __forceinline__ void tile_settle(Acc (&acc)[C::MI][C::NJ]) {
 }
 
 // The epilogue's type Epi has
-//   struct Held             what it reads from memory for eight results
-//   Held hold(m, n, left)   reads that, ahead of the results (left: columns from n on that exist)
-//   void put(m, n, left, split, held, v)            eight results, or with GLU
-//   void put(m, n, left, split, held, v, w)         eight of each matrix
+//   struct Held                       what it reads from memory for eight results
+//   Held hold(m, n)                   reads that, ahead of the results
+//   void put(which, m, n, left, held, v)       eight results (left: columns from n on that exist), or with GLU
+//   void put(which, m, n, left, held, v, w)    eight of each matrix
+// and, where JOINS, for products whose K is split (tile_join adds the pieces and calls put with the sums),
+//   Value* part                       [splits][rows of M][rows of N rounded up to 8]
 template <class C, class Epi>
-__global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArgs p, Epi epi) {
+__global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArgs p0, TileArgs p1, Epi epi) {
   constexpr int MI = C::MI, NJ = C::NJ, R = C::R, H = (R - 1) / 2, BM = C::BM, BN = C::BN;
   using ML = typename C::ML;
   using NL = typename C::NL;
@@ -210,26 +217,37 @@ __global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArg
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / WAVE));
   const int wm = wave / C::WN, wn = wave % C::WN, rho = lane & 15, g = lane >> 4;
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
-  const int full = (int)(p.K / C::BK), part = full == p.nk ? 0 : p.nkt / p.nk;
   // this block's share: every gridDim / 8-th tile of its XCD's range
-  const int range = (p.nblocks + 7) / 8, first = (int)(blockIdx.x & 7) * range + (int)(blockIdx.x >> 3);
-  const int end = min((int)(blockIdx.x & 7) * range + range, p.nblocks), stride = gridDim.x >> 3;
+  const int all = p0.nblocks + p1.nblocks;
+  const int range = (all + 7) / 8, first = (int)(blockIdx.x & 7) * range + (int)(blockIdx.x >> 3);
+  const int end = min((int)(blockIdx.x & 7) * range + range, all), stride = gridDim.x >> 3;
 
   ML ml;
   NL nl;
-  int m0, n0, split, k0, nkt;
+  struct Place {  // of a tile of results
+    int which, m0, n0, split, splits, tile, rows_m, rows_n;
+  } at;
+  int full, part, k0, nkt, turn = 0;
   auto start = [&](int lb) {
     constexpr int GROUP = 8;
+    const bool second = lb >= p0.nblocks;
+    const TileArgs& p = second ? p1 : p0;
+    if (second) lb -= p0.nblocks;
     const int per = p.ntm * p.ntn;
-    split = lb / per;
-    const int tile = lb - split * per;
+    const int split = lb / per, tile = lb - split * per;
     const int span = GROUP * p.ntn, grp = tile / span, from = grp * GROUP;
     const int gs = p.ntm - from < GROUP ? p.ntm - from : GROUP;
     const int within = tile - grp * span;
-    m0 = (from + within % gs) * BM;
-    n0 = (within / gs) * C::OUT_N;
+    const int m0 = (from + within % gs) * BM, n0 = (within / gs) * C::OUT_N;
+    at = Place{p.which, m0, n0, split, p.splits, tile, p.m.rows, p.n.rows};
+    full = (int)(p.K / C::BK);
+    part = full == p.nk ? 0 : p.nkt / p.nk;
     k0 = (int)((int64_t)p.nkt * split / p.splits);
     nkt = (int)((int64_t)p.nkt * (split + 1) / p.splits) - k0;
+    if constexpr (C::TURN) {
+      const int whole = nkt - (k0 < part ? min(part - k0, nkt) : 0);
+      turn = whole > 0 && p.n.ld % 4096 == 0 ? (tile * 11) % whole : 0;
+    }
     ml.init(p.m, m0, p.K, C::ES, wave, lane);
     nl.init(p.n, n0, p.K, C::ES, wave, lane);
   };
@@ -237,6 +255,10 @@ __global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArg
   // the loads ahead of the loop have to look for them.
   auto place = [&](int t, bool& seg1) {
     int kt = k0 + t - part;
+    if constexpr (C::TURN) {
+      kt += turn;
+      if (kt >= k0 + nkt - part) kt -= nkt - (k0 < part ? part - k0 : 0);
+    }
     seg1 = kt >= full;
     return seg1 ? kt - full : kt;
   };
@@ -251,14 +273,14 @@ __global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArg
 
   // the operands of one step in registers
   u32x4_t fm[2][MI], fn[2][NJ];
-  auto tr_read = [&](const uint8_t* at, int row_bytes) {
+  auto tr_read = [&](const uint8_t* from, int row_bytes) {
     typedef __attribute__((address_space(3))) tg_s16x4* lp;
     union {
       tg_s16x4 h[2];
       u32x4_t v;
     } r;
-    r.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)at);
-    r.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(at + 4 * row_bytes));
+    r.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)from);
+    r.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(from + 4 * row_bytes));
     return r.v;
   };
   auto read_tile = [&](const uint8_t* slot, auto orderc, auto widthc, int ks, int row, int col0) -> u32x4_t {
@@ -271,13 +293,13 @@ __global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArg
     }
   };
   auto read_m = [&](const uint8_t* slot, int ks, int i) {
-    const int at = 16 * MI * wm + 16 * i;
-    return read_tile(slot, std::integral_constant<int, C::MORD>{}, std::integral_constant<int, ML::RP>{}, ks, at + rho, at);
+    const int r = 16 * MI * wm + 16 * i;
+    return read_tile(slot, std::integral_constant<int, C::MORD>{}, std::integral_constant<int, ML::RP>{}, ks, r + rho, r);
   };
   auto read_n = [&](const uint8_t* slot, int ks, int j) {
-    const int at = 16 * NJ * wn + 16 * j;
-    const int row = C::GLU ? (rho >> 3) * (BN / 2) + at / 2 + (rho & 7) : at + rho;
-    return read_tile(slot, std::integral_constant<int, C::NORD>{}, std::integral_constant<int, NL::RP>{}, ks, row, at);
+    const int r = 16 * NJ * wn + 16 * j;
+    const int row = C::GLU ? (rho >> 3) * (BN / 2) + r / 2 + (rho & 7) : r + rho;
+    return read_tile(slot, std::integral_constant<int, C::NORD>{}, std::integral_constant<int, NL::RP>{}, ks, row, r);
   };
   Acc acc[MI][NJ];
 
@@ -350,27 +372,36 @@ __global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArg
     return next;
   };
 
+  // one piece of a split K
+  auto store_part = [&](const Place& e, int m, int n, const Value (&v)[8]) {
+    if constexpr (Epi::JOINS) {
+      Value* q = epi.part + ((int64_t)e.split * e.rows_m + m) * ((e.rows_n + 7) & ~7) + n;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) *reinterpret_cast<Acc*>(q + 4 * h) = Acc{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+    }
+  };
+
   // Sixteen rows of the wave's results at a time through its part of the last slot (which the first
   // loads of the next tile leave alone), so that memory is met in runs of whole rows: row rho is
   // 16 NJ words, four of them at a time stored at their place ^ rho % 8 (of an odd NJ, whose rows
   // alternate between the halves of 128 bytes, ^ rho / 2 % 4).
-  auto epilogue = [&](int em, int en, int es) {
+  auto epilogue = [&](const Place& e) {
     constexpr int PR = (C::GLU ? 8 : 16) * NJ / 8;        // pieces of eight results of a row (of one matrix)
     constexpr int P = 16 * PR, PL = (P + 63) / 64;        // of 16 rows, and of a lane
     uint8_t* mine = lds + (R - 1) * C::SLOT + wave * (16 * 64 * NJ);
     const int wcols = (C::GLU ? 8 : 16) * NJ * wn;
     auto where = [&](int s, int i, int& m, int& n) {
       const int x = lane + 64 * s, row = x / PR, piece = x - row * PR;
-      m = em + 16 * MI * wm + 16 * i + row;
-      n = en + wcols + 8 * piece;
-      return x < P && m < p.m.rows && n < p.n.rows;
+      m = e.m0 + 16 * MI * wm + 16 * i + row;
+      n = e.n0 + wcols + 8 * piece;
+      return x < P && m < e.rows_m && n < e.rows_n;
     };
     typename Epi::Held held[2][PL];
     auto hold = [&](int i) {
 #pragma unroll
       for (int s = 0; s < PL; ++s) {
         int m, n;
-        if (where(s, i, m, n)) held[i & 1][s] = epi.hold(m, n, p.n.rows - n);
+        if (where(s, i, m, n)) held[i & 1][s] = epi.hold(m, n);
       }
     };
     hold(0);
@@ -402,9 +433,11 @@ __global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArg
         if constexpr (C::GLU) eight(8 * NJ + 8 * piece, w);
         if (in) {
           if constexpr (C::GLU)
-            epi.put(m, n, p.n.rows - n, es, held[i & 1][s], v, w);
+            epi.put(e.which, m, n, e.rows_n - n, held[i & 1][s], v, w);
+          else if (!Epi::JOINS || e.splits == 1)
+            epi.put(e.which, m, n, e.rows_n - n, held[i & 1][s], v);
           else
-            epi.put(m, n, p.n.rows - n, es, held[i & 1][s], v);
+            store_part(e, m, n, v);
         }
       }
       __builtin_amdgcn_wave_barrier();
@@ -433,14 +466,14 @@ __global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArg
     for (; t < nkt; ++t) slot = run_tile(std::false_type{}, t, slot);  // nothing left to load
     tile_settle<C>(acc);
     tile_wait_barrier<0>();  // the reads past the last step are done everywhere: the LDS is free
-    const int em = m0, en = n0, es = split;
+    const Place done = at;
     lb += stride;
     const bool more = lb < end;
     if (more) {
       start(lb);
       load_first();
     }
-    epilogue(em, en, es);
+    epilogue(done);
     if (!more) break;
   }
 }
@@ -452,22 +485,61 @@ inline bool tiles_of_224(int64_t M, int64_t N) {
   return turns(224) * 7 < turns(256) * 8;
 }
 
-template <class C, class Epi>
-hipError_t launch_tile_gemm(TileArgs a, int segs, const Epi& epi, hipStream_t st) {
+// The sums of the pieces of a split K, added in their order (the same call gives the same bits).  A
+// launch of its own, 4 us: joined by whichever block of a tile comes last, the pieces had to pass the
+// XCDs' own caches and one unit read all of a tile's (33 tokens, 7168 -> 3584: 20.4 us in all, 10.1 + 4 so).
+template <class Value, class Epi>
+__global__ void __launch_bounds__(256) tile_join_kernel(int64_t pieces, int32_t M, int32_t N, int splits, Epi epi) {
+  const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (x >= pieces) return;
+  typedef Value V4 __attribute__((ext_vector_type(4)));
+  const int32_t row = (N + 7) / 8;
+  const int m = (int)(x / row), n = 8 * (int)(x - (int64_t)m * row);
+  V4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const V4* q = reinterpret_cast<const V4*>(epi.part + ((int64_t)s * pieces + x) * 8);
+    a += q[0];
+    b += q[1];
+  }
+  const Value v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  epi.put(0, m, n, N - n, epi.hold(m, n), v);
+}
+
+// the K tiles and tiles of results of one product
+template <class C>
+bool tile_plan(TileArgs& a, int segs) {
   a.ntm = (int32_t)ceil_div(a.m.rows, C::BM);
   a.ntn = (int32_t)ceil_div(a.n.rows, C::OUT_N);
   a.nk = (int32_t)ceil_div(a.K, C::BK);
   a.nkt = a.nk * segs;
   const int64_t nb = (int64_t)a.ntm * a.ntn * a.splits;
-  if (a.splits < 1 || a.splits > a.nkt || nb > 0x7FFFFFF0) return hipErrorInvalidValue;
   a.nblocks = (int32_t)nb;
+  return a.splits >= 1 && a.splits <= a.nkt && nb <= 0x3FFFFFF0;
+}
+// One product, or two in one launch (of one K segment each).
+template <class C, class Epi>
+hipError_t launch_tile_gemm(TileArgs a, int segs, const Epi& epi, hipStream_t st, const TileArgs* second = nullptr) {
+  TileArgs b{};
+  if (second) b = *second;
+  if (!tile_plan<C>(a, segs) || (second && !tile_plan<C>(b, 1))) return hipErrorInvalidValue;
+  const int64_t nb = (int64_t)a.nblocks + b.nblocks;
   const unsigned grid = (unsigned)(nb < C::BLOCKS ? (nb + 7) / 8 * 8 : C::BLOCKS);
   if constexpr (C::LDS > 65536) {
     static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&tile_gemm_kernel<C, Epi>),
                                                     hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((tile_gemm_kernel<C, Epi>), dim3(grid), dim3(C::NW * 64), C::LDS, st, a, epi);
+  hipLaunchKernelGGL((tile_gemm_kernel<C, Epi>), dim3(grid), dim3(C::NW * 64), C::LDS, st, a, b, epi);
+  if constexpr (Epi::JOINS) {
+    if (a.splits > 1) {
+      if (second) return hipErrorInvalidValue;
+      using Value = std::conditional_t<C::I8, int32_t, float>;
+      const int64_t pieces = (int64_t)a.m.rows * ceil_div(a.n.rows, 8);
+      hipLaunchKernelGGL((tile_join_kernel<Value, Epi>), dim3((unsigned)ceil_div(pieces, 256)), dim3(256), 0, st, pieces,
+                         a.m.rows, a.n.rows, a.splits, epi);
+    }
+  }
   return hipGetLastError();
 }
 
