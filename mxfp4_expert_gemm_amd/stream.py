@@ -14,16 +14,19 @@ shrinks), five times the 288 GB of one MI355X.  Two facts of that post decide th
   others stream (section on streaming the trunk, which applies it to the dense weights).
 
 `plan_prefix` sizes N for an HBM budget, `cache_hits` replays the scan for either policy,
-and `LayerStack` runs a stack with the first N layers resident and the rest streamed.
+and `LayerStack` runs a stack with the first N layers resident and the rest streamed: each
+layer on an input of its own (`step`), or as the blocks of one residual stream with the norms
+between them, dense layers among them and a projection of the result (`forward`).
 """
 from __future__ import annotations
 
 from collections import OrderedDict
-from typing import List, Optional, Sequence
+from typing import List, Optional, Sequence, Tuple
 
 import torch
 
-from . import alloc_expert_slots, alloc_workspace, layer_forward, layer_forward_streamed, make_config
+from . import (NORM_EPS, _at, alloc_expert_slots, alloc_workspace, block_norms, gated_ffn, gated_ffn_workspace_size,
+               layer_forward, layer_forward_streamed, linear_bf16, linear_int8, make_config)
 
 
 def plan_prefix(num_layers: int, layer_expert_bytes: int, hbm_budget_bytes: int, reserved_bytes: int = 0) -> int:
@@ -59,6 +62,10 @@ def cache_hits(num_layers: int, passes: int, slots: int, policy: str) -> int:
     return hits
 
 
+def _dense(layer: dict) -> bool:
+    return "w_gate" in layer
+
+
 class LayerStack:
     """A stack of MoE layers: dense weights in HBM, experts in HBM for the first `pinned`
     layers and in pinned host memory for the others.
@@ -67,6 +74,12 @@ class LayerStack:
     and expert_blob_host (pinned host uint8 tensor, E records).  Layers may share tensors
     (the same object is uploaded once).  Every layer call uses one workspace and one slot
     buffer, sized for `num_tokens` tokens.
+
+    A dict with w_gate, w_up and w_down (device bf16 tensors) is a dense layer instead, a gated
+    block whose weights stay in HBM; it counts among the pinned layers where it stands among them.
+    For `forward`, a layer's dict may hold pre_norm (bf16 [d]: the norm of its input; without it
+    the layer takes the stream as it is), post_norm (bf16 [d]: the norm of its result), gate
+    (bf16 [d] or [num_tokens, d]) and scale (a number) for its result's way into the stream.
     """
 
     def __init__(self, layers: Sequence[dict], k: int, d_ffn: int, pinned: int, num_tokens: int, *,
@@ -77,7 +90,12 @@ class LayerStack:
         self.k, self.d_ffn, self.pinned, self.packed = k, d_ffn, pinned, packed
         self.resident: List[Optional[torch.Tensor]] = []
         uploaded = {}
+        width = None
         for i, lay in enumerate(self.layers):
+            width = width or (lay["w_gate"] if _dense(lay) else lay["router_w"]).shape[1]
+            if _dense(lay):
+                self.resident.append(None)
+                continue
             host = lay["expert_blob_host"]
             if host.is_cuda or not host.is_pinned():
                 raise ValueError(f"layer {i}: expert_blob_host must be a pinned host tensor")
@@ -88,22 +106,67 @@ class LayerStack:
                 self.resident.append(uploaded[key])
             else:
                 self.resident.append(None)
-        first = self.layers[0]
-        T, d = num_tokens, first["router_w"].shape[1]
-        cfg = make_config(T, d, first["latent_down"].shape[0], d_ffn, first["router_w"].shape[0], packed=packed)
-        self.workspace = alloc_workspace(cfg, k, device)
-        self.slots = alloc_expert_slots(cfg, k, device) if pinned < len(self.layers) else None
-        self.num_tokens = T
+        T, self.d_model, self.num_tokens = num_tokens, width, num_tokens
+        self.workspace = self.slots = None
+        sparse = [i for i, lay in enumerate(self.layers) if not _dense(lay)]
+        if sparse:
+            first = self.layers[sparse[0]]
+            cfg = make_config(T, width, first["latent_down"].shape[0], d_ffn, first["router_w"].shape[0], packed=packed)
+            self.workspace = alloc_workspace(cfg, k, device)
+            self.slots = alloc_expert_slots(cfg, k, device) if pinned <= sparse[-1] else None
+        widest = [gated_ffn_workspace_size(T, width, lay["w_gate"].shape[0]) for lay in self.layers if _dense(lay)]
+        self.dense_workspace = torch.empty(max(widest), dtype=torch.uint8, device=device) if widest else None
 
     def forward_layer(self, i: int, x: torch.Tensor, out: Optional[torch.Tensor] = None,
                       routing: Optional[dict] = None, stream=None) -> torch.Tensor:
         lay = self.layers[i]
+        if _dense(lay):
+            if routing is not None:
+                raise ValueError(f"layer {i} is dense: it routes nothing")
+            # of another number of tokens the workspace may be too small
+            work = self.dense_workspace if x.shape[0] == self.num_tokens else None
+            return gated_ffn(x, lay["w_gate"], lay["w_up"], lay["w_down"], out=out, workspace=work, stream=stream)
         args = (x, lay["router_w"], lay["latent_down"], lay["latent_up"])
         kw = dict(d_ffn=self.d_ffn, bias=lay.get("bias"), out=out, workspace=self.workspace, routing=routing,
                   stream=stream, packed=self.packed)
         if self.resident[i] is not None:
             return layer_forward(*args, self.resident[i], self.k, **kw)
         return layer_forward_streamed(*args, lay["expert_blob_host"], self.k, expert_slots=self.slots, **kw)
+
+    def forward(self, x: torch.Tensor, *, final_norm: Optional[torch.Tensor] = None, head=None, eps: float = NORM_EPS,
+                stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+        """One pass of a residual stream over the stack, x bf16 [num_tokens, d] its start: for each layer
+            stream = stream + scale gate norm(layer(norm(stream) pre_norm)) post_norm
+        with what its dict holds of them; attention, which comes between them in a model, is not part of
+        this path.  One call to block_norms ends a layer and begins the next.  Returns (stream, None),
+        with final_norm (bf16 [d]) the normed stream as the second, and with head the projection of it:
+        a bf16 [n_out, d] for linear_bf16 or (codes, scales) for linear_int8."""
+        if x.shape != (self.num_tokens, self.d_model):
+            raise ValueError(f"x must be of shape {(self.num_tokens, self.d_model)}")
+        if head is not None and final_norm is None:
+            raise ValueError("head needs final_norm")
+        residual = y = None
+        done = {}
+        for i, lay in enumerate(self.layers + [{"pre_norm": final_norm}]):
+            pre = lay.get("pre_norm")
+            if y is None:  # the start: x itself, of which there is at most the norm
+                residual, h = x, x
+                if pre is not None:
+                    h = block_norms(None, x, pre_weight=pre, eps=eps, stream=stream)[1]
+            else:  # the first result takes a place of its own, the others are added there
+                into = None if residual is x else residual
+                residual, h = block_norms(y, residual, pre_weight=pre, post_weight=done.get("post_norm"),
+                                          gate=done.get("gate"), scale=done.get("scale", 1.0), eps=eps, out=into,
+                                          stream=stream)
+                h = residual if pre is None else h
+            if i < len(self.layers):
+                y, done = self.forward_layer(i, h, stream=stream), lay
+        if head is None:
+            return residual, None if final_norm is None else h
+        with _at(stream):
+            if isinstance(head, torch.Tensor):
+                return residual, linear_bf16(h, head)
+            return residual, linear_int8(h, *head)
 
     def step(self, xs: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]] = None,
              stream=None) -> List[torch.Tensor]:
