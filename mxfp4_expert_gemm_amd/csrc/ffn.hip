@@ -4,8 +4,9 @@
 //   backward:  dA = Wd^T dout (fp32), s = 1 / (1 + e^-g),
 //              a = bf16(g s u), dU = bf16(dA g s), dG = bf16(dA u s (1 + g (1 - s))),
 //              dx = bf16(Wg^T dG + Wu^T dU), dWg = bf16(dG^T x), dWu = bf16(dU^T x), dWd = bf16(dout^T a)
-// a, dG and dU are rounded to bf16 since the matrix cores read them; every sum is fp32 (the kept
-// g and u are bf16 so that training holds 4 bytes for a token and inner channel and not 8).
+// a, dG and dU are rounded to bf16 since the matrix cores read them (of few tokens, where that costs
+// nothing, they keep 16 bits or all); every sum is fp32 (the kept g and u are bf16 so that training
+// holds 4 bytes for a token and inner channel and not 8).
 #include "common.h"
 #include "kernels.h"
 #include "mfma_stream.h"
@@ -70,11 +71,19 @@ struct EpiGlu {
   }
 };
 
-// dA's tile meets the kept g and u: a, dG, dU.  dgu holds dG and dU side by side, [T][2 F].
+// what rounding v to bf16 leaves, or 0 where it does not stay finite
+__device__ __forceinline__ float rounded_off(float v) {
+  const float r = v - (float)(__bf16)v;
+  return fabsf(r) < INFINITY ? r : 0.f;
+}
+
+// dA's tile meets the kept g and u: a, dG, dU.  dgu holds dG and dU side by side, [T][2 F].  LOW: behind
+// the T rows of either lie as many of what the rounding of those left.
+template <bool LOW>
 struct EpiGluBack {
   const uint16_t *gate, *up;
   uint16_t *a, *dgu;
-  int32_t F;
+  int32_t F, T;
   struct Held {
     uint4 g, u;
   };
@@ -99,6 +108,18 @@ struct EpiGluBack {
     uint16_t* o = dgu + (int64_t)m * 2 * F + n;
     store8(o, dg);
     store8(o + F, du);
+    if constexpr (LOW) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        av[i] = rounded_off(av[i]);
+        dg[i] = rounded_off(dg[i]);
+        du[i] = rounded_off(du[i]);
+      }
+      store8(a + (int64_t)(m + T) * F + n, av);
+      o += (int64_t)T * 2 * F;
+      store8(o, dg);
+      store8(o + F, du);
+    }
   }
 };
 
@@ -107,21 +128,27 @@ struct EpiGluBack {
 // out[t][row] = sum_k w[row][k] in[t][k]; GLU: bf16(silu(g) u), and g and u where they are kept.
 // Bound: HBM.  A lane's sum is at most K / 128 pairs of products one after another, in fp32, then a
 // tree over the lanes.
+// WIDE: a stays fp32 between the two launches (GLU writes it so, the other reads it so).
 struct GemvArgs {
   const uint16_t *w, *w1;  // [rows][K]
-  const uint16_t* in;      // [T][K]
-  uint16_t *out, *gate, *up;  // [T][rows]; the last two nullable
+  const void* in;          // [T][K]
+  void* out;               // [T][rows]
+  uint16_t *gate, *up;     // [T][rows], nullable
   int32_t T, K, rows;
 };
 constexpr int GEMV_TOKENS = 8;
-template <int G, bool GLU>
-__global__ void __launch_bounds__(256) ffn_gemv_kernel(GemvArgs p) {
-  constexpr int U = 8, M = GLU ? 2 : 1;
+// rows of a block: every block reads all tokens, which of fp32 values is as much as two rows of weights
+// each (8192 -> 7168, one token: 22.7 us with four rows)
+constexpr int gemv_rows(bool glu, bool wide) { return wide && !glu ? 8 : 4; }
+template <int G, bool GLU, bool WIDE>
+__global__ void __launch_bounds__(64 * gemv_rows(GLU, WIDE)) ffn_gemv_kernel(GemvArgs p) {
+  constexpr int ROWS = gemv_rows(GLU, WIDE);
+  constexpr int U = 8, M = GLU ? 2 : 1, P = WIDE && !GLU ? 2 : 1;  // P x 16 bytes: eight values of a token
   extern __shared__ __align__(16) uint8_t lds[];
-  uint4* xs = reinterpret_cast<uint4*>(lds);  // [G][K / 8]
+  uint4* xs = reinterpret_cast<uint4*>(lds);  // [G][P][K / 8]
   const int lane = lane_id(), wave = threadIdx.x / WAVE;
-  const int row = min((int)blockIdx.x * 4 + wave, p.rows - 1);
-  const bool mine = blockIdx.x * 4 + wave < p.rows;
+  const int row = min((int)blockIdx.x * ROWS + wave, p.rows - 1);
+  const bool mine = blockIdx.x * ROWS + wave < p.rows;
   const int pieces = p.K / 8;
   const uint4* w[2];
   w[0] = reinterpret_cast<const uint4*>(p.w + (int64_t)row * p.K);
@@ -138,8 +165,8 @@ __global__ void __launch_bounds__(256) ffn_gemv_kernel(GemvArgs p) {
   load(0);
 #pragma unroll
   for (int t = 0; t < G; ++t) {
-    const uint4* x = reinterpret_cast<const uint4*>(p.in + (int64_t)min(t, p.T - 1) * p.K);
-    for (int i = threadIdx.x; i < pieces; i += 256) xs[t * pieces + i] = x[i];
+    const uint4* x = static_cast<const uint4*>(p.in) + (int64_t)min(t, p.T - 1) * pieces * P;
+    for (int i = threadIdx.x; i < pieces * P; i += 64 * ROWS) xs[(t * P + i % P) * pieces + i / P] = x[i];
   }
   lds_barrier();
   float acc[M][G];
@@ -160,8 +187,18 @@ __global__ void __launch_bounds__(256) ffn_gemv_kernel(GemvArgs p) {
       if (base + 64 * u >= pieces) break;
 #pragma unroll
       for (int t = 0; t < G; ++t) {
-        const uint4 x = xs[t * pieces + min(at, pieces - 1)];
+        const uint4 x = xs[t * P * pieces + min(at, pieces - 1)];
         const bool in = at < pieces;
+        if constexpr (P == 2) {
+          const uint4 y = xs[(t * P + 1) * pieces + min(at, pieces - 1)];
+          float v[8], s = acc[0][t];
+          unpack8(cur[0][u], v);
+          const uint32_t b[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s = __builtin_fmaf(__builtin_bit_cast(float, b[i]), v[i], s);
+          acc[0][t] = in ? s : acc[0][t];
+          continue;
+        }
 #pragma unroll
         for (int m = 0; m < M; ++m) {
           float s = acc[m][t];
@@ -182,38 +219,47 @@ __global__ void __launch_bounds__(256) ffn_gemv_kernel(GemvArgs p) {
     if (lane == 0 && mine && t < p.T) {
       const int64_t at = (int64_t)t * p.rows + row;
       if constexpr (GLU) {
-        p.out[at] = glu_bf16(v[0], v[1]);
+        if constexpr (WIDE)
+          static_cast<float*>(p.out)[at] = silu_f32(v[0]) * v[1];
+        else
+          static_cast<uint16_t*>(p.out)[at] = glu_bf16(v[0], v[1]);
         if (p.gate) {
           p.gate[at] = f32_to_bf16(v[0]);
           p.up[at] = f32_to_bf16(v[1]);
         }
       } else {
-        p.out[at] = f32_to_bf16(v[0]);
+        static_cast<uint16_t*>(p.out)[at] = f32_to_bf16(v[0]);
       }
     }
   }
 }
-template <int G, bool GLU>
+template <int G, bool GLU, bool WIDE>
 hipError_t launch_gemv(const GemvArgs& a, hipStream_t st) {
-  const size_t lds = (size_t)G * a.K * 2;
+  const size_t lds = (size_t)G * a.K * (WIDE && !GLU ? 4 : 2);
   if (lds > 65536) {
-    static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&ffn_gemv_kernel<G, GLU>),
+    static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&ffn_gemv_kernel<G, GLU, WIDE>),
                                                     hipFuncAttributeMaxDynamicSharedMemorySize, 163840);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((ffn_gemv_kernel<G, GLU>), dim3((unsigned)ceil_div(a.rows, 4)), dim3(256), lds, st, a);
+  hipLaunchKernelGGL((ffn_gemv_kernel<G, GLU, WIDE>), dim3((unsigned)ceil_div(a.rows, gemv_rows(GLU, WIDE))),
+                     dim3(64 * gemv_rows(GLU, WIDE)), lds, st, a);
   return hipGetLastError();
 }
 template <bool GLU>
-hipError_t gemv(const GemvArgs& a, hipStream_t st) {
-  if (a.T == 1) return launch_gemv<1, GLU>(a, st);
-  if (a.T == 2) return launch_gemv<2, GLU>(a, st);
-  return a.T <= 4 ? launch_gemv<4, GLU>(a, st) : launch_gemv<8, GLU>(a, st);
+hipError_t gemv(const GemvArgs& a, bool wide, hipStream_t st) {
+  if (a.T > 4) return launch_gemv<8, GLU, false>(a, st);
+  if (a.T > 2) return wide ? launch_gemv<4, GLU, true>(a, st) : launch_gemv<4, GLU, false>(a, st);
+  if (a.T > 1) return wide ? launch_gemv<2, GLU, true>(a, st) : launch_gemv<2, GLU, false>(a, st);
+  return launch_gemv<1, GLU, true>(a, st);  // of one token every width fits
 }
 // the tokens' rows have to fit the LDS
-bool gemv_takes(int64_t T, int32_t K) {
-  return T <= GEMV_TOKENS && (int64_t)(T <= 2 ? T : T <= 4 ? 4 : 8) * K * 2 <= 163840;
+bool gemv_takes(int64_t T, int32_t K, int value_bytes = 2) {
+  return T <= GEMV_TOKENS && (int64_t)(T <= 2 ? T : T <= 4 ? 4 : 8) * K * value_bytes <= 163840;
 }
+// Up to four tokens a stays fp32 where it fits: the results are off by their own rounding alone
+// (8192 -> 7168, one token: 21.4 us, of a rounded 20.8).  Of eight tokens the reads of fp32 values
+// would bind on the LDS.
+bool gemv_wide(int64_t T, int32_t d, int32_t F) { return T <= 4 && gemv_takes(T, d) && gemv_takes(T, F, 4); }
 
 // Tiles by the rows of M: few tokens take 16, 32, 48 or 64 rows by 64 columns in blocks of two
 // waves, two blocks a unit, with a deep ring; then 128 x 128, two blocks a unit; and 256 x 256 (or
@@ -234,10 +280,16 @@ int splits_of(int64_t M, int64_t N, int64_t K, bool row_major) {
   const int64_t most = K / 512, want = 256 / tiles, s = want < most ? want : most;
   return s < 1 ? 1 : s > 16 ? 16 : (int)s;
 }
-size_t part_bytes(int64_t M, int64_t N, int64_t K, bool row_major) {
+size_t part_bytes(int64_t M, int64_t N, int64_t K, bool row_major, int halves = 1) {
   const int s = splits_of(M, N, K, row_major);
-  return s > 1 ? (size_t)s * M * N * 4 : 0;
+  return s * halves > 1 ? (size_t)s * M * N * 4 : 0;
 }
+// Backward of few tokens: a, dG and dU are held in two halves of 8 bits each, since that is free there
+// (one tile of rows and of K takes both).  Of more tokens each is rounded once.
+constexpr int64_t HALVES_TOKENS = 64;
+int halves_of(int64_t T) { return T <= HALVES_TOKENS ? 2 : 1; }
+template <int MO, int NO, bool GLU>
+using Tile128 = TileCfg<4, 4, 2, 2, 5, MO, NO, GLU>;
 template <int MO, int NO, bool GLU, class Epi>
 hipError_t run_tiles(TileSize z, const TileArgs& a, int segs, const Epi& e, hipStream_t st, const TileArgs* b = nullptr) {
   if (z == TILE_256) return launch_tile_gemm<TileCfg<8, 8, 2, 2, 5, MO, NO, GLU>>(a, segs, e, st, b);
@@ -251,7 +303,7 @@ hipError_t run_tiles(TileSize z, const TileArgs& a, int segs, const Epi& e, hipS
       default: break;
     }
   }
-  return launch_tile_gemm<TileCfg<4, 4, 2, 2, 5, MO, NO, GLU>>(a, segs, e, st, b);
+  return launch_tile_gemm<Tile128<MO, NO, GLU>>(a, segs, e, st, b);
 }
 
 TileOperand operand(const void* p, int64_t ld_values, int32_t rows, const void* p1 = nullptr) {
@@ -263,17 +315,18 @@ TileOperand operand(const void* p, int64_t ld_values, int32_t rows, const void* 
 FfnLayout ffn_layout(int64_t T, int32_t d, int32_t F) {
   FfnLayout l;
   l.a = 0;
-  l.part = l.a + align_up((size_t)T * F * 2, 256);
+  l.part = l.a + align_up((size_t)T * F * (gemv_wide(T, d, F) ? 4 : 2), 256);
   l.dgu = 0;
   l.total = l.part + align_up(part_bytes(T, d, F, false), 256);
   return l;
 }
 FfnLayout ffn_backward_layout(int64_t T, int32_t d, int32_t F) {
   FfnLayout l;
+  const int h = halves_of(T);
   l.a = 0;
-  l.dgu = l.a + align_up((size_t)T * F * 2, 256);
-  l.part = l.dgu + align_up((size_t)T * F * 4, 256);
-  l.total = l.part + align_up(part_bytes(T, d, 2 * (int64_t)F, true), 256);
+  l.dgu = l.a + align_up((size_t)T * F * 2 * h, 256);
+  l.part = l.dgu + align_up((size_t)T * F * 4 * h, 256);
+  l.total = l.part + align_up(part_bytes(h * T, d, 2 * (int64_t)F, true, h), 256);
   return l;
 }
 
@@ -284,21 +337,23 @@ hipError_t launch_ffn(const FfnArgs& p, void* ws, hipStream_t st) {
   const int32_t T = (int32_t)p.T;
   hipError_t err;
   TileArgs t{};
+  const bool wide = gemv_wide(T, p.d, p.F);
   if (gemv_takes(T, p.d)) {
-    err = gemv<true>(GemvArgs{p.w_gate, p.w_up, p.x, a, p.gate, p.up, T, p.d, p.F}, st);
+    err = gemv<true>(GemvArgs{p.w_gate, p.w_up, p.x, a, p.gate, p.up, T, p.d, p.F}, wide, st);
   } else {
     t.m = operand(p.x, p.d, T);
     t.n = operand(p.w_gate, p.d, p.F, p.w_up);
     t.K = p.d;
-    t.splits = 1;
+    t.splits = t.halves = 1;
     err = run_tiles<TILE_KMAJ, TILE_KMAJ, true>(tile_size(T, 2 * (int64_t)p.F, false), t, 1, EpiGlu{a, p.gate, p.up, p.F}, st);
   }
   if (err != hipSuccess) return err;
-  if (gemv_takes(T, p.F)) return gemv<false>(GemvArgs{p.w_down, nullptr, a, p.out, nullptr, nullptr, T, p.F, p.d}, st);
+  if (gemv_takes(T, p.F)) return gemv<false>(GemvArgs{p.w_down, nullptr, a, p.out, nullptr, nullptr, T, p.F, p.d}, wide, st);
   t.m = operand(a, p.F, T);
   t.n = operand(p.w_down, p.F, p.d);
   t.K = p.F;
   t.splits = splits_of(T, p.d, p.F, false);
+  t.halves = 1;
   const EpiRows e{{p.out, nullptr, nullptr}, T, {p.d, 0}, reinterpret_cast<float*>(w + l.part)};
   return run_tiles<TILE_KMAJ, TILE_KMAJ, false>(tile_size(T, p.d, false), t, 1, e, st);
 }
@@ -311,33 +366,38 @@ hipError_t launch_ffn_backward(const FfnBackArgs& p, void* ws, hipStream_t st) {
   uint16_t* a = reinterpret_cast<uint16_t*>(w + l.a);
   uint16_t* dgu = reinterpret_cast<uint16_t*>(w + l.dgu);
   const int32_t T = (int32_t)p.T;
+  const int h = halves_of(T);
   TileArgs t{};
   t.m = operand(p.dout, p.d, T);
   t.n = operand(p.w_down, p.F, p.F);
   t.K = p.d;
-  t.splits = 1;
-  hipError_t err = run_tiles<TILE_KMAJ, TILE_RMAJ, false>(tile_size(T, p.F, true), t, 1,
-                                                          EpiGluBack{p.gate, p.up, a, dgu, p.F}, st);
+  t.splits = t.halves = 1;
+  hipError_t err;
+  if (h > 1)  // always tiles of 128
+    err = launch_tile_gemm<Tile128<TILE_KMAJ, TILE_RMAJ, false>>(t, 1, EpiGluBack<true>{p.gate, p.up, a, dgu, p.F, T}, st);
+  else
+    err = run_tiles<TILE_KMAJ, TILE_RMAJ, false>(tile_size(T, p.F, true), t, 1, EpiGluBack<false>{p.gate, p.up, a, dgu, p.F, T}, st);
   if (err == hipSuccess && p.dx) {
-    t.m = operand(dgu, 2 * (int64_t)p.F, T, dgu + p.F);
+    t.m = operand(dgu, 2 * (int64_t)p.F, h * T, dgu + p.F);
     t.n = operand(p.w_gate, p.d, p.d, p.w_up);
     t.K = p.F;
-    t.splits = splits_of(T, p.d, 2 * (int64_t)p.F, true);
+    t.splits = splits_of(h * T, p.d, 2 * (int64_t)p.F, true);
+    t.halves = h;
     const EpiRows e{{p.dx, nullptr, nullptr}, T, {p.d, 0}, reinterpret_cast<float*>(w + l.part)};
-    err = run_tiles<TILE_KMAJ, TILE_RMAJ, false>(tile_size(T, p.d, true), t, 2, e, st);
+    err = run_tiles<TILE_KMAJ, TILE_RMAJ, false>(tile_size(h * T, p.d, true), t, 2, e, st);
   }
   if (err == hipSuccess && p.dw_gate) {
     TileArgs u{};
-    t.m = operand(dgu, 2 * (int64_t)p.F, 2 * p.F);
+    t.m = operand(dgu, 2 * (int64_t)p.F, 2 * p.F, dgu + 2 * (int64_t)p.F * T);  // the second halves, of h == 2
     t.n = operand(p.x, p.d, p.d);
     u.m = operand(p.dout, p.d, p.d);
-    u.n = operand(a, p.F, p.F);
+    u.n = operand(a, p.F, p.F, a + (int64_t)p.F * T);
     t.K = u.K = T;
-    t.splits = u.splits = 1;
+    t.splits = u.splits = t.halves = u.halves = 1;
     u.which = 1;
     const EpiRows e{{p.dw_gate, p.dw_up, p.dw_down}, p.F, {p.d, p.F}, nullptr};
     // one tile for both: by the three matrices' area in rows of d
-    err = run_tiles<TILE_RMAJ, TILE_RMAJ, false>(tile_size(3 * (int64_t)p.F, p.d, true), t, 1, e, st, &u);
+    err = run_tiles<TILE_RMAJ, TILE_RMAJ, false>(tile_size(3 * (int64_t)p.F, p.d, true), t, h, e, st, &u);
   }
   return err;
 }

@@ -142,6 +142,7 @@ hipError_t launch_linear_int8(const int8_t* q, const float* xs, const int8_t* W,
   a.n = TileOperand{{W, W}, n_in, n_out};
   a.K = n_in;
   a.splits = int8_splits(T, n_out, n_in);
+  a.halves = 1;
   const EpiInt8 e{xs, ws, out, n_out, part};
   constexpr int KM = TILE_KMAJ;
   switch (int8_tile(T, n_out)) {

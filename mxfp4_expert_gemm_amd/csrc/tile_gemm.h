@@ -54,6 +54,7 @@ struct TileArgs {
   TileOperand m, n;
   int64_t K;       // values of one K segment; K-major: whole pieces of 16 bytes
   int32_t splits;  // the K tiles are dealt to so many blocks; tile_join adds their results
+  int32_t halves;  // 2: the second half of M's rows are the low bits of the first's; tile_join adds their results
   int32_t which;   // told to the epilogue: of two products in one launch, whose results these are
   // set by the launcher
   int32_t nk;        // K tiles of a segment
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArg
   ML ml;
   NL nl;
   struct Place {  // of a tile of results
-    int which, m0, n0, split, splits, tile, rows_m, rows_n;
+    int which, m0, n0, split, joins, tile, rows_m, rows_n;
   } at;
   int full, part, k0, nkt, turn = 0;
   auto start = [&](int lb) {
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArg
     const int gs = p.ntm - from < GROUP ? p.ntm - from : GROUP;
     const int within = tile - grp * span;
     const int m0 = (from + within % gs) * BM, n0 = (within / gs) * C::OUT_N;
-    at = Place{p.which, m0, n0, split, p.splits, tile, p.m.rows, p.n.rows};
+    at = Place{p.which, m0, n0, split, p.splits * p.halves, tile, p.m.rows, p.n.rows};
     full = (int)(p.K / C::BK);
     part = full == p.nk ? 0 : p.nkt / p.nk;
     k0 = (int)((int64_t)p.nkt * split / p.splits);
@@ -434,7 +435,7 @@ __global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArg
         if (in) {
           if constexpr (C::GLU)
             epi.put(e.which, m, n, e.rows_n - n, held[i & 1][s], v, w);
-          else if (!Epi::JOINS || e.splits == 1)
+          else if (!Epi::JOINS || e.joins == 1)
             epi.put(e.which, m, n, e.rows_n - n, held[i & 1][s], v);
           else
             store_part(e, m, n, v);
@@ -517,12 +518,12 @@ bool tile_plan(TileArgs& a, int segs) {
   a.nblocks = (int32_t)nb;
   return a.splits >= 1 && a.splits <= a.nkt && nb <= 0x3FFFFFF0;
 }
-// One product, or two in one launch (of one K segment each).
+// One product, or two in one launch (of as many K segments each).
 template <class C, class Epi>
 hipError_t launch_tile_gemm(TileArgs a, int segs, const Epi& epi, hipStream_t st, const TileArgs* second = nullptr) {
   TileArgs b{};
   if (second) b = *second;
-  if (!tile_plan<C>(a, segs) || (second && !tile_plan<C>(b, 1))) return hipErrorInvalidValue;
+  if (!tile_plan<C>(a, segs) || (second && !tile_plan<C>(b, segs))) return hipErrorInvalidValue;
   const int64_t nb = (int64_t)a.nblocks + b.nblocks;
   const unsigned grid = (unsigned)(nb < C::BLOCKS ? (nb + 7) / 8 * 8 : C::BLOCKS);
   if constexpr (C::LDS > 65536) {
@@ -532,12 +533,13 @@ hipError_t launch_tile_gemm(TileArgs a, int segs, const Epi& epi, hipStream_t st
   }
   hipLaunchKernelGGL((tile_gemm_kernel<C, Epi>), dim3(grid), dim3(C::NW * 64), C::LDS, st, a, b, epi);
   if constexpr (Epi::JOINS) {
-    if (a.splits > 1) {
-      if (second) return hipErrorInvalidValue;
+    if (a.splits * a.halves > 1) {
+      if (second || a.m.rows % a.halves) return hipErrorInvalidValue;
       using Value = std::conditional_t<C::I8, int32_t, float>;
-      const int64_t pieces = (int64_t)a.m.rows * ceil_div(a.n.rows, 8);
+      const int32_t rows = a.m.rows / a.halves;  // a piece of all of M's rows is one of each half
+      const int64_t pieces = (int64_t)rows * ceil_div(a.n.rows, 8);
       hipLaunchKernelGGL((tile_join_kernel<Value, Epi>), dim3((unsigned)ceil_div(pieces, 256)), dim3(256), 0, st, pieces,
-                         a.m.rows, a.n.rows, a.splits, epi);
+                         rows, a.n.rows, a.splits * a.halves, epi);
     }
   }
   return hipGetLastError();

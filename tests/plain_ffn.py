@@ -26,8 +26,8 @@ def sigmoid(g):
     return 1.0 / (1.0 + torch.exp(-g))
 
 
-def forward(x, wg, wu, wd):
-    """{name: (value, bound)} of out, gate, up."""
+def forward(x, wg, wu, wd, inner=H):
+    """{name: (value, bound)} of out, gate, up; inner: what a's rounding may leave, relative."""
     d, F = wg.shape[1], wg.shape[0]
     g, u = mat(x, wg.T), mat(x, wu.T)
     dg = mat(x.abs(), wg.abs().T) * sum_bound(d)
@@ -35,14 +35,15 @@ def forward(x, wg, wu, wd):
     s = g * sigmoid(g)
     a = s * u
     # |silu'| <= 1.1; silu and the product in fp32: 16 ulps
-    da = 2 * (1.1 * dg * u.abs() + s.abs() * du) + a.abs() * (H + 2.0 ** -20)
+    da = 2 * (1.1 * dg * u.abs() + s.abs() * du) + a.abs() * (inner + 2.0 ** -20)
     out = mat(a, wd.T)
     dout = 2 * mat(da + LEAST, wd.abs().T) + LEAST + mat(a.abs(), wd.abs().T) * 2 * sum_bound(F) + out.abs() * H
     return dict(out=(out, dout), gate=(g, dg + g.abs() * H), up=(u, du + u.abs() * H))
 
 
-def backward(dout, x, wg, wu, wd, g, u):
-    """{name: (value, bound)} of the gradients, g and u the kept bf16 projections."""
+def backward(dout, x, wg, wu, wd, g, u, inner=H):
+    """{name: (value, bound)} of the gradients, g and u the kept bf16 projections; inner: what the roundings
+    of a, dG and dU may leave, relative."""
     T, d = x.shape
     F = wg.shape[0]
     g, u, x, dout = g.double(), u.double(), x.double(), dout.double()
@@ -54,9 +55,9 @@ def backward(dout, x, wg, wu, wd, g, u):
     # the factors in fp32: s within 8 ulps (1 - s absolutely, times g up to 88), then the rounding;
     # 1 + g (1 - s) may cancel, so its error counts against 1 + |g|
     dG, dU = dA * fg, dA * fu
-    eG = 2 * eA * fg.abs() + dG.abs() * H + 2 * dA.abs() * u.abs() * s * (1 + g.abs()) * 2.0 ** -19
-    eU = 2 * eA * fu.abs() + dU.abs() * H + 2 * dU.abs() * 2.0 ** -19
-    ea = a.abs() * (H + 2.0 ** -19)
+    eG = 2 * eA * fg.abs() + dG.abs() * inner + 2 * dA.abs() * u.abs() * s * (1 + g.abs()) * 2.0 ** -19
+    eU = 2 * eA * fu.abs() + dU.abs() * inner + 2 * dU.abs() * 2.0 ** -19
+    ea = a.abs() * (inner + 2.0 ** -19)
 
     def product(terms, K):
         v = sum(mat(p, q) for p, _, q in terms)

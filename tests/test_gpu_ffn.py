@@ -61,6 +61,37 @@ def test_backward(T, d, F):
     assert half.dx is None and torch.equal(half.dw_gate, got.dw_gate) and torch.equal(half.dw_down, got.dw_down)
 
 
+@pytest.mark.parametrize("T,d,F", [(1, 64, 64), (1, 4096, 8192), (2, 1032, 24576), (3, 512, 1000), (4, 2048, 10240)])
+def test_up_to_four_tokens_keep_the_inner_values(T, d, F):
+    """a stays fp32 there: no rounding of it.  (2, .., 24576) does not fit and rounds."""
+    x, (wg, wu, wd) = plain.bf16((T, d), 1.0, T).cuda(), weights(d, F)
+    want = plain_ffn.forward(x, wg, wu, wd, inner=2.0 ** -8 if F == 24576 else 0.0)
+    check(dict(out=moe.gated_ffn(x, wg, wu, wd)), want, (T, d, F))
+
+
+@pytest.mark.parametrize("T,d,F", [(1, 64, 64), (1, 1000, 520), (7, 4104, 136), (33, 136, 2056), (63, 512, 1000), (64, 1024, 512)])
+def test_backward_of_few_tokens_keeps_two_halves(T, d, F):
+    """a, dG and dU in two halves: the low one, at most 2^-8 of the value, is off by 2^-8 of itself."""
+    x, dout = plain.bf16((T, d), 1.0, T).cuda(), plain.bf16((T, d), 0.01, T + 1).cuda()
+    wg, wu, wd = weights(d, F)
+    gate, up = plain.bf16((T, F), 1.5, 7).cuda(), plain.bf16((T, F), 1.0, 8).cuda()
+    got = moe.gated_ffn_backward(dout, x, wg, wu, wd, gate, up)
+    check(got._asdict(), plain_ffn.backward(dout, x, wg, wu, wd, gate, up, inner=2.0 ** -16), (T, d, F))
+
+
+def test_halves_of_values_that_overflow():
+    """An inner gradient past bf16's range is infinite, as one rounded once is, and not NaN."""
+    T, d, F = 3, 64, 64
+    x, (wg, wu, wd) = plain.bf16((T, d), 1.0, 1).cuda().abs() + 1, weights(d, F)
+    big = torch.full((T, d), 2.0 ** 120, dtype=torch.bfloat16, device="cuda")
+    gate = torch.full((T, F), 2.0 ** 6, dtype=torch.bfloat16, device="cuda")  # silu(g) = g, its derivative 1
+    up = torch.full((T, F), 2.0 ** 6, dtype=torch.bfloat16, device="cuda")
+    wd = wd.abs() + 1  # dA above 2^126, dU and dG above 2^132
+    got = moe.gated_ffn_backward(big, x, wg.abs() + 1, wu.abs() + 1, wd, gate, up)
+    for t in got:  # dw_down: 3 2^120 2^12
+        assert (t == float("inf")).all()
+
+
 def test_backward_against_differences():
     """The gradient of L = sum(out * dout) along a direction, against L's difference in fp64."""
     T, d, F = 9, 64, 96
