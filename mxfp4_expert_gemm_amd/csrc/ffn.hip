@@ -12,6 +12,8 @@
 #include "mfma_stream.h"
 #include "tile_gemm.h"
 
+#include <algorithm>
+
 namespace moe {
 
 namespace {
@@ -43,7 +45,6 @@ struct EpiRows {
   int32_t N[2];
   float* part;
   using Held = NoHeld;
-  static constexpr bool JOINS = true;
   __device__ __forceinline__ Held hold(int, int) const { return {}; }
   __device__ __forceinline__ void put(int which, int m, int n, int, const Held&, const float (&v)[8]) const {
     uint16_t* o = which ? out[2] + (int64_t)m * N[1] : m < cut ? out[0] + (int64_t)m * N[0] : out[1] + (int64_t)(m - cut) * N[0];
@@ -55,8 +56,8 @@ struct EpiRows {
 struct EpiGlu {
   uint16_t *a, *gate, *up;
   int32_t F;
+  float* part;
   using Held = NoHeld;
-  static constexpr bool JOINS = false;
   __device__ __forceinline__ Held hold(int, int) const { return {}; }
   __device__ __forceinline__ void put(int, int m, int n, int, const Held&, const float (&g)[8], const float (&u)[8]) const {
     const int64_t at = (int64_t)m * F + n;
@@ -84,10 +85,10 @@ struct EpiGluBack {
   const uint16_t *gate, *up;
   uint16_t *a, *dgu;
   int32_t F, T;
+  float* part;
   struct Held {
     uint4 g, u;
   };
-  static constexpr bool JOINS = false;
   __device__ __forceinline__ Held hold(int m, int n) const {
     const int64_t at = (int64_t)m * F + n;
     return {*reinterpret_cast<const uint4*>(gate + at), *reinterpret_cast<const uint4*>(up + at)};
@@ -273,16 +274,27 @@ TileSize tile_size(int64_t M, int64_t N, bool row_major) {
 // K is split where the tiles of the output alone leave units idle: no more pieces than bring the
 // grid to a block a unit, of 8 K tiles at least, 16 at most (33 tokens, 7168 -> 3584, 56 tiles:
 // 23 us whole, 12.1 in two, 10.1 in four, 10.6 in eight).
-int splits_of(int64_t M, int64_t N, int64_t K, bool row_major) {
-  const TileSize z = tile_size(M, N, row_major);
-  if (z >= TILE_224) return 1;
-  const int64_t tiles = z == TILE_128 ? ceil_div(M, 128) * ceil_div(N, 128) : ceil_div(N, 64);
+int splits_of(int64_t tiles, int64_t K) {
   const int64_t most = K / 512, want = 256 / tiles, s = want < most ? want : most;
   return s < 1 ? 1 : s > 16 ? 16 : (int)s;
+}
+int64_t tiles_of(TileSize z, int64_t M, int64_t N) {
+  return z == TILE_128 ? ceil_div(M, 128) * ceil_div(N, 128) : ceil_div(N, 64);
+}
+int splits_of(int64_t M, int64_t N, int64_t K, bool row_major) {
+  const TileSize z = tile_size(M, N, row_major);
+  return z >= TILE_224 ? 1 : splits_of(tiles_of(z, M, N), K);
 }
 size_t part_bytes(int64_t M, int64_t N, int64_t K, bool row_major, int halves = 1) {
   const int s = splits_of(M, N, K, row_major);
   return s * halves > 1 ? (size_t)s * M * N * 4 : 0;
+}
+// of the weights' gradients, two products in one launch: one tile for both, by the three matrices'
+// area in rows of d
+TileSize weights_tile(int32_t d, int32_t F) { return tile_size(3 * (int64_t)F, d, true); }
+int weights_splits(int64_t T, int32_t d, int32_t F) {
+  const TileSize z = weights_tile(d, F);
+  return z >= TILE_224 ? 1 : splits_of(tiles_of(z, 2 * (int64_t)F, d) + tiles_of(z, d, F), T);
 }
 // Backward of few tokens: a, dG and dU are held in two halves of 8 bits each, since that is free there
 // (one tile of rows and of K takes both).  Of more tokens each is rounded once.
@@ -317,7 +329,10 @@ FfnLayout ffn_layout(int64_t T, int32_t d, int32_t F) {
   l.a = 0;
   l.part = l.a + align_up((size_t)T * F * (gemv_wide(T, d, F) ? 4 : 2), 256);
   l.dgu = 0;
-  l.total = l.part + align_up(part_bytes(T, d, F, false), 256);
+  // used one after another: pieces of g and u, and of out
+  const size_t glu = gemv_takes(T, d) ? 0 : part_bytes(T, 2 * (int64_t)F, d, false);
+  const size_t out = gemv_takes(T, F) ? 0 : part_bytes(T, d, F, false);
+  l.total = l.part + align_up(glu > out ? glu : out, 256);
   return l;
 }
 FfnLayout ffn_backward_layout(int64_t T, int32_t d, int32_t F) {
@@ -326,7 +341,12 @@ FfnLayout ffn_backward_layout(int64_t T, int32_t d, int32_t F) {
   l.a = 0;
   l.dgu = l.a + align_up((size_t)T * F * 2 * h, 256);
   l.part = l.dgu + align_up((size_t)T * F * 4 * h, 256);
-  l.total = l.part + align_up(part_bytes(h * T, d, 2 * (int64_t)F, true, h), 256);
+  // used one after another: pieces of dA, of dx, of the weights' gradients
+  const int sw = weights_splits(T, d, F);
+  size_t most = part_bytes(T, F, d, true);
+  most = std::max(most, part_bytes(h * T, d, 2 * (int64_t)F, true, h));
+  most = std::max(most, sw > 1 ? (size_t)sw * 3 * F * d * 4 : 0);
+  l.total = l.part + align_up(most, 256);
   return l;
 }
 
@@ -334,6 +354,7 @@ hipError_t launch_ffn(const FfnArgs& p, void* ws, hipStream_t st) {
   const FfnLayout l = ffn_layout(p.T, p.d, p.F);
   char* w = static_cast<char*>(ws);
   uint16_t* a = reinterpret_cast<uint16_t*>(w + l.a);
+  float* part = reinterpret_cast<float*>(w + l.part);
   const int32_t T = (int32_t)p.T;
   hipError_t err;
   TileArgs t{};
@@ -344,8 +365,10 @@ hipError_t launch_ffn(const FfnArgs& p, void* ws, hipStream_t st) {
     t.m = operand(p.x, p.d, T);
     t.n = operand(p.w_gate, p.d, p.F, p.w_up);
     t.K = p.d;
-    t.splits = t.halves = 1;
-    err = run_tiles<TILE_KMAJ, TILE_KMAJ, true>(tile_size(T, 2 * (int64_t)p.F, false), t, 1, EpiGlu{a, p.gate, p.up, p.F}, st);
+    t.splits = splits_of(T, 2 * (int64_t)p.F, p.d, false);
+    t.halves = 1;
+    err = run_tiles<TILE_KMAJ, TILE_KMAJ, true>(tile_size(T, 2 * (int64_t)p.F, false), t, 1,
+                                                EpiGlu{a, p.gate, p.up, p.F, part}, st);
   }
   if (err != hipSuccess) return err;
   if (gemv_takes(T, p.F)) return gemv<false>(GemvArgs{p.w_down, nullptr, a, p.out, nullptr, nullptr, T, p.F, p.d}, wide, st);
@@ -354,7 +377,7 @@ hipError_t launch_ffn(const FfnArgs& p, void* ws, hipStream_t st) {
   t.K = p.F;
   t.splits = splits_of(T, p.d, p.F, false);
   t.halves = 1;
-  const EpiRows e{{p.out, nullptr, nullptr}, T, {p.d, 0}, reinterpret_cast<float*>(w + l.part)};
+  const EpiRows e{{p.out, nullptr, nullptr}, T, {p.d, 0}, part};
   return run_tiles<TILE_KMAJ, TILE_KMAJ, false>(tile_size(T, p.d, false), t, 1, e, st);
 }
 
@@ -365,25 +388,27 @@ hipError_t launch_ffn_backward(const FfnBackArgs& p, void* ws, hipStream_t st) {
   char* w = static_cast<char*>(ws);
   uint16_t* a = reinterpret_cast<uint16_t*>(w + l.a);
   uint16_t* dgu = reinterpret_cast<uint16_t*>(w + l.dgu);
+  float* part = reinterpret_cast<float*>(w + l.part);
   const int32_t T = (int32_t)p.T;
   const int h = halves_of(T);
   TileArgs t{};
   t.m = operand(p.dout, p.d, T);
   t.n = operand(p.w_down, p.F, p.F);
   t.K = p.d;
-  t.splits = t.halves = 1;
+  t.splits = splits_of(T, p.F, p.d, true);
+  t.halves = 1;
   hipError_t err;
   if (h > 1)  // always tiles of 128
-    err = launch_tile_gemm<Tile128<TILE_KMAJ, TILE_RMAJ, false>>(t, 1, EpiGluBack<true>{p.gate, p.up, a, dgu, p.F, T}, st);
+    err = launch_tile_gemm<Tile128<TILE_KMAJ, TILE_RMAJ, false>>(t, 1, EpiGluBack<true>{p.gate, p.up, a, dgu, p.F, T, part}, st);
   else
-    err = run_tiles<TILE_KMAJ, TILE_RMAJ, false>(tile_size(T, p.F, true), t, 1, EpiGluBack<false>{p.gate, p.up, a, dgu, p.F, T}, st);
+    err = run_tiles<TILE_KMAJ, TILE_RMAJ, false>(tile_size(T, p.F, true), t, 1, EpiGluBack<false>{p.gate, p.up, a, dgu, p.F, T, part}, st);
   if (err == hipSuccess && p.dx) {
     t.m = operand(dgu, 2 * (int64_t)p.F, h * T, dgu + p.F);
     t.n = operand(p.w_gate, p.d, p.d, p.w_up);
     t.K = p.F;
     t.splits = splits_of(h * T, p.d, 2 * (int64_t)p.F, true);
     t.halves = h;
-    const EpiRows e{{p.dx, nullptr, nullptr}, T, {p.d, 0}, reinterpret_cast<float*>(w + l.part)};
+    const EpiRows e{{p.dx, nullptr, nullptr}, T, {p.d, 0}, part};
     err = run_tiles<TILE_KMAJ, TILE_RMAJ, false>(tile_size(h * T, p.d, true), t, 2, e, st);
   }
   if (err == hipSuccess && p.dw_gate) {
@@ -393,11 +418,12 @@ hipError_t launch_ffn_backward(const FfnBackArgs& p, void* ws, hipStream_t st) {
     u.m = operand(p.dout, p.d, p.d);
     u.n = operand(a, p.F, p.F, a + (int64_t)p.F * T);
     t.K = u.K = T;
-    t.splits = u.splits = t.halves = u.halves = 1;
+    t.splits = u.splits = weights_splits(T, p.d, p.F);
+    t.halves = u.halves = 1;
     u.which = 1;
-    const EpiRows e{{p.dw_gate, p.dw_up, p.dw_down}, p.F, {p.d, p.F}, nullptr};
-    // one tile for both: by the three matrices' area in rows of d
-    err = run_tiles<TILE_RMAJ, TILE_RMAJ, false>(tile_size(3 * (int64_t)p.F, p.d, true), t, h, e, st, &u);
+    u.part = (int64_t)t.splits * 2 * p.F * p.d;
+    const EpiRows e{{p.dw_gate, p.dw_up, p.dw_down}, p.F, {p.d, p.F}, part};
+    err = run_tiles<TILE_RMAJ, TILE_RMAJ, false>(weights_tile(p.d, p.F), t, h, e, st, &u);
   }
   return err;
 }

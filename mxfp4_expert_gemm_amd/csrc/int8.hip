@@ -16,7 +16,6 @@ struct EpiInt8 {
   int32_t N;
   int32_t* part;
   struct Held {};
-  static constexpr bool JOINS = true;
   __device__ __forceinline__ Held hold(int, int) const { return {}; }
   __device__ __forceinline__ void put(int, int m, int n, int left, const Held&, const int32_t (&v)[8]) const {
     const float s = xs[m];
@@ -143,6 +142,7 @@ hipError_t launch_linear_int8(const int8_t* q, const float* xs, const int8_t* W,
   a.K = n_in;
   a.splits = int8_splits(T, n_out, n_in);
   a.halves = 1;
+  a.part = 0;
   const EpiInt8 e{xs, ws, out, n_out, part};
   constexpr int KM = TILE_KMAJ;
   switch (int8_tile(T, n_out)) {

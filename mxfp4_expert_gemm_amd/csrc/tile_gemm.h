@@ -56,6 +56,7 @@ struct TileArgs {
   int32_t splits;  // the K tiles are dealt to so many blocks; tile_join adds their results
   int32_t halves;  // 2: the second half of M's rows are the low bits of the first's; tile_join adds their results
   int32_t which;   // told to the epilogue: of two products in one launch, whose results these are
+  int64_t part;    // where in the epilogue's part the product's pieces begin
   // set by the launcher
   int32_t nk;        // K tiles of a segment
   int32_t nkt;       // K tiles in all (nk, or 2 nk)
@@ -152,8 +153,10 @@ struct TileCfg {
   using ML = TileLoader<MORD, BM, NW, false>;
   using NL = TileLoader<NORD, BN, NW, GLU>;
   static constexpr int SLOT = ML::BYTES > NL::BYTES ? ML::BYTES : NL::BYTES, LDS = R * SLOT;
-  // one wave a SIMD where the accumulators need it
+  // One wave a SIMD where the accumulators need it.  The others' products may be split: those tiles
+  // are taken where there are enough of them.
   static constexpr int WAVES = MI * NJ > 32 ? 1 : 2;
+  static constexpr bool JOINS = WAVES == 2;
   // Few-token tiles stream their weights, all blocks at one pace: where rows are multiples of 4 KB
   // apart they would all ask the same memory channels at once, so there each block begins elsewhere
   // in K (one token, 8192 -> 7168: 22.5 us from 26; 7168 -> 8192, rows of 14 KB: 42.5 from 40.8).
@@ -203,8 +206,8 @@ __device__ __forceinline__ void tile_settle(Acc (&acc)[C::MI][C::NJ]) {
 //   Held hold(m, n)                   reads that, ahead of the results
 //   void put(which, m, n, left, held, v)       eight results (left: columns from n on that exist), or with GLU
 //   void put(which, m, n, left, held, v, w)    eight of each matrix
-// and, where JOINS, for products whose K is split (tile_join adds the pieces and calls put with the sums),
-//   Value* part                       [splits][rows of M][rows of N rounded up to 8]
+//   Value* part                       pieces of products whose K is split, which tile_join adds and calls
+//                                     put with: [splits][rows of M][rows of N rounded up to 8], GLU [splits][2]..
 template <class C, class Epi>
 __global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArgs p0, TileArgs p1, Epi epi) {
   constexpr int MI = C::MI, NJ = C::NJ, R = C::R, H = (R - 1) / 2, BM = C::BM, BN = C::BN;
@@ -227,6 +230,7 @@ __global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArg
   NL nl;
   struct Place {  // of a tile of results
     int which, m0, n0, split, joins, tile, rows_m, rows_n;
+    int64_t part;
   } at;
   int full, part, k0, nkt, turn = 0;
   auto start = [&](int lb) {
@@ -240,7 +244,7 @@ __global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArg
     const int gs = p.ntm - from < GROUP ? p.ntm - from : GROUP;
     const int within = tile - grp * span;
     const int m0 = (from + within % gs) * BM, n0 = (within / gs) * C::OUT_N;
-    at = Place{p.which, m0, n0, split, p.splits * p.halves, tile, p.m.rows, p.n.rows};
+    at = Place{p.which, m0, n0, split, p.splits * p.halves, tile, p.m.rows, p.n.rows, p.part};
     full = (int)(p.K / C::BK);
     part = full == p.nk ? 0 : p.nkt / p.nk;
     k0 = (int)((int64_t)p.nkt * split / p.splits);
@@ -373,13 +377,12 @@ __global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArg
     return next;
   };
 
-  // one piece of a split K
-  auto store_part = [&](const Place& e, int m, int n, const Value (&v)[8]) {
-    if constexpr (Epi::JOINS) {
-      Value* q = epi.part + ((int64_t)e.split * e.rows_m + m) * ((e.rows_n + 7) & ~7) + n;
+  // one piece of a split K (GLU: of matrix `second`)
+  auto store_part = [&](const Place& e, int second, int m, int n, const Value (&v)[8]) {
+    const int64_t row = ((int64_t)e.split * (C::GLU ? 2 : 1) + second) * e.rows_m + m;
+    Value* q = epi.part + e.part + row * ((e.rows_n + 7) & ~7) + n;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) *reinterpret_cast<Acc*>(q + 4 * h) = Acc{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
-    }
+    for (int h = 0; h < 2; ++h) *reinterpret_cast<Acc*>(q + 4 * h) = Acc{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
   };
 
   // Sixteen rows of the wave's results at a time through its part of the last slot (which the first
@@ -432,13 +435,15 @@ __global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArg
         Value v[8], w[8];
         eight(8 * piece, v);
         if constexpr (C::GLU) eight(8 * NJ + 8 * piece, w);
-        if (in) {
+        if (!in) continue;
+        if (!C::JOINS || e.joins == 1) {
           if constexpr (C::GLU)
             epi.put(e.which, m, n, e.rows_n - n, held[i & 1][s], v, w);
-          else if (!Epi::JOINS || e.joins == 1)
-            epi.put(e.which, m, n, e.rows_n - n, held[i & 1][s], v);
           else
-            store_part(e, m, n, v);
+            epi.put(e.which, m, n, e.rows_n - n, held[i & 1][s], v);
+        } else {
+          store_part(e, 0, m, n, v);
+          if constexpr (C::GLU) store_part(e, 1, m, n, w);
         }
       }
       __builtin_amdgcn_wave_barrier();
@@ -487,24 +492,43 @@ inline bool tiles_of_224(int64_t M, int64_t N) {
 }
 
 // The sums of the pieces of a split K, added in their order (the same call gives the same bits).  A
-// launch of its own, 4 us: joined by whichever block of a tile comes last, the pieces had to pass the
+// launch of its own, 2 to 4 us: joined by whichever block of a tile comes last, the pieces had to pass the
 // XCDs' own caches and one unit read all of a tile's (33 tokens, 7168 -> 3584: 20.4 us in all, 10.1 + 4 so).
-template <class Value, class Epi>
-__global__ void __launch_bounds__(256) tile_join_kernel(int64_t pieces, int32_t M, int32_t N, int splits, Epi epi) {
-  const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (x >= pieces) return;
+struct TileJoin {  // of one product
+  int64_t pieces, part;  // eight results each
+  int32_t N, parts, which;
+};
+template <class Value, bool GLU, class Epi>
+__global__ void __launch_bounds__(256) tile_join_kernel(TileJoin p0, TileJoin p1, Epi epi) {
+  int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const bool second = x >= p0.pieces;
+  const TileJoin p = second ? p1 : p0;
+  if (second) x -= p0.pieces;
+  if (x >= p.pieces) return;
   typedef Value V4 __attribute__((ext_vector_type(4)));
-  const int32_t row = (N + 7) / 8;
+  constexpr int G = GLU ? 2 : 1;
+  const int32_t row = (p.N + 7) / 8;
   const int m = (int)(x / row), n = 8 * (int)(x - (int64_t)m * row);
-  V4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
+  V4 a[2 * G];
+#pragma unroll
+  for (int i = 0; i < 2 * G; ++i) a[i] = V4{0, 0, 0, 0};
 #pragma unroll 4
-  for (int s = 0; s < splits; ++s) {
-    const V4* q = reinterpret_cast<const V4*>(epi.part + ((int64_t)s * pieces + x) * 8);
-    a += q[0];
-    b += q[1];
-  }
-  const Value v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-  epi.put(0, m, n, N - n, epi.hold(m, n), v);
+  for (int s = 0; s < p.parts; ++s)
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      const V4* q = reinterpret_cast<const V4*>(epi.part + p.part + ((int64_t)(s * G + i) * p.pieces + x) * 8);
+      a[2 * i] += q[0];
+      a[2 * i + 1] += q[1];
+    }
+  Value v[G][8];
+#pragma unroll
+  for (int i = 0; i < G; ++i)
+#pragma unroll
+    for (int r = 0; r < 8; ++r) v[i][r] = a[2 * i + r / 4][r % 4];
+  if constexpr (GLU)
+    epi.put(p.which, m, n, p.N - n, epi.hold(m, n), v[0], v[1]);
+  else
+    epi.put(p.which, m, n, p.N - n, epi.hold(m, n), v[0]);
 }
 
 // the K tiles and tiles of results of one product
@@ -516,7 +540,8 @@ bool tile_plan(TileArgs& a, int segs) {
   a.nkt = a.nk * segs;
   const int64_t nb = (int64_t)a.ntm * a.ntn * a.splits;
   a.nblocks = (int32_t)nb;
-  return a.splits >= 1 && a.splits <= a.nkt && nb <= 0x3FFFFFF0;
+  return a.splits >= 1 && a.splits <= a.nkt && nb <= 0x3FFFFFF0 && a.m.rows % a.halves == 0 &&
+         (C::JOINS || a.splits * a.halves == 1);
 }
 // One product, or two in one launch (of as many K segments each).
 template <class C, class Epi>
@@ -532,15 +557,16 @@ hipError_t launch_tile_gemm(TileArgs a, int segs, const Epi& epi, hipStream_t st
     if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL((tile_gemm_kernel<C, Epi>), dim3(grid), dim3(C::NW * 64), C::LDS, st, a, b, epi);
-  if constexpr (Epi::JOINS) {
-    if (a.splits * a.halves > 1) {
-      if (second || a.m.rows % a.halves) return hipErrorInvalidValue;
-      using Value = std::conditional_t<C::I8, int32_t, float>;
-      const int32_t rows = a.m.rows / a.halves;  // a piece of all of M's rows is one of each half
-      const int64_t pieces = (int64_t)rows * ceil_div(a.n.rows, 8);
-      hipLaunchKernelGGL((tile_join_kernel<Value, Epi>), dim3((unsigned)ceil_div(pieces, 256)), dim3(256), 0, st, pieces,
-                         rows, a.n.rows, a.splits * a.halves, epi);
-    }
+  if constexpr (C::JOINS) {
+    using Value = std::conditional_t<C::I8, int32_t, float>;
+    auto join = [](const TileArgs& p) {  // a piece of all of M's rows is one of each half
+      if (p.nblocks == 0 || p.splits * p.halves == 1) return TileJoin{};
+      return TileJoin{(int64_t)(p.m.rows / p.halves) * ceil_div(p.n.rows, 8), p.part, p.n.rows, p.splits * p.halves, p.which};
+    };
+    const TileJoin ja = join(a), jb = join(b);
+    if (ja.pieces + jb.pieces > 0)
+      hipLaunchKernelGGL((tile_join_kernel<Value, C::GLU, Epi>), dim3((unsigned)ceil_div(ja.pieces + jb.pieces, 256)),
+                         dim3(256), 0, st, ja, jb, epi);
   }
   return hipGetLastError();
 }
