@@ -262,28 +262,10 @@ bool gemv_takes(int64_t T, int32_t K, int value_bytes = 2) {
 // would bind on the LDS.
 bool gemv_wide(int64_t T, int32_t d, int32_t F) { return T <= 4 && gemv_takes(T, d) && gemv_takes(T, F, 4); }
 
-// Tiles by the rows of M: few tokens take 16, 32, 48 or 64 rows by 64 columns in blocks of two
-// waves, two blocks a unit, with a deep ring; then 128 x 128, two blocks a unit; and 256 x 256 (or
-// 224) where those fill three quarters of the units.
-enum TileSize { TILE_16, TILE_32, TILE_48, TILE_64, TILE_128, TILE_224, TILE_256 };
-TileSize tile_size(int64_t M, int64_t N, bool row_major) {
-  if (ceil_div(M, 256) * ceil_div(N, 256) >= 192) return tiles_of_224(M, N) ? TILE_224 : TILE_256;
-  if (M > 64 || row_major) return TILE_128;
-  return (TileSize)((M - 1) / 16);
-}
-// K is split where the tiles of the output alone leave units idle: no more pieces than bring the
-// grid to a block a unit, of 8 K tiles at least, 16 at most (33 tokens, 7168 -> 3584, 56 tiles:
-// 23 us whole, 12.1 in two, 10.1 in four, 10.6 in eight).
-int splits_of(int64_t tiles, int64_t K) {
-  const int64_t most = K / 512, want = 256 / tiles, s = want < most ? want : most;
-  return s < 1 ? 1 : s > 16 ? 16 : (int)s;
-}
-int64_t tiles_of(TileSize z, int64_t M, int64_t N) {
-  return z == TILE_128 ? ceil_div(M, 128) * ceil_div(N, 128) : ceil_div(N, 64);
-}
+int64_t k_tiles(int64_t K) { return ceil_div(K, 64); }
 int splits_of(int64_t M, int64_t N, int64_t K, bool row_major) {
-  const TileSize z = tile_size(M, N, row_major);
-  return z >= TILE_224 ? 1 : splits_of(tiles_of(z, M, N), K);
+  const TileSize z = tile_size(M, N, k_tiles(K), row_major);
+  return tile_splits(z, tiles_of(z, M, N), K / 64);
 }
 size_t part_bytes(int64_t M, int64_t N, int64_t K, bool row_major, int halves = 1) {
   const int s = splits_of(M, N, K, row_major);
@@ -291,33 +273,15 @@ size_t part_bytes(int64_t M, int64_t N, int64_t K, bool row_major, int halves = 
 }
 // of the weights' gradients, two products in one launch: one tile for both, by the three matrices'
 // area in rows of d
-TileSize weights_tile(int32_t d, int32_t F) { return tile_size(3 * (int64_t)F, d, true); }
+TileSize weights_tile(int64_t T, int32_t d, int32_t F) { return tile_size(3 * (int64_t)F, d, k_tiles(T), true); }
 int weights_splits(int64_t T, int32_t d, int32_t F) {
-  const TileSize z = weights_tile(d, F);
-  return z >= TILE_224 ? 1 : splits_of(tiles_of(z, 2 * (int64_t)F, d) + tiles_of(z, d, F), T);
+  const TileSize z = weights_tile(T, d, F);
+  return tile_splits(z, tiles_of(z, 2 * (int64_t)F, d) + tiles_of(z, d, F), T / 64);
 }
 // Backward of few tokens: a, dG and dU are held in two halves of 8 bits each, since that is free there
 // (one tile of rows and of K takes both).  Of more tokens each is rounded once.
 constexpr int64_t HALVES_TOKENS = 64;
 int halves_of(int64_t T) { return T <= HALVES_TOKENS ? 2 : 1; }
-template <int MO, int NO, bool GLU>
-using Tile128 = TileCfg<4, 4, 2, 2, 5, MO, NO, GLU>;
-template <int MO, int NO, bool GLU, class Epi>
-hipError_t run_tiles(TileSize z, const TileArgs& a, int segs, const Epi& e, hipStream_t st, const TileArgs* b = nullptr) {
-  if (z == TILE_256) return launch_tile_gemm<TileCfg<8, 8, 2, 2, 5, MO, NO, GLU>>(a, segs, e, st, b);
-  if (z == TILE_224) return launch_tile_gemm<TileCfg<8, 7, 2, 2, 5, MO, NO, GLU>>(a, segs, e, st, b);
-  if constexpr (MO == TILE_KMAJ && NO == TILE_KMAJ) {
-    switch (z) {
-      case TILE_16: return launch_tile_gemm<TileCfg<1, 2, 1, 2, 9, MO, NO, GLU>>(a, segs, e, st, b);
-      case TILE_32: return launch_tile_gemm<TileCfg<2, 2, 1, 2, 9, MO, NO, GLU>>(a, segs, e, st, b);
-      case TILE_48: return launch_tile_gemm<TileCfg<3, 2, 1, 2, 9, MO, NO, GLU>>(a, segs, e, st, b);
-      case TILE_64: return launch_tile_gemm<TileCfg<4, 2, 1, 2, 9, MO, NO, GLU>>(a, segs, e, st, b);
-      default: break;
-    }
-  }
-  return launch_tile_gemm<Tile128<MO, NO, GLU>>(a, segs, e, st, b);
-}
-
 TileOperand operand(const void* p, int64_t ld_values, int32_t rows, const void* p1 = nullptr) {
   return TileOperand{{p, p1 ? p1 : p}, ld_values * 2, rows};
 }
@@ -367,7 +331,7 @@ hipError_t launch_ffn(const FfnArgs& p, void* ws, hipStream_t st) {
     t.K = p.d;
     t.splits = splits_of(T, 2 * (int64_t)p.F, p.d, false);
     t.halves = 1;
-    err = run_tiles<TILE_KMAJ, TILE_KMAJ, true>(tile_size(T, 2 * (int64_t)p.F, false), t, 1,
+    err = run_tiles<TILE_KMAJ, TILE_KMAJ, true, false>(tile_size(T, 2 * (int64_t)p.F, k_tiles(p.d), false), t, 1,
                                                 EpiGlu{a, p.gate, p.up, p.F, part}, st);
   }
   if (err != hipSuccess) return err;
@@ -378,7 +342,7 @@ hipError_t launch_ffn(const FfnArgs& p, void* ws, hipStream_t st) {
   t.splits = splits_of(T, p.d, p.F, false);
   t.halves = 1;
   const EpiRows e{{p.out, nullptr, nullptr}, T, {p.d, 0}, part};
-  return run_tiles<TILE_KMAJ, TILE_KMAJ, false>(tile_size(T, p.d, false), t, 1, e, st);
+  return run_tiles<TILE_KMAJ, TILE_KMAJ, false, false>(tile_size(T, p.d, k_tiles(p.F), false), t, 1, e, st);
 }
 
 // Three launches, and a join where dx's K is split: dA with a, dG and dU; dx, whose K is dG's and then dU's; and the weights' gradients,
@@ -398,10 +362,11 @@ hipError_t launch_ffn_backward(const FfnBackArgs& p, void* ws, hipStream_t st) {
   t.splits = splits_of(T, p.F, p.d, true);
   t.halves = 1;
   hipError_t err;
-  if (h > 1)  // always tiles of 128
-    err = launch_tile_gemm<Tile128<TILE_KMAJ, TILE_RMAJ, false>>(t, 1, EpiGluBack<true>{p.gate, p.up, a, dgu, p.F, T, part}, st);
+  const TileSize z = tile_size(T, p.F, k_tiles(p.d), true);
+  if (h > 1)  // never the large tiles
+    err = run_middle_tiles<TILE_KMAJ, TILE_RMAJ, false, false>(z, t, 1, EpiGluBack<true>{p.gate, p.up, a, dgu, p.F, T, part}, st);
   else
-    err = run_tiles<TILE_KMAJ, TILE_RMAJ, false>(tile_size(T, p.F, true), t, 1, EpiGluBack<false>{p.gate, p.up, a, dgu, p.F, T, part}, st);
+    err = run_tiles<TILE_KMAJ, TILE_RMAJ, false, false>(z, t, 1, EpiGluBack<false>{p.gate, p.up, a, dgu, p.F, T, part}, st);
   if (err == hipSuccess && p.dx) {
     t.m = operand(dgu, 2 * (int64_t)p.F, h * T, dgu + p.F);
     t.n = operand(p.w_gate, p.d, p.d, p.w_up);
@@ -409,7 +374,7 @@ hipError_t launch_ffn_backward(const FfnBackArgs& p, void* ws, hipStream_t st) {
     t.splits = splits_of(h * T, p.d, 2 * (int64_t)p.F, true);
     t.halves = h;
     const EpiRows e{{p.dx, nullptr, nullptr}, T, {p.d, 0}, part};
-    err = run_tiles<TILE_KMAJ, TILE_RMAJ, false>(tile_size(h * T, p.d, true), t, 2, e, st);
+    err = run_tiles<TILE_KMAJ, TILE_RMAJ, false, false>(tile_size(h * T, p.d, k_tiles(2 * (int64_t)p.F), true), t, 2, e, st);
   }
   if (err == hipSuccess && p.dw_gate) {
     TileArgs u{};
@@ -423,7 +388,7 @@ hipError_t launch_ffn_backward(const FfnBackArgs& p, void* ws, hipStream_t st) {
     u.which = 1;
     u.part = (int64_t)t.splits * 2 * p.F * p.d;
     const EpiRows e{{p.dw_gate, p.dw_up, p.dw_down}, p.F, {p.d, p.F}, part};
-    err = run_tiles<TILE_RMAJ, TILE_RMAJ, false>(weights_tile(p.d, p.F), t, h, e, st, &u);
+    err = run_tiles<TILE_RMAJ, TILE_RMAJ, false, false>(weights_tile(T, p.d, p.F), t, h, e, st, &u);
   }
   return err;
 }

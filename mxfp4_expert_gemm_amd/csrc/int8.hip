@@ -10,6 +10,9 @@ namespace moe {
 
 namespace {
 
+// 16 bytes at any even address: rows of odd widths lie so
+typedef uint32_t any_u32x4_t __attribute__((ext_vector_type(4), aligned(2)));
+
 struct EpiInt8 {
   const float *xs, *ws;
   uint16_t* out;
@@ -20,7 +23,7 @@ struct EpiInt8 {
   __device__ __forceinline__ void put(int, int m, int n, int left, const Held&, const int32_t (&v)[8]) const {
     const float s = xs[m];
     uint16_t* o = out + (int64_t)m * N + n;
-    if (left >= 8 && N % 8 == 0) {
+    if (left >= 8) {
       const float4 a = *reinterpret_cast<const float4*>(ws + n), b = *reinterpret_cast<const float4*>(ws + n + 4);
       const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
       uint32_t d[4];
@@ -29,7 +32,7 @@ struct EpiInt8 {
         const bf16x2_t c = {(__bf16)((float)v[2 * r] * s * w[2 * r]), (__bf16)((float)v[2 * r + 1] * s * w[2 * r + 1])};
         d[r] = __builtin_bit_cast(uint32_t, c);
       }
-      *reinterpret_cast<uint4*>(o) = make_uint4(d[0], d[1], d[2], d[3]);
+      *reinterpret_cast<any_u32x4_t*>(o) = any_u32x4_t{d[0], d[1], d[2], d[3]};
     } else {
 #pragma unroll
       for (int r = 0; r < 8; ++r)
@@ -104,18 +107,9 @@ __global__ void __launch_bounds__(256) quantize_int8_kernel(const uint16_t* __re
   for (int col = 8 * (threadIdx.x + 256 * C); col < n; col += 8 * 256) write(*reinterpret_cast<const uint4*>(row + col), col);
 }
 
-// the tiles of ffn.hip, by the same rules
-enum Int8Tile { I8_16, I8_32, I8_48, I8_64, I8_128, I8_224, I8_256 };
-Int8Tile int8_tile(int64_t M, int64_t N) {
-  if (ceil_div(M, 256) * ceil_div(N, 256) >= 192) return tiles_of_224(M, N) ? I8_224 : I8_256;
-  return M > 64 ? I8_128 : (Int8Tile)((M - 1) / 16);
-}
 int int8_splits(int64_t M, int64_t N, int64_t K) {
-  const Int8Tile z = int8_tile(M, N);
-  if (z >= I8_224) return 1;
-  const int64_t tiles = z == I8_128 ? ceil_div(M, 128) * ceil_div(N, 128) : ceil_div(N, 64);
-  const int64_t most = K / 1024, want = 256 / tiles, s = want < most ? want : most;
-  return s < 1 ? 1 : s > 16 ? 16 : (int)s;
+  const TileSize z = tile_size(M, N, ceil_div(K, 128), false);
+  return tile_splits(z, tiles_of(z, M, N), K / 128);
 }
 
 }  // namespace
@@ -144,16 +138,7 @@ hipError_t launch_linear_int8(const int8_t* q, const float* xs, const int8_t* W,
   a.halves = 1;
   a.part = 0;
   const EpiInt8 e{xs, ws, out, n_out, part};
-  constexpr int KM = TILE_KMAJ;
-  switch (int8_tile(T, n_out)) {
-    case I8_256: return launch_tile_gemm<TileCfg<8, 8, 2, 2, 5, KM, KM, false, true>>(a, 1, e, st);
-    case I8_224: return launch_tile_gemm<TileCfg<8, 7, 2, 2, 5, KM, KM, false, true>>(a, 1, e, st);
-    case I8_128: return launch_tile_gemm<TileCfg<4, 4, 2, 2, 5, KM, KM, false, true>>(a, 1, e, st);
-    case I8_64: return launch_tile_gemm<TileCfg<4, 2, 1, 2, 9, KM, KM, false, true>>(a, 1, e, st);
-    case I8_48: return launch_tile_gemm<TileCfg<3, 2, 1, 2, 9, KM, KM, false, true>>(a, 1, e, st);
-    case I8_32: return launch_tile_gemm<TileCfg<2, 2, 1, 2, 9, KM, KM, false, true>>(a, 1, e, st);
-    default: return launch_tile_gemm<TileCfg<1, 2, 1, 2, 9, KM, KM, false, true>>(a, 1, e, st);
-  }
+  return run_tiles<TILE_KMAJ, TILE_KMAJ, false, true>(tile_size(T, n_out, ceil_div(n_in, 128), false), a, 1, e, st);
 }
 
 }  // namespace moe

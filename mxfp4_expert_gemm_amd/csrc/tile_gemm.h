@@ -571,4 +571,49 @@ hipError_t launch_tile_gemm(TileArgs a, int segs, const Epi& epi, hipStream_t st
   return hipGetLastError();
 }
 
+// Tiles by the rows of M: few tokens take 16, 32, 48 or 64 rows by 64 columns in blocks of two
+// waves, two blocks a unit, with a deep ring; 256 x 256 (or 224) where those fill three quarters of
+// the units; between them 128 x 128, two blocks a unit, or where those leave units idle and K is
+// short, so that beginning and ending count and not the stream, 64 x 64 (77 tokens, 512 and 1000 wide:
+// forward 14.5 us from 20.2, backward 24 from 31; 512 tokens, 1024 -> 1024: forward 18.5 from 27.5.
+// With a longer K they lose: 100 tokens, 4096 -> 4096 46 from 36.8).
+enum TileSize { TILE_16, TILE_32, TILE_48, TILE_64, TILE_SQUARE_64, TILE_128, TILE_224, TILE_256 };
+inline TileSize tile_size(int64_t M, int64_t N, int64_t k_tiles, bool row_major) {
+  if (ceil_div(M, 256) * ceil_div(N, 256) >= 192) return tiles_of_224(M, N) ? TILE_224 : TILE_256;
+  if (M <= 64 && !row_major) return (TileSize)((M - 1) / 16);
+  return ceil_div(M, 128) * ceil_div(N, 128) <= 128 && k_tiles <= 32 ? TILE_SQUARE_64 : TILE_128;
+}
+inline int64_t tiles_of(TileSize z, int64_t M, int64_t N) {
+  const int64_t m = z == TILE_128 ? 128 : 64, n = z == TILE_128 ? 128 : 64;
+  return ceil_div(M, m) * ceil_div(N, n);
+}
+// K is split where the tiles of the output alone leave units idle: no more pieces than bring the
+// grid to a block a unit, of 8 K tiles at least, 16 at most (33 tokens, 7168 -> 3584, 56 tiles:
+// 23 us whole, 12.1 in two, 10.1 in four, 10.6 in eight).
+inline int tile_splits(TileSize z, int64_t tiles, int64_t k_tiles) {
+  if (z >= TILE_224) return 1;
+  const int64_t most = k_tiles / 8, want = 256 / tiles, s = want < most ? want : most;
+  return s < 1 ? 1 : s > 16 ? 16 : (int)s;
+}
+template <int MO, int NO, bool GLU, bool I8, class Epi>
+hipError_t run_middle_tiles(TileSize z, const TileArgs& a, int segs, const Epi& e, hipStream_t st, const TileArgs* b = nullptr) {
+  if (z == TILE_SQUARE_64) return launch_tile_gemm<TileCfg<2, 2, 2, 2, 5, MO, NO, GLU, I8>>(a, segs, e, st, b);
+  return launch_tile_gemm<TileCfg<4, 4, 2, 2, 5, MO, NO, GLU, I8>>(a, segs, e, st, b);
+}
+template <int MO, int NO, bool GLU, bool I8, class Epi>
+hipError_t run_tiles(TileSize z, const TileArgs& a, int segs, const Epi& e, hipStream_t st, const TileArgs* b = nullptr) {
+  if (z == TILE_256) return launch_tile_gemm<TileCfg<8, 8, 2, 2, 5, MO, NO, GLU, I8>>(a, segs, e, st, b);
+  if (z == TILE_224) return launch_tile_gemm<TileCfg<8, 7, 2, 2, 5, MO, NO, GLU, I8>>(a, segs, e, st, b);
+  if constexpr (MO == TILE_KMAJ && NO == TILE_KMAJ) {
+    switch (z) {
+      case TILE_16: return launch_tile_gemm<TileCfg<1, 2, 1, 2, 9, MO, NO, GLU, I8>>(a, segs, e, st, b);
+      case TILE_32: return launch_tile_gemm<TileCfg<2, 2, 1, 2, 9, MO, NO, GLU, I8>>(a, segs, e, st, b);
+      case TILE_48: return launch_tile_gemm<TileCfg<3, 2, 1, 2, 9, MO, NO, GLU, I8>>(a, segs, e, st, b);
+      case TILE_64: return launch_tile_gemm<TileCfg<4, 2, 1, 2, 9, MO, NO, GLU, I8>>(a, segs, e, st, b);
+      default: break;
+    }
+  }
+  return run_middle_tiles<MO, NO, GLU, I8>(z, a, segs, e, st, b);
+}
+
 }  // namespace moe

@@ -29,7 +29,7 @@ def check(got, want, what):
 FORWARD = [(1, 8, 8), (1, 256, 344), (1, 7168, 2048), (2, 4096, 512), (3, 72, 1000), (5, 256, 344), (8, 1024, 4096), (9, 512, 512),
            (15, 264, 120), (16, 64, 64), (17, 2048, 1032), (31, 1000, 88), (33, 3584, 7168), (64, 512, 2048), (65, 320, 640),
            (127, 136, 4104), (128, 1024, 1024), (200, 2056, 96), (513, 512, 1528), (1021, 1032, 2056),
-           (20, 7168, 512), (64, 1032, 72), (130, 4096, 264),
+           (20, 7168, 512), (64, 1032, 72), (130, 4096, 264), (200, 2048, 1928),
            (2048, 520, 8200), (4096, 4096, 1024), (3600, 7168, 3600)]  # the last: tiles of 224 columns, cut
 
 
@@ -46,7 +46,7 @@ def test_forward(T, d, F):
 
 
 BACKWARD = [(1, 8, 8), (1, 512, 264), (5, 64, 128), (33, 136, 72), (77, 512, 1000), (128, 128, 128), (129, 1032, 520),
-            (11, 3952, 72), (65, 2056, 264), (300, 256, 2056), (1021, 640, 1528), (3001, 72, 136), (5000, 344, 520),
+            (11, 3952, 72), (65, 2056, 264), (100, 1928, 1000), (300, 256, 2056), (1021, 640, 1528), (3001, 72, 136), (5000, 344, 520),
              (2048, 2048, 2048), (4100, 264, 4104), (1000, 4096, 4096), (3900, 3592, 7176)]
 
 

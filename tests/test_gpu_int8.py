@@ -58,7 +58,7 @@ def test_rows_that_are_not_finite():
 # that are no multiple of anything, splits of the inner width, the large tiles
 CASES = [(1, 16, 1), (1, 7168, 3584), (5, 64, 33), (16, 3584, 7168), (32, 208, 130), (33, 4096, 1000), (48, 7168, 3584),
          (64, 1040, 65), (65, 128, 127), (100, 8192, 96), (257, 3584, 515), (1000, 2048, 2049), (1021, 7168, 320),
-         (4096, 272, 4100), (3001, 3584, 7168)]
+         (300, 4096, 264), (4096, 272, 4100), (3001, 3584, 7168)]
 
 
 @pytest.mark.parametrize("T,n_in,n_out", CASES)
