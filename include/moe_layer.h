@@ -468,7 +468,8 @@ moe_status moe_layer_decode(const void* x, const void* router_w, const void* lat
  * an expert in bf16 while it is trained:
  *   g = x w_gate^T, u = x w_up^T,  a = bf16(silu(g) u),  out = bf16(a w_down^T)
  * with x [T][d], w_gate and w_up [F][d], w_down [d][F], out [T][d], all bf16; g, u and every sum
- * fp32, silu in fp32.  gate and up (both or neither): [T][F], receive bf16(g) and bf16(u), which
+ * fp32, silu in fp32 (of up to four tokens a stays fp32 too, where the widths leave room for it in
+ * the kernel).  gate and up (both or neither): [T][F], receive bf16(g) and bf16(u), which
  * the backward pass reads.  d and F multiples of 8, at most 32768; T up to 2^24.  Every pointer
  * 16-byte aligned; outputs and workspace overlap nothing.  Sums are joined in a fixed order: the
  * same call gives the same bits. */
@@ -481,7 +482,8 @@ moe_status moe_gated_ffn(const void* x, const void* w_gate, const void* w_up, co
  * the gate and up that the forward pass gave.  With s = 1 / (1 + e^-g) and dA = dout w_down:
  *   a = bf16(g s u), dU = bf16(dA g s), dG = bf16(dA u s (1 + g (1 - s))),
  *   dx = bf16(dG w_gate + dU w_up), dw_gate = bf16(dG^T x), dw_up = bf16(dU^T x), dw_down = bf16(dout^T a)
- * each shaped like what it is the gradient of, sums in fp32.  dx may be NULL, and dw_gate, dw_up
+ * each shaped like what it is the gradient of, sums in fp32 (of up to 64 tokens a, dG and dU keep
+ * 16 bits each and not 8).  dx may be NULL, and dw_gate, dw_up
  * and dw_down together may be NULL: what is not asked for is not computed.  num_tokens 0 leaves dx
  * empty and sets the weights' gradients to zero. */
 moe_status moe_gated_ffn_backward_workspace_size(int64_t num_tokens, int32_t d_model, int32_t d_ffn, size_t* bytes);

@@ -11,6 +11,9 @@
 // Bound: HBM.  A row is held in registers from its first load on, so each tensor is read and
 // written once: 8 bytes an element forward, 12 backward, 2 and 4 more with a gate of each token.
 // A row belongs to one wave, or to four or eight where it is long.  Sums are fp32.
+// Measured: forward 8192 x 7168 with a gate of each token 103 us (5.7 TB/s), one row 3.6; backward
+// 8192 x 4096 103-105 us (3.9 TB/s: some 60 fp32 operations an element on half-filled units, with
+// two rows' tensors in registers) and 6 for the join of the blocks' sums, 333 x 1000 6.2 and 4.
 #include "common.h"
 #include "kernels.h"
 
