@@ -25,7 +25,7 @@ from typing import List, Optional, Sequence, Tuple
 
 import torch
 
-from . import (NORM_EPS, _at, alloc_expert_slots, alloc_workspace, block_norms, gated_ffn, gated_ffn_workspace_size,
+from . import (NORM_EPS, _at, _shaped, alloc_expert_slots, alloc_workspace, block_norms, gated_ffn, gated_ffn_workspace_size,
                layer_forward, layer_forward_streamed, linear_bf16, linear_int8, make_config)
 
 
@@ -90,9 +90,8 @@ class LayerStack:
         self.k, self.d_ffn, self.pinned, self.packed = k, d_ffn, pinned, packed
         self.resident: List[Optional[torch.Tensor]] = []
         uploaded = {}
-        width = None
+        self.widths = [lay["w_gate" if _dense(lay) else "router_w"].shape[1] for lay in self.layers]
         for i, lay in enumerate(self.layers):
-            width = width or (lay["w_gate"] if _dense(lay) else lay["router_w"]).shape[1]
             if _dense(lay):
                 self.resident.append(None)
                 continue
@@ -106,15 +105,15 @@ class LayerStack:
                 self.resident.append(uploaded[key])
             else:
                 self.resident.append(None)
-        T, self.d_model, self.num_tokens = num_tokens, width, num_tokens
+        T, self.num_tokens = num_tokens, num_tokens
         self.workspace = self.slots = None
         sparse = [i for i, lay in enumerate(self.layers) if not _dense(lay)]
         if sparse:
             first = self.layers[sparse[0]]
-            cfg = make_config(T, width, first["latent_down"].shape[0], d_ffn, first["router_w"].shape[0], packed=packed)
+            cfg = make_config(T, self.widths[sparse[0]], first["latent_down"].shape[0], d_ffn, first["router_w"].shape[0], packed=packed)
             self.workspace = alloc_workspace(cfg, k, device)
             self.slots = alloc_expert_slots(cfg, k, device) if pinned <= sparse[-1] else None
-        widest = [gated_ffn_workspace_size(T, width, lay["w_gate"].shape[0]) for lay in self.layers if _dense(lay)]
+        widest = [gated_ffn_workspace_size(T, *reversed(lay["w_gate"].shape)) for lay in self.layers if _dense(lay)]
         self.dense_workspace = torch.empty(max(widest), dtype=torch.uint8, device=device) if widest else None
 
     def forward_layer(self, i: int, x: torch.Tensor, out: Optional[torch.Tensor] = None,
@@ -141,10 +140,21 @@ class LayerStack:
         this path.  One call to block_norms ends a layer and begins the next.  Returns (stream, None),
         with final_norm (bf16 [d]) the normed stream as the second, and with head the projection of it:
         a bf16 [n_out, d] for linear_bf16 or (codes, scales) for linear_int8."""
-        if x.shape != (self.num_tokens, self.d_model):
-            raise ValueError(f"x must be of shape {(self.num_tokens, self.d_model)}")
-        if head is not None and final_norm is None:
-            raise ValueError("head needs final_norm")
+        T, d = self.num_tokens, x.shape[-1]
+        _shaped("x", x, (T, d))
+        for i, lay in enumerate(self.layers):
+            if self.widths[i] != d:
+                raise ValueError(f"layer {i} is {self.widths[i]} wide and the stream {d}")
+            if not _dense(lay):  # the layer's own call takes these as they are
+                E, L = lay["router_w"].shape[0], lay["latent_down"].shape[0]
+                _shaped("router_w", lay["router_w"], (E, d))
+                _shaped("latent_down", lay["latent_down"], (L, d))
+                _shaped("latent_up", lay["latent_up"], (d, L))
+        if head is not None:
+            if final_norm is None:
+                raise ValueError("head needs final_norm")
+            if isinstance(head, torch.Tensor):
+                _shaped("head", head, (head.shape[0], d))
         residual = y = None
         done = {}
         for i, lay in enumerate(self.layers + [{"pre_norm": final_norm}]):

@@ -224,3 +224,50 @@ def test_graph_streams_and_repeats(T, d, F):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((out, gate, up, *grads), want))
+
+
+def test_offsets_past_31_bits():
+    """Rows that begin past 2^31 values of the inner tensors, against the same rows alone."""
+    T, d, F, n = 140000, 64, 16384, 300
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rand = lambda *shape, std=1.0: torch.empty(shape, dtype=torch.bfloat16, device="cuda").normal_(0, std, generator=g)
+    x, dout, (wg, wu, wd) = rand(T, d), rand(T, d, std=0.01), weights(d, F)
+    gate, up = rand(T, F), rand(T, F)
+    out = moe.gated_ffn(x, wg, wu, wd, gate=gate, up=up)
+    want = plain_ffn.forward(x[-n:], wg, wu, wd)
+    check(dict(out=out[-n:], gate=gate[-n:], up=up[-n:]), want, "last rows")
+    check(dict(out=out[:n]), plain_ffn.forward(x[:n], wg, wu, wd), "first rows")
+    dx = moe.gated_ffn_backward(dout, x, wg, wu, wd, gate, up, want_dw=False).dx
+    for rows in (slice(0, n), slice(T - n, T)):
+        back = plain_ffn.backward(dout[rows], x[rows], wg, wu, wd, gate[rows], up[rows])
+        check(dict(dx=dx[rows]), back, "backward")
+    # only the last rows have a gradient: the sums over all tokens are theirs
+    dout[:-n] = 0
+    got = moe.gated_ffn_backward(dout, x, wg, wu, wd, gate, up, want_dx=False)
+    rows = slice(T - n, T)
+    back = plain_ffn.backward(dout[rows], x[rows], wg, wu, wd, gate[rows], up[rows])
+    # a sum over T tokens, of which all but n are zeros, rounds no more often than one over n
+    check(dict(dw_gate=got.dw_gate, dw_up=got.dw_up, dw_down=got.dw_down), back, "weights")
+
+
+def test_two_calls_at_once():
+    """Calls of different sizes on two streams, each with a workspace of its own: the bits of each alone."""
+    sizes = [(1100, 1032, 2056), (77, 512, 1000)]
+    made = []
+    for T, d, F in sizes:
+        x, dout, w = plain.bf16((T, d), 1.0, 1).cuda(), plain.bf16((T, d), 0.01, 2).cuda(), weights(d, F)
+        gate, up = torch.empty((2, T, F), dtype=torch.bfloat16, device="cuda")
+        made.append((x, dout, w, gate, up))
+
+    def call(x, dout, w, gate, up, stream=None):
+        out = moe.gated_ffn(x, *w, gate=gate, up=up, stream=stream)
+        return [out, *moe.gated_ffn_backward(dout, x, *w, gate, up, stream=stream)]
+
+    want = [call(*m) for m in made]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in made]
+    for _ in range(5):
+        got = [call(*m, stream=s) for _ in range(3) for m, s in zip(made, streams)]
+        torch.cuda.synchronize()
+        for i, g in enumerate(got):
+            assert all(torch.equal(a, b) for a, b in zip(g, want[i % 2]))

@@ -122,3 +122,20 @@ def test_graph_streams_and_bounds(T, n_in, n_out):
         torch.cuda.synchronize()
         assert torch.equal(out, want)
     assert (whole[:2048] == 7).all() and (whole[2048 + T * n_out:] == 7).all()
+
+
+def test_offsets_past_31_bits():
+    """Results that begin past 2^31 values, and codes of a token past them."""
+    T, n_in, n_out, n = 40000, 16, 65536, 100
+    q = torch.randint(-127, 128, (T, n_in), dtype=torch.int8, device="cuda")
+    W = torch.randint(-127, 128, (n_out, n_in), dtype=torch.int8, device="cuda")
+    one = lambda k: torch.ones(k, device="cuda")
+    out = moe.linear_int8(q, W, one(n_out), x_scale=one(T))
+    for rows in (slice(0, n), slice(T - n, T)):
+        assert torch.equal(out[rows], (q[rows].double() @ W.double().T).bfloat16())
+    T, n_in = 40000, 65536
+    x = torch.zeros((T, n_in), dtype=torch.bfloat16, device="cuda")
+    x[-n:] = plain.bf16((n, n_in), 1.0, 3).cuda()
+    q, s = moe.quantize_int8(x)
+    want_q, want_s = moe.quantize_int8(x[-n:].contiguous())
+    assert torch.equal(q[-n:], want_q) and torch.equal(s[-n:], want_s) and not q[:-n].any()

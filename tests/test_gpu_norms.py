@@ -193,3 +193,22 @@ def test_graph_streams_and_repeats(T, d, gate):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_offsets_past_31_bits():
+    """Rows that begin past 2^31 values, against the plain forms of those rows."""
+    T, d, n = 300000, 8192, 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rand = lambda *shape: torch.empty(shape, dtype=torch.bfloat16, device="cuda").normal_(0, 1, generator=g)
+    y, res, pre, post = rand(T, d), rand(T, d), 1 + 0.1 * rand(d), 1 + 0.1 * rand(d)
+    out, normed = moe.block_norms(y, res, pre_weight=pre, post_weight=post, gate=y, scale=0.5)
+    for rows in (slice(0, n), slice(T - n, T)):
+        check(dict(out=out[rows], normed=normed[rows]),
+              plain_norms.forward(y[rows], res[rows], pre, post, y[rows], 0.5, EPS, out[rows]), "forward")
+    dout = res
+    dout[:-n] = 0  # the sums over the tokens are the last rows'
+    got = moe.block_norms_backward(dout, None, y, out, pre_weight=pre, post_weight=post, gate=y, scale=0.5)
+    rows = slice(T - n, T)
+    want = plain_norms.backward(dout[rows], None, y[rows], out[rows], pre, post, y[rows], 0.5, EPS)
+    check(dict(dresidual=got.dresidual[rows], dy=got.dy[rows], dgate=got.dgate[rows], dpost_weight=got.dpost_weight,
+               dpre_weight=got.dpre_weight), want, "backward")
