@@ -27,14 +27,16 @@
 //
 // LDS layouts, in pieces of 16 bytes, free of bank conflicts for the reads:
 //  K-major: a row is 8 pieces, piece c stored at c ^ (row % 8);
-//  row-major: a k is RP/8 pieces, piece p stored at p ^ 2 (k % 4), read by the transposing LDS
-//    read: 16 lanes hand in 4 k x 16 rows, and lane i receives row i's four k.
+//  row-major: a k is RP/8 pieces, piece p stored at p ^ 2 (k % 4) ^ 8 (k / 8 % 2) (of 64 rows, whose k
+//    alternate between the halves of 256 bytes, ^ 2 (k / 8 % 2)), read by the transposing LDS read:
+//    16 lanes hand in 4 k x 16 rows, and lane i receives row i's four k; 32 lanes, of k and k + 8,
+//    are served at once.  (With p ^ 2 (k % 4) alone those two met: 5.1e7 conflicts in the weights'
+//    gradients of 4096 tokens, 18% of the cycles; the products hid them.)
 // What bounds it at large sizes: a wave of 128 x 128 reads (128 + 128) x 64 bytes from LDS for 64
 // products of 16 cycles, four waves half of the LDS's 128 bytes a cycle, the loads into LDS a
 // quarter; the products themselves run at what the card's power allows (1.9 GHz under this load).
 // Counted at 4096 tokens: the matrix cores busy for 74% of the units' cycles in the gate/up product, 80%
-// in dx, 72% in the weights' gradients (both operands row-major: 18% of the cycles are bank
-// conflicts of the transposing reads), 53% in 8 bits (of twice the rate).
+// in dx, 72% in the weights' gradients, 53% in 8 bits (of twice the rate).
 #pragma once
 
 #include "common.h"
@@ -95,6 +97,8 @@ struct TileLoader {
   static constexpr int NU = BYTES / (1024 * NW);  // loads of a wave for one tile
   static_assert(NU * 1024 * NW == BYTES, "whole loads");
   static_assert(!SPLIT || ORDER == TILE_KMAJ, "two matrices by their rows");
+  // where a row-major k has its pieces
+  static __device__ __forceinline__ int swizzle(int k) { return (2 * (k % 4)) ^ (k / 8 % 2 * (RP == 64 ? 2 : 8)); }
   uint32_t off[NU];
   const uint8_t* base[2];
   int64_t step, K16;  // bytes (K-major) or k (row-major) of a segment
@@ -115,7 +119,7 @@ struct TileLoader {
         off[u] = (uint32_t)((in < left ? in : left - 1) * o.ld + 16 * c);
       } else {
         const int k = p * (512 / RP) + lane / (RP / 8), pos = lane % (RP / 8);
-        const int piece = pos ^ (2 * (k % 4)), last = (left - 1) / 8;
+        const int piece = pos ^ swizzle(k), last = (left - 1) / 8;
         off[u] = (uint32_t)(k * o.ld + 16 * (piece < last ? piece : last));
       }
     }
@@ -297,7 +301,8 @@ __global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArg
     } else {  // lane: k = 32 ks + 8 g + rho / 4 (and + 4), four rows from 4 (rho % 4)
       constexpr int W = 2 * decltype(widthc)::value;
       const int k = 32 * ks + 8 * g + (rho >> 2), q = rho & 3;
-      return tr_read(slot + k * W + 16 * ((col0 / 8 + (q >> 1)) ^ (2 * (rho >> 2))) + 8 * (q & 1), W);
+      const int swizzle = (2 * (rho >> 2)) ^ ((g & 1) * (W == 128 ? 2 : 8));
+      return tr_read(slot + k * W + 16 * ((col0 / 8 + (q >> 1)) ^ swizzle) + 8 * (q & 1), W);
     }
   };
   auto read_m = [&](const uint8_t* slot, int ks, int i) {
