@@ -597,10 +597,11 @@ inline int64_t tiles_of(TileSize z, int64_t M, int64_t N) {
 }
 // K is split where the tiles of the output alone leave units idle: no more pieces than bring the
 // grid to a block a unit, of 8 K tiles at least, 16 at most (33 tokens, 7168 -> 3584, 56 tiles:
-// 23 us whole, 12.1 in two, 10.1 in four, 10.6 in eight).
+// 23 us whole, 12.1 in two, 10.1 in four, 10.6 in eight).  Below 24 K tiles the join costs what the
+// pieces save or more (128 tokens, 1024 and 2048 wide: forward 16.8 us whole, 19.8 in two pieces each).
 inline int tile_splits(TileSize z, int64_t tiles, int64_t k_tiles) {
   if (z >= TILE_224) return 1;
-  const int64_t most = k_tiles / 8, want = 256 / tiles, s = want < most ? want : most;
+  const int64_t most = k_tiles < 24 ? 1 : k_tiles / 8, want = 256 / tiles, s = want < most ? want : most;
   return s < 1 ? 1 : s > 16 ? 16 : (int)s;
 }
 template <int MO, int NO, bool GLU, bool I8, class Epi>
