@@ -74,10 +74,16 @@ static __device__ __align__(16) const uint32_t tile_zero[4] = {0u, 0u, 0u, 0u};
 
 // 16 bytes a lane from scalar base + lane offset, or from a lane's own address, to LDS at lds + 16
 // lane.  m0 is left changed: the compiler keeps nothing there on this target, it writes m0 right
-// before its own uses.
+// before its own uses.  A write of m0 needs one wait state before the load that reads it, and the
+// compiler does not look for that inside asm: so they stand in one block with an s_nop between, or
+// apart, as tile_dma_to and tile_dma_go, with an instruction in between that is asm volatile like
+// them (one of the compiler's own may be moved away).
 __device__ __forceinline__ void tile_dma_to(uint32_t lds) { asm volatile("s_mov_b32 m0, %0" ::"s"(lds)); }
-__device__ __forceinline__ void tile_dma_go(const uint8_t* base, uint32_t off) {  // one instruction or more behind tile_dma_to
+__device__ __forceinline__ void tile_dma_go(const uint8_t* base, uint32_t off) {
   asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base) : "memory");
+}
+__device__ __forceinline__ void tile_dma(const uint8_t* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory");
 }
 __device__ __forceinline__ void tile_dma(const uint8_t* at, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(at), "s"(lds) : "memory");
@@ -128,7 +134,10 @@ struct TileLoader {
     if constexpr (SPLIT) return base[p >= ROWS / 16 ? 1 : 0] + kt * step;  // 8 rows a load, half the rows
     return (seg1 ? base[1] : base[0]) + kt * step;
   }
-  // load u of K tile kt (of its segment), all of whose k exist: first where to, then the load
+  // load u of K tile kt (of its segment), all of whose k exist; or first where to, then the load
+  __device__ __forceinline__ void load(int kt, bool seg1, int u, uint32_t lds, int wave) const {
+    tile_dma(at(kt, NW * u + wave, seg1), off[u], lds + (NW * u + wave) * 1024);
+  }
   __device__ __forceinline__ void load_to(int u, uint32_t lds, int wave) const { tile_dma_to(lds + (NW * u + wave) * 1024); }
   __device__ __forceinline__ void load_go(int kt, bool seg1, int u, int wave) const {
     tile_dma_go(at(kt, NW * u + wave, seg1), off[u]);
@@ -332,7 +341,8 @@ __global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArg
       constexpr int X = decltype(sc)::value, Q = X / NJ, JJ = X % NJ;
       // loads u at products floor(u S / U); reads r at floor(3 r S / 4 A)
       constexpr int U0 = (X * U + S - 1) / S, U1 = ((X + 1) * U + S - 1) / S;
-      if constexpr (FETCH && U1 > U0) {
+      constexpr bool ASM = C::WAVES == 1;  // the product between m0 and the first load is asm
+      if constexpr (FETCH && ASM && U1 > U0) {
         if constexpr (KS == 0)
           ml.load_to(U0, to, wave);
         else
@@ -342,17 +352,17 @@ __global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArg
       if constexpr (FETCH) {
         unroll_n<U1 - U0>([&](auto uc) {
           constexpr int V = U0 + decltype(uc)::value;
-          if constexpr (V > U0) {
+          if constexpr (ASM && V == U0) {
             if constexpr (KS == 0)
-              ml.load_to(V, to, wave);
+              ml.load_go(kt, seg1, V, wave);
             else
-              nl.load_to(V, to, wave);
-            asm volatile("s_nop 0");
+              nl.load_go(kt, seg1, V, wave);
+          } else {
+            if constexpr (KS == 0)
+              ml.load(kt, seg1, V, to, wave);
+            else
+              nl.load(kt, seg1, V, to, wave);
           }
-          if constexpr (KS == 0)
-            ml.load_go(kt, seg1, V, wave);
-          else
-            nl.load_go(kt, seg1, V, wave);
         });
       }
       constexpr int R0 = (4 * A * X + 3 * S - 1) / (3 * S), R1 = (4 * A * (X + 1) + 3 * S - 1) / (3 * S);
