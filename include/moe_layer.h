@@ -502,7 +502,8 @@ moe_status moe_gated_ffn_backward(const void* dout, const void* x, const void* w
  * y, residual, out, normed bf16 [T][d]; post_weight, pre_weight bf16 [d]; gate bf16 [d]
  * (gate_row_stride 0: one for all tokens) or [T][d] (gate_row_stride d).  y NULL: the norm alone,
  * normed of residual, and post_weight, gate and out are NULL; pre_weight NULL: no normed.  Statistics
- * and sums are fp32 (squares of values past 2^63 leave its range).  The K3 port's eps is fp32's,
+ * and sums are fp32; a row's squares are scaled where they would leave its range, so rows of any finite
+ * values have their norm (with eps 0, those whose rms is at least 2^-120).  The K3 port's eps is fp32's,
  * 2^-23 (kimi-k3-mlx digest, the choice of the RMSNorm eps).  d a multiple of 8, at most 8192; T up to
  * 2^24; every pointer 16-byte aligned.  out may be residual itself; otherwise outputs overlap
  * nothing. */

@@ -10,10 +10,12 @@
 //              dpost = sum_t b yh,  dy = (f - yh mean(f yh)) / rms(y)   (dy = b without a norm)
 // Bound: HBM.  A row is held in registers from its first load on, so each tensor is read and
 // written once: 8 bytes an element forward, 12 backward, 2 and 4 more with a gate of each token.
-// A row belongs to one wave, or to four or eight where it is long.  Sums are fp32.
+// A row belongs to one wave, or to four or eight where it is long.  Sums are fp32, of squares scaled by
+// a power of two where they would leave its range.
 // Measured: forward 8192 x 7168 with a gate of each token 103 us (5.7 TB/s), one row 3.6; backward
-// 8192 x 4096 103-105 us (3.9 TB/s: some 60 fp32 operations an element on half-filled units, with
-// two rows' tensors in registers) and 6 for the join of the blocks' sums, 333 x 1000 6.2 and 4.
+// 8192 x 4096 107-109 us (3.7 TB/s: some 60 fp32 operations an element on half-filled units, with two
+// rows' tensors in registers; 4 us of it for the look at each sum's range) and 6 for the join of the
+// blocks' sums, 333 x 1000 6.2 and 4.
 #include "common.h"
 #include "kernels.h"
 
@@ -66,15 +68,112 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* lds, int turn) {
   }
 }
 
-__device__ __forceinline__ float inverse_rms(float squares, float inv_d, float eps) {
-  return 1.f / sqrtf(squares * inv_d + eps);
+// The squares of a row.  Of values past 2^60, and with a tiny eps of those under 2^-50, the sum of
+// their squares nears an end of fp32's range or leaves it; a wave that finds its sum there takes it
+// again of its values times a power of two (a branch of whole waves, from registers).  Range says
+// which: of a row's waves the largest counts, and the others' sums are brought to it.
+enum Range { IN = 0, HIGH = 1, LOW = 2 };
+__device__ __forceinline__ int range_of(float squares, float eps) {
+  const float t = squares + eps;
+  return t < 0x1p120f ? (t < 0x1p-100f ? LOW : IN) : HIGH;  // an infinity or NaN: HIGH
+}
+__device__ __forceinline__ float range_scale(int range) { return range == IN ? 1.f : range == HIGH ? 0x1p-72f : 0x1p72f; }
+// the larger of two, and what a value scaled for `from` is to be multiplied with to be scaled for `to`
+__device__ __forceinline__ int range_max(int a, int b) { return a == HIGH || b == HIGH ? HIGH : a == IN || b == IN ? IN : LOW; }
+__device__ __forceinline__ float range_step(int from, int to) {
+  return from == to ? 1.f : from == LOW && to == HIGH ? 0.f : 0x1p-72f;  // 2^-144 of what is below 1
+}
+
+// row_sums of s[0] a row's squares, s[1] products with its values, s[2] another row's squares, each of
+// the range that r (of the first two) and y say; on return those are the row's.
+template <int WPR, int N>
+__device__ __forceinline__ void row_statistics(float (&s)[N], int& r, int& y, float* lds, int turn) {
+  static_assert(N == 1 || N == 3, "squares; or squares, products, squares");
+  if constexpr (WPR > 1) {
+    const int wave = threadIdx.x / WAVE, nw = blockDim.x / WAVE;
+    float4* at = reinterpret_cast<float4*>(lds) + turn * nw;
+    if (lane_id() == 0) at[wave] = make_float4(s[0], N > 1 ? s[1] : 0.f, N > 1 ? s[2] : 0.f, __int_as_float(r | y << 2));
+    lds_barrier();
+    const float4* mine = at + wave / WPR * WPR;
+    int any = 0;
+    float sum[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) {
+      const float4 v = mine[w];
+      sum[0] += v.x;
+      sum[1] += v.y;
+      sum[2] += v.z;
+      any |= __float_as_int(v.w);
+    }
+    any = __builtin_amdgcn_readfirstlane(any);
+    if (any != 0) {
+      r = y = LOW;
+#pragma unroll 1
+      for (int w = 0; w < WPR; ++w) {
+        const int f = __float_as_int(mine[w].w);
+        r = range_max(r, f & 3);
+        y = range_max(y, f >> 2);
+      }
+      sum[0] = sum[1] = sum[2] = 0.f;
+#pragma unroll 1
+      for (int w = 0; w < WPR; ++w) {
+        const float4 v = mine[w];
+        const int f = __float_as_int(v.w);
+        const float a = range_step(f & 3, r), b = range_step(f >> 2, y);
+        sum[0] += v.x * a * a;
+        sum[1] += v.y * a;
+        sum[2] += v.z * b * b;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = sum[i];
+  }
+}
+
+// sum of (x kx) w (y ky), w null: 1.  Word by word, and nothing that was computed from them is kept for
+// it or by it: it is rare, and stands where registers are few.
+template <int C>
+__device__ __forceinline__ float scaled_sum(const uint4 (&x)[C], const uint4 (&y)[C], const uint4* w, float kx, float ky) {
+  float s = 0.f;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const uint32_t a[4] = {x[c].x, x[c].y, x[c].z, x[c].w}, b[4] = {y[c].x, y[c].y, y[c].z, y[c].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t p = a[i], q = b[i], r = 0x3F803F80u;  // two ones
+      if (w) r = i == 0 ? w[c].x : i == 1 ? w[c].y : i == 2 ? w[c].z : w[c].w;
+      asm volatile("" : "+v"(p), "+v"(q), "+v"(r), "+v"(s));
+      s += (bf16lo(p) * kx) * bf16lo(r) * (bf16lo(q) * ky);
+      s += (bf16hi(p) * kx) * bf16hi(r) * (bf16hi(q) * ky);
+    }
+  }
+  return s;
+}
+
+// 1 / rms of the row itself, from squares of values times range_scale(range)
+__device__ __forceinline__ float inverse_rms(float squares, int range, float inv_d, float eps) {
+  const float k = range_scale(range);
+  return k / sqrtf(squares * inv_d + eps * k * k);
+}
+
+// 1 / rms of the row whose pieces x are, s the lane's sum of their squares
+template <int WPR, int C>
+__device__ __forceinline__ float row_inverse_rms(const uint4 (&x)[C], float s0, float inv_d, float eps, float* red, int turn) {
+  float s[1] = {wave_sum_dpp(s0)};
+  int range = range_of(s[0], eps), none = IN;
+  if (range != IN) {
+    const float k = range_scale(range);
+    s[0] = wave_sum_dpp(scaled_sum<C>(x, x, nullptr, k, k));
+  }
+  row_statistics<WPR>(s, range, none, red, turn);
+  return inverse_rms(s[0], range, inv_d, eps);
 }
 
 // WPR waves a row, C pieces of 8 columns a thread
 template <int WPR, int C>
 __global__ void __launch_bounds__(256) block_norms_kernel(NormArgs p) {
   constexpr int GT = WPR * WAVE, ROWS = 256 / GT;
-  __shared__ float red[2 * 4 * 4];
+  __shared__ __align__(16) float red[2 * 4 * 4];
   const int at = threadIdx.x % GT;
   int64_t t = (int64_t)blockIdx.x * ROWS + threadIdx.x / GT;
   if constexpr (ROWS > 1) {
@@ -96,18 +195,17 @@ __global__ void __launch_bounds__(256) block_norms_kernel(NormArgs p) {
   const float inv_d = 1.f / (float)p.d;
   float m = p.scale;
   if (p.post) {
-    float s[1] = {0.f};
+    float s = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       float v[8];
       unpack8(y[c], v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[0] += v[i] * v[i];
+      for (int i = 0; i < 8; ++i) s += v[i] * v[i];
     }
-    row_sums<WPR>(s, red, 0);
-    m = inverse_rms(s[0], inv_d, p.eps);
+    m = row_inverse_rms<WPR>(y, s, inv_d, p.eps, red, 0);
   }
-  float s[1] = {0.f};
+  float s = 0.f;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     if (p.y) {
@@ -136,11 +234,10 @@ __global__ void __launch_bounds__(256) block_norms_kernel(NormArgs p) {
     float v[8];
     unpack8(r[c], v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[0] += v[i] * v[i];
+    for (int i = 0; i < 8; ++i) s += v[i] * v[i];
   }
   if (!p.pre) return;
-  row_sums<WPR>(s, red, 1);
-  const float k = inverse_rms(s[0], inv_d, p.eps);
+  const float k = row_inverse_rms<WPR>(r, s, inv_d, p.eps, red, 1);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int col = 8 * (at + GT * c);
@@ -238,9 +335,22 @@ __global__ void __launch_bounds__(back_threads(WPR)) block_norms_backward_kernel
         for (int i = 0; i < 8; ++i) s[2] += a[i] * a[i];
       }
     }
-    row_sums<WPR>(s, red, 0);
-    const float ir = inverse_rms(s[0], inv_d, p.eps), mean = s[1] * inv_d * ir * ir;  // mean(e rh) / rms(r)
-    const float iy = p.post ? inverse_rms(s[2], inv_d, p.eps) : 1.f;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) s[i] = wave_sum_dpp(s[i]);
+    int rr = p.pre ? range_of(s[0], p.eps) : IN, ry = p.post ? range_of(s[2], p.eps) : IN;
+    if (rr != IN) {
+      s[0] = wave_sum_dpp(scaled_sum<C>(cr, cr, nullptr, range_scale(rr), range_scale(rr)));
+      s[1] = wave_sum_dpp(scaled_sum<C>(cn, cr, nw, 1.f, range_scale(rr)));
+    }
+    if (ry != IN) s[2] = wave_sum_dpp(scaled_sum<C>(cy, cy, nullptr, range_scale(ry), range_scale(ry)));
+    row_statistics<WPR>(s, rr, ry, red, 0);
+    if constexpr (C > 1) {  // not kept unpacked from above: past the branches there are no registers for it
+#pragma unroll
+      for (int c = 0; c < C; ++c) asm volatile("" : "+v"(cn[c].x), "+v"(cn[c].y), "+v"(cn[c].z), "+v"(cn[c].w));
+    }
+    const float ir = inverse_rms(s[0], rr, inv_d, p.eps);
+    const float mean = s[1] * inv_d * (rr == IN ? ir : ir * range_scale(HIGH + LOW - rr)) * ir;  // mean(e rh) / rms(r)
+    const float iy = p.post ? inverse_rms(s[2], ry, inv_d, p.eps) : 1.f;
     float f[C][8], q[1] = {0.f};
 #pragma unroll
     for (int c = 0; c < C; ++c) {
