@@ -127,8 +127,13 @@ Int8Layout int8_layout(int64_t T, int32_t n_in, int32_t n_out, bool quantize) {
   return l;
 }
 hipError_t launch_quantize_int8(const uint16_t* x, int64_t T, int32_t n, int8_t* q, float* scale, hipStream_t st) {
-  hipLaunchKernelGGL(quantize_int8_kernel, dim3((unsigned)T), dim3(256), 0, st, x, n, q, scale);
-  return hipGetLastError();
+  hipError_t err = hipSuccess;
+  for (int64_t t = 0; t < T && err == hipSuccess; t += LAUNCH_BLOCKS) {
+    const unsigned rows = (unsigned)(T - t < LAUNCH_BLOCKS ? T - t : LAUNCH_BLOCKS);
+    hipLaunchKernelGGL(quantize_int8_kernel, dim3(rows), dim3(256), 0, st, x + t * n, n, q + t * n, scale + t);
+    err = hipGetLastError();
+  }
+  return err;
 }
 
 hipError_t launch_linear_int8(const int8_t* q, const float* xs, const int8_t* W, const float* ws, int64_t T, int32_t n_in,

@@ -274,6 +274,10 @@ FfnLayout ffn_backward_layout(int64_t T, int32_t d, int32_t F);
 hipError_t launch_ffn(const FfnArgs& p, void* ws, hipStream_t st);
 hipError_t launch_ffn_backward(const FfnBackArgs& p, void* ws, hipStream_t st);
 
+// Blocks of up to 256 threads a launch: a launch counts its threads in 32 bits, and 2^24 rows, a block
+// each, are one too many.  Calls of more blocks take a launch for each part.
+constexpr int64_t LAUNCH_BLOCKS = (int64_t)1 << 23;
+
 // ---- norms.hip: the norms, gate and sum between two blocks of a residual stream
 struct NormArgs {
   const uint16_t *y, *residual, *post, *pre, *gate;  // y, post, pre, gate nullable

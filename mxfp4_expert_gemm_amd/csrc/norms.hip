@@ -501,8 +501,21 @@ int64_t backward_blocks(int64_t T, int32_t d) {
 
 template <int WPR, int C>
 hipError_t launch_forward(const NormArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((block_norms_kernel<WPR, C>), dim3((unsigned)ceil_div(a.T, 4 / WPR)), dim3(256), 0, st, a);
-  return hipGetLastError();
+  constexpr int64_t ROWS = 4 / WPR;
+  hipError_t err = hipSuccess;
+  for (int64_t t = 0; t < a.T && err == hipSuccess; t += LAUNCH_BLOCKS * ROWS) {
+    NormArgs p = a;
+    auto from = [&](auto* rows) { return rows ? rows + t * a.d : nullptr; };
+    p.y = from(a.y);
+    p.residual = from(a.residual);
+    p.out = from(a.out);
+    p.normed = from(a.normed);
+    if (a.gate_stride) p.gate = from(a.gate);
+    p.T = a.T - t < LAUNCH_BLOCKS * ROWS ? a.T - t : LAUNCH_BLOCKS * ROWS;
+    hipLaunchKernelGGL((block_norms_kernel<WPR, C>), dim3((unsigned)ceil_div(p.T, ROWS)), dim3(256), 0, st, p);
+    err = hipGetLastError();
+  }
+  return err;
 }
 template <int WPR, int C>
 hipError_t launch_backward(const NormBackArgs& a, hipStream_t st) {
