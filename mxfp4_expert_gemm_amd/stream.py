@@ -25,8 +25,11 @@ from typing import List, Optional, Sequence, Tuple
 
 import torch
 
-from . import (NORM_EPS, _at, _shaped, alloc_expert_slots, alloc_workspace, block_norms, gated_ffn, gated_ffn_workspace_size,
-               layer_forward, layer_forward_streamed, linear_bf16, linear_int8, make_config)
+from . import (_BF16, _F32, _I8, NORM_EPS, _at, _shaped, alloc_expert_slots, alloc_workspace, block_norms,
+               expert_bytes, gated_ffn, gated_ffn_workspace_size, layer_forward, layer_forward_streamed, linear_bf16,
+               linear_int8, make_config, packed_expert_bytes)
+
+_FLT_MAX = torch.finfo(torch.float32).max
 
 
 def plan_prefix(num_layers: int, layer_expert_bytes: int, hbm_budget_bytes: int, reserved_bytes: int = 0) -> int:
@@ -132,6 +135,62 @@ class LayerStack:
             return layer_forward(*args, self.resident[i], self.k, **kw)
         return layer_forward_streamed(*args, lay["expert_blob_host"], self.k, expert_slots=self.slots, **kw)
 
+    def _check_pass(self, x: torch.Tensor, final_norm: Optional[torch.Tensor], head, eps: float):
+        """What forward is given and what the layers hold, before any of it runs: a pass that is refused
+        half way has fetched experts for nothing, and the routed layers' calls take their tensors as they are."""
+        T, d, device = self.num_tokens, x.shape[-1], x.get_device()
+
+        def fits(name, t, shape, dtypes=_BF16):
+            if t.shape != shape or t.dtype not in dtypes or t.get_device() != device or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {dtypes[0]} tensor of shape {shape} on the device of x")
+
+        _shaped("x", x, (T, d))
+        if not 0 <= eps <= _FLT_MAX:
+            raise ValueError("eps must be a finite fp32 number, 0 or more")
+        each = packed_expert_bytes if self.packed else expert_bytes
+        sizes = {}
+        for i, lay in enumerate(self.layers):
+            if self.widths[i] != d:
+                raise ValueError(f"layer {i} is {self.widths[i]} wide and the stream {d}")
+            for name in ("pre_norm", "post_norm"):
+                if lay.get(name) is not None:
+                    fits(name, lay[name], (d,))
+            gate = lay.get("gate")
+            if gate is not None:
+                fits("gate", gate, (d,) if gate.dim() == 1 else (T, d))
+            if not abs(lay.get("scale", 1.0)) <= _FLT_MAX:
+                raise ValueError("scale must be a finite fp32 number")
+            if _dense(lay):
+                F = lay["w_gate"].shape[0]
+                for name, shape in (("w_gate", (F, d)), ("w_up", (F, d)), ("w_down", (d, F))):
+                    fits(name, lay[name], shape)
+                continue
+            E, L = lay["router_w"].shape[0], lay["latent_down"].shape[0]
+            fits("router_w", lay["router_w"], (E, d))
+            fits("latent_down", lay["latent_down"], (L, d))
+            fits("latent_up", lay["latent_up"], (d, L))
+            bias = lay.get("bias")
+            if bias is not None:
+                fits("bias", bias, (E,) if bias.dim() == 1 else (T, E), _F32)
+            if L not in sizes:
+                sizes[L] = each(L, self.d_ffn)
+            blob = lay["expert_blob_host"]
+            if blob.numel() * blob.element_size() < E * sizes[L]:
+                raise ValueError(f"layer {i}: expert_blob_host is smaller than {E} experts")
+        if final_norm is not None:
+            fits("final_norm", final_norm, (d,))
+        if head is not None:
+            if final_norm is None:
+                raise ValueError("head needs final_norm")
+            if isinstance(head, torch.Tensor):
+                fits("head", head, (head.shape[0], d))
+            else:
+                W, w_scale = head
+                fits("head", W, (W.shape[0], d), _I8)
+                fits("the head's scales", w_scale, (W.shape[0],), _F32)
+                if d % 16:
+                    raise ValueError("a head in 8 bits takes widths that are multiples of 16")
+
     def forward(self, x: torch.Tensor, *, final_norm: Optional[torch.Tensor] = None, head=None, eps: float = NORM_EPS,
                 stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
         """One pass of a residual stream over the stack, x bf16 [num_tokens, d] its start: for each layer
@@ -139,22 +198,9 @@ class LayerStack:
         with what its dict holds of them; attention, which comes between them in a model, is not part of
         this path.  One call to block_norms ends a layer and begins the next.  Returns (stream, None),
         with final_norm (bf16 [d]) the normed stream as the second, and with head the projection of it:
-        a bf16 [n_out, d] for linear_bf16 or (codes, scales) for linear_int8."""
-        T, d = self.num_tokens, x.shape[-1]
-        _shaped("x", x, (T, d))
-        for i, lay in enumerate(self.layers):
-            if self.widths[i] != d:
-                raise ValueError(f"layer {i} is {self.widths[i]} wide and the stream {d}")
-            if not _dense(lay):  # the layer's own call takes these as they are
-                E, L = lay["router_w"].shape[0], lay["latent_down"].shape[0]
-                _shaped("router_w", lay["router_w"], (E, d))
-                _shaped("latent_down", lay["latent_down"], (L, d))
-                _shaped("latent_up", lay["latent_up"], (d, L))
-        if head is not None:
-            if final_norm is None:
-                raise ValueError("head needs final_norm")
-            if isinstance(head, torch.Tensor):
-                _shaped("head", head, (head.shape[0], d))
+        a bf16 [n_out, d] for linear_bf16 or (codes, scales) for linear_int8.  Shapes, types and places are
+        checked before anything runs."""
+        self._check_pass(x, final_norm, head, eps)
         residual = y = None
         done = {}
         for i, lay in enumerate(self.layers + [{"pre_norm": final_norm}]):
