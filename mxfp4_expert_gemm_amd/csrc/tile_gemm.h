@@ -589,9 +589,12 @@ hipError_t launch_tile_gemm(TileArgs a, int segs, const Epi& epi, hipStream_t st
   return hipGetLastError();
 }
 
-// Tiles by the rows of M: few tokens take 16, 32, 48 or 64 rows by 64 columns in blocks of two
-// waves, two blocks a unit, with a deep ring; 256 x 256 (or 224) where those fill three quarters of
-// the units; between them 128 x 128, two blocks a unit, or where those leave units idle and K is
+// Tiles by the size of the output: 256 x 256 (or 224) where those fill three quarters of the units;
+// otherwise few tokens take 16, 32, 48 or 64 rows by 64 columns in blocks of two waves, two blocks a
+// unit, with a deep ring.  Outputs of more than 48,896 columns (each matrix of a GLU: 24,448) fill the
+// units with large tiles whatever their rows, most of which then do not exist: one token in 8 bits,
+// 7168 -> 49152 94.7 us (3.7 TB/s), -> 163840 263 (4.5), where 40960 columns, on tiles of 16 rows, take
+// 64.1 (4.6).  Between them 128 x 128, two blocks a unit, or where those leave units idle and K is
 // short, so that beginning and ending count and not the stream, 64 x 64 (77 tokens, 512 and 1000 wide:
 // forward 14.5 us from 20.2, backward 24 from 31; 512 tokens, 1024 -> 1024: forward 18.5 from 27.5.
 // With a longer K they lose: 100 tokens, 4096 -> 4096 46 from 36.8).
