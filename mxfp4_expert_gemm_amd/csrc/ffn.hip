@@ -4,9 +4,12 @@
 //   backward:  dA = Wd^T dout (fp32), s = 1 / (1 + e^-g),
 //              a = bf16(g s u), dU = bf16(dA g s), dG = bf16(dA u s (1 + g (1 - s))),
 //              dx = bf16(Wg^T dG + Wu^T dU), dWg = bf16(dG^T x), dWu = bf16(dU^T x), dWd = bf16(dout^T a)
-// a, dG and dU are rounded to bf16 since the matrix cores read them (of few tokens, where that costs
-// nothing, they keep 16 bits or all); every sum is fp32 (the kept g and u are bf16 so that training
-// holds 4 bytes for a token and inner channel and not 8).
+// a, dG and dU are rounded to bf16 once each, since the matrix cores read them: the results are off by
+// 0.0023 to 0.0024 (rms, relative), of which 0.0017 is their own rounding.  Fewer roundings where
+// they were found to cost nothing: up to four tokens forward a stays fp32 if it fits the LDS (gemv_wide),
+// up to 64 tokens backward each is held in two halves (0.0017 both).  So a token's result depends on
+// how many are with it, within those roundings.  Every sum is fp32 (the kept g and u are bf16 so that
+// training holds 4 bytes for a token and inner channel and not 8).
 //
 // Measured (kernels; rates of 2 M N K operations, bytes of weights read):
 //   4096 tokens, 7168 -> 3584: gate/up 300-350 us (1.2-1.4 PFLOP/s), down 160-190 (1.1-1.3)
@@ -15,7 +18,7 @@
 //     (1.4-1.5), weights' gradients 593-650 (1.3-1.4)
 //   33 tokens, 3584 -> 7168: gate/up 23 us (4.5 TB/s), down 13.4 (3.8 TB/s) and 4 to join its pieces
 //   1 token, 7168 -> 8192: gate/up 36.7 us (6.4 TB/s), down 21.5 (5.5 TB/s)
-//   77 tokens, 512 -> 1000, backward: 7.2 + 7.2 + 3.2 + 5.9 us, of which some 5 a launch are there with
+//   77 tokens, 512 -> 1000, backward: 7-8 + 7 + 3.5 + 6 us, of which some 5 a launch are there with
 //     8 x 8 matrices too
 #include "common.h"
 #include "kernels.h"
@@ -136,6 +139,10 @@ struct EpiGluBack {
 
 // Up to eight tokens on the vector units: one wave a row of the weights (GLU: the same row of both
 // matrices), 16 bytes a lane and load, eight loads (of each) on their way, the block's tokens in LDS.
+// Good for narrow blocks, where the call is short (5 tokens, 256 -> 344: 5.2 + 4.6 us).  Of wide ones it
+// falls off past four tokens: 7168 -> 8192 58.7 us for one, 87 for four, 164 for five and 176 for
+// eight, where nine on the tiles take 69.4; the tokens of 7168 values then fill 112 KB of a unit's
+// LDS, so one block of four waves runs there and fills it anew for every four rows of weights.
 // out[t][row] = sum_k w[row][k] in[t][k]; GLU: bf16(silu(g) u), and g and u where they are kept.
 // Bound: HBM.  A lane's sum is at most K / 128 pairs of products one after another, in fp32, then a
 // tree over the lanes.

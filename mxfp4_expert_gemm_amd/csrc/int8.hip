@@ -2,7 +2,7 @@
 // sums exact in 32 bits, on the tiles of tile_gemm.h (v_mfma_i32_16x16x64_i8: the same bytes a
 // step as the bf16 products, for twice the values); and the quantiser of its tokens,
 //   q = 127 x / max|x| rounded to the nearest whole number, ties to even, x_scale = max|x| / 127.
-// Measured: 8191 tokens, 3584 -> 7168: product 190-214 us (2.0-2.2 POP/s), quantiser 18-21 (4.2-4.9 TB/s
+// Measured: 8191 tokens, 3584 -> 7168: product 190-222 us (1.9-2.2 POP/s), quantiser 18-21 (4.2-4.9 TB/s
 // of x and codes); 48 tokens, 7168 -> 3584: quantiser 4.2 us, product 9.2 (2.8 TB/s of weights: a
 // stream this short is mostly its beginning and end), join 3.
 #include "common.h"

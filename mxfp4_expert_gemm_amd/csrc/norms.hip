@@ -13,9 +13,9 @@
 // A row belongs to one wave, or to four or eight where it is long.  Sums are fp32, of squares scaled by
 // a power of two where they would leave its range.
 // Measured: forward 8192 x 7168 with a gate of each token 103 us (5.7 TB/s), one row 3.6; backward
-// 8192 x 4096 107-109 us (3.7 TB/s: some 60 fp32 operations an element on half-filled units, with two
-// rows' tensors in registers; 4 us of it for the look at each sum's range) and 6 for the join of the
-// blocks' sums, 333 x 1000 6.2 and 4.
+// 8192 x 4096 108-111 us (3.7 TB/s: some 60 fp32 operations an element on half-filled units, with two
+// rows' tensors in registers; 5 us of it for the look at each sum's range) and 6 for the join of the
+// blocks' sums, 333 x 1000 6.2-6.5 and 4.
 #include "common.h"
 #include "kernels.h"
 

@@ -35,8 +35,9 @@
 // What bounds it at large sizes: a wave of 128 x 128 reads (128 + 128) x 64 bytes from LDS for 64
 // products of 16 cycles, four waves half of the LDS's 128 bytes a cycle, the loads into LDS a
 // quarter; the products themselves run at what the card's power allows (1.9 GHz under this load).
-// Counted at 4096 tokens: the matrix cores busy for 74% of the units' cycles in the gate/up product, 80%
-// in dx, 72% in the weights' gradients, 53% in 8 bits (of twice the rate).
+// Counted at 4096 tokens: the matrix cores busy for 74% of the units' cycles in the gate/up product, 68%
+// in down, 51% in dA (its epilogue), 81% in dx, 72% in the weights' gradients; 53% in 8 bits, 8191 tokens
+// (of twice the rate).
 #pragma once
 
 #include "common.h"
