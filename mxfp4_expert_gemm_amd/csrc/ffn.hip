@@ -85,6 +85,20 @@ struct EpiGlu {
   }
 };
 
+// s = 1 / (1 + e^-g), 1 - s and g s, each to a few fp32 ulps (and what |g| 2^-24 makes of the exponential)
+// for every g: from e^-|g|, past the range of the hardware's 2^x, which ends at 2^-126, from 2^32 times it,
+// as in silu_f32.
+struct Sigmoid {
+  float s, rest, gs;
+};
+__device__ __forceinline__ Sigmoid sigmoid_f32(float g) {
+  const float x = -fabsf(g) * 1.44269504088896341f;
+  const bool tiny = x < -120.f;
+  const float e2 = __builtin_amdgcn_exp2f(tiny ? x + 32.f : x), sc = tiny ? 0x1p-32f : 1.f;
+  const float e = e2 * sc, r = __builtin_amdgcn_rcpf(1.f + e), less = e * r;
+  return g >= 0.f ? Sigmoid{r, less, g * r} : Sigmoid{less, r, (g * e2) * sc * r};
+}
+
 // what rounding v to bf16 leaves, or 0 where it does not stay finite
 __device__ __forceinline__ float rounded_off(float v) {
   const float r = v - (float)(__bf16)v;
@@ -112,11 +126,10 @@ struct EpiGluBack {
     unpack8(h.u, u);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      // the hardware's 2^x and reciprocal: a few ulps each, against the rounding that follows
-      const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896341f * g[i])), gs = g[i] * s;
-      av[i] = gs * u[i];
-      du[i] = d[i] * gs;
-      dg[i] = d[i] * u[i] * (s + gs * (1.f - s));
+      const Sigmoid t = sigmoid_f32(g[i]);
+      av[i] = t.gs * u[i];
+      du[i] = d[i] * t.gs;
+      dg[i] = d[i] * (u[i] * (t.s + t.gs * t.rest));  // u meets the slope first: d u may be past fp32 where this is not
     }
     store8(a + (int64_t)m * F + n, av);
     uint16_t* o = dgu + (int64_t)m * 2 * F + n;
