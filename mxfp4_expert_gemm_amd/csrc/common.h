@@ -272,6 +272,10 @@ __device__ __forceinline__ void unroll_n(Fn&& f) {
   unroll_impl(f, std::make_integer_sequence<int, N>{});
 }
 
+// the top bit of each bf16 half that is an infinity or NaN, and the pair without those halves
+__device__ __forceinline__ uint32_t not_finite2(uint32_t v) { return ((v & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u; }
+__device__ __forceinline__ uint32_t finite2(uint32_t v) { return v & ~((not_finite2(v) >> 15) * 0xFFFFu); }
+
 // Workgroup barrier that hands over LDS only: it waits for this wave's LDS operations
 // and not for its global loads in flight.  (__syncthreads also waits for every
 // outstanding global load, which empties a prefetch pipeline at each barrier.)  The

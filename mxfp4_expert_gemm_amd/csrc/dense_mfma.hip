@@ -67,10 +67,6 @@ __device__ __forceinline__ u32x4_t keep_ranks(u32x4_t v, int valid) {
   return v;
 }
 
-// the top bit of each bf16 half that is an infinity or NaN, and the pair without those halves
-__device__ __forceinline__ uint32_t not_finite2(uint32_t v) { return ((v & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u; }
-__device__ __forceinline__ uint32_t finite2(uint32_t v) { return v & ~((not_finite2(v) >> 15) * 0xFFFFu); }
-
 // The adapters' term of a wave's tile (16 WM tokens from tb, 16 WN rows from nb), added to
 // its accumulators: each adapter met among the tokens multiplies, per 16 tokens that hold one
 // of its own, all 16 rows of u by its B (u in U_TERMS terms, all 24 bits of its fp32 sums: the

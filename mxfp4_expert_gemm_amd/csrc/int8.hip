@@ -21,6 +21,7 @@ struct EpiInt8 {
   uint16_t* out;
   int32_t N;
   int32_t* part;
+  static constexpr bool BEGINS = false;
   struct Held {};
   __device__ __forceinline__ Held hold(int, int) const { return {}; }
   __device__ __forceinline__ void put(int, int m, int n, int left, const Held&, const int32_t (&v)[8]) const {

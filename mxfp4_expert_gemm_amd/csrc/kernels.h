@@ -255,7 +255,7 @@ hipError_t launch_combine(const float* y, const float* w, int64_t T, int32_t k, 
 
 // ---- ffn.hip: the dense gated block and its backward pass
 struct FfnLayout {
-  size_t a, dgu, part, total;  // workspace: GLU rows, dG | dU, pieces of split sums
+  size_t a, dgu, finite, part, total;  // workspace: GLU rows, dG | dU, x and dout for low halves, pieces of split sums
 };
 struct FfnArgs {
   const uint16_t *x, *w_gate, *w_up, *w_down;  // [T][d], [F][d], [F][d], [d][F]

@@ -60,7 +60,8 @@ struct TileArgs {
   TileOperand m, n;
   int64_t K;       // values of one K segment; K-major: whole pieces of 16 bytes
   int32_t splits;  // the K tiles are dealt to so many blocks; tile_join adds their results
-  int32_t halves;  // 2: the second half of M's rows are the low bits of the first's; tile_join adds their results
+  int32_t halves;  // 2: the second half of M's rows are the low bits of the first's; tile_join adds their results,
+                   // without the second's where the first's are not finite (there 0 may have met an infinity)
   int32_t which;   // told to the epilogue: of two products in one launch, whose results these are
   int64_t part;    // where in the epilogue's part the product's pieces begin
   // set by the launcher
@@ -219,6 +220,7 @@ __device__ __forceinline__ void tile_settle(Acc (&acc)[C::MI][C::NJ]) {
 }
 
 // The epilogue's type Epi has
+//   static constexpr bool BEGINS      void begin(), if so: what the grid's threads do before their tiles
 //   struct Held                       what it reads from memory for eight results
 //   Held hold(m, n)                   reads that, ahead of the results
 //   void put(which, m, n, left, held, v)       eight results (left: columns from n on that exist), or with GLU
@@ -235,6 +237,7 @@ __global__ void __launch_bounds__(C::NW * 64, C::WAVES) tile_gemm_kernel(TileArg
   using Value = std::conditional_t<C::I8, int32_t, float>;
   extern __shared__ __align__(16) uint8_t lds[];
 
+  if constexpr (Epi::BEGINS) epi.begin();
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / WAVE));
   const int wm = wave / C::WN, wn = wave % C::WN, rho = lane & 15, g = lane >> 4;
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
@@ -515,7 +518,7 @@ inline bool tiles_of_224(int64_t M, int64_t N) {
 // XCDs' own caches and one unit read all of a tile's (33 tokens, 7168 -> 3584: 20.4 us in all, 10.1 + 4 so).
 struct TileJoin {  // of one product
   int64_t pieces, part;  // eight results each
-  int32_t N, parts, which;
+  int32_t N, parts, which, halves;
 };
 template <class Value, bool GLU, class Epi>
 __global__ void __launch_bounds__(256) tile_join_kernel(TileJoin p0, TileJoin p1, Epi epi) {
@@ -544,6 +547,23 @@ __global__ void __launch_bounds__(256) tile_join_kernel(TileJoin p0, TileJoin p1
   for (int i = 0; i < G; ++i)
 #pragma unroll
     for (int r = 0; r < 8; ++r) v[i][r] = a[2 * i + r / 4][r % 4];
+  if constexpr (!GLU && std::is_same_v<Value, float>) {
+    if (p.halves == 2) {
+      bool finite = true;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) finite = finite && fabsf(v[0][r]) < INFINITY;
+      if (!finite) {  // the first halves' sums alone
+        a[0] = a[1] = V4{0, 0, 0, 0};
+        for (int s = 0; s < p.parts; s += 2) {
+          const V4* q = reinterpret_cast<const V4*>(epi.part + p.part + ((int64_t)s * p.pieces + x) * 8);
+          a[0] += q[0];
+          a[1] += q[1];
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r) v[0][r] = fabsf(v[0][r]) < INFINITY ? v[0][r] : a[r / 4][r % 4];
+      }
+    }
+  }
   if constexpr (GLU)
     epi.put(p.which, m, n, p.N - n, epi.hold(m, n), v[0], v[1]);
   else
@@ -580,7 +600,7 @@ hipError_t launch_tile_gemm(TileArgs a, int segs, const Epi& epi, hipStream_t st
     using Value = std::conditional_t<C::I8, int32_t, float>;
     auto join = [](const TileArgs& p) {  // a piece of all of M's rows is one of each half
       if (p.nblocks == 0 || p.splits * p.halves == 1) return TileJoin{};
-      return TileJoin{(int64_t)(p.m.rows / p.halves) * ceil_div(p.n.rows, 8), p.part, p.n.rows, p.splits * p.halves, p.which};
+      return TileJoin{(int64_t)(p.m.rows / p.halves) * ceil_div(p.n.rows, 8), p.part, p.n.rows, p.splits * p.halves, p.which, p.halves};
     };
     const TileJoin ja = join(a), jb = join(b);
     if (ja.pieces + jb.pieces > 0)
