@@ -18,7 +18,7 @@
 //     (1.4-1.5), weights' gradients 593-650 (1.3-1.4)
 //   33 tokens, 3584 -> 7168: gate/up 23 us (4.5 TB/s), down 13.4 (3.8 TB/s) and 4 to join its pieces
 //   1 token, 7168 -> 8192: gate/up 36.7 us (6.4 TB/s), down 21.5 (5.5 TB/s)
-//   77 tokens, 512 -> 1000, backward: 7-8 + 7 + 3.5 + 6 us, of which some 5 a launch are there with
+//   77 tokens, 512 -> 1000, backward: 8.6 + 6.8 + 3.5 + 6 us, of which some 5 a launch are there with
 //     8 x 8 matrices too
 #include "common.h"
 #include "kernels.h"
