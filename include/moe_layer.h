@@ -541,7 +541,7 @@ moe_status moe_quantize_int8(const void* x, int64_t rows, int32_t n, void* q, fl
  * W int8 [n_out][n_in] with w_scale fp32 [n_out].  x_scale not NULL: x int8 [T][n_in], one scale a
  * token; x_scale NULL: x bf16 [T][n_in], quantised as by moe_quantize_int8 on the way in.  The sums
  * are exact (codes from -128 to 127), then two fp32 products and one rounding; the product of sum and
- * x_scale has to stay within fp32's range.  n_in a multiple of 16, at most 65536; any n_out; T up to 2^24.
+ * x_scale has to stay within fp32's range.  n_in a multiple of 16, at most 65536; n_out up to 2^31 - 256; T up to 2^24.
  * Every pointer 16-byte aligned.  out and workspace overlap nothing; workspace of moe_linear_int8_workspace_size bytes (quantize 1
  * for x_scale NULL), needing no clearing; it may be NULL where that is 0. */
 moe_status moe_linear_int8_workspace_size(int64_t num_tokens, int32_t n_in, int32_t n_out, int32_t quantize,

@@ -21,6 +21,7 @@ constexpr int MAX_DIM = 8192;  // columns a GEMV wave holds in registers
 constexpr int MAX_EXPERT_DIM = 7168;  // latent / FFN width whose staged activation rows fit LDS
 constexpr int MAX_SHARED = 8;
 constexpr int MAX_INT8_DIM = 65536;  // codes of -128: sums stay below 2^31
+constexpr int MAX_INT8_OUT = INT32_MAX - 255;  // a tile's last column is still a 32-bit number
 constexpr int MAX_FFN_DIM = 32768;  // dense block: a tile's row offsets stay within 32 bits
 
 // Experts run as grouped GEMMs over 64-row tiles once they hold 8 routed rows on
@@ -1313,7 +1314,7 @@ moe_status moe_block_norms_backward(const void* dout, const void* dnormed, const
 // ---- the 8-bit projection
 static moe_status check_int8(int64_t T, int32_t n_in, int32_t n_out) {
   if (T < 0 || n_in <= 0 || n_out <= 0 || n_in % 16) return MOE_ERR_INVALID_ARG;
-  if (T > (int64_t)1 << 24 || n_in > MAX_INT8_DIM) return MOE_ERR_UNSUPPORTED;
+  if (T > (int64_t)1 << 24 || n_in > MAX_INT8_DIM || n_out > MAX_INT8_OUT) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

@@ -32,3 +32,22 @@ def test_gated_ffn(T, d, F):
     dout = plain.bf16((T, d), 0.01, T + 1).cuda()
     got = moe.gated_ffn_backward(dout, x, wg, wu, wd, gate, up)
     check(got._asdict(), plain_ffn.backward(dout, x, wg, wu, wd, gate, up), (T, d, F))
+
+
+def test_widest_linear_int8():
+    """The most columns that the call takes: 34 GB of codes."""
+    n = 2 ** 31 - 256
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB of device memory")
+    W, ws = torch.zeros((n, 16), dtype=torch.int8, device="cuda"), torch.ones(n, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rand = lambda *shape: torch.randint(-127, 128, shape, dtype=torch.int8, device="cuda", generator=g)
+    q, xs = rand(2, 16), torch.tensor([0.5, 2.0], device="cuda")
+    for part in (slice(0, 300), slice(2 ** 30 - 300, 2 ** 30 + 300), slice(n - 600, n)):
+        W[part] = rand(part.stop - part.start, 16)
+    out = moe.linear_int8(q, W, ws, x_scale=xs)
+    for part in (slice(0, 600), slice(2 ** 30 - 600, 2 ** 30 + 600), slice(n - 1200, n)):
+        v = product(q, xs, W[part], ws[part])
+        assert ((out[:, part].double() - v).abs() <= v.abs() * 2.0 ** -8).all()
+    del W, ws, out
+    torch.cuda.empty_cache()
